@@ -25,10 +25,15 @@ __all__ = [
     "fp8_cast_amax", "fp8_cast_transpose", "fp8_dbias_workspace_bytes", "fp8_dbias_cast_transpose",
     "fp8_dbias_cast_transpose_noalloc", "fp8_scale_update", "fp8_gemm_bias", "fp8_gemm_bias_chunked", "fp8_gemm_bias_fp8", "fp8_transpose",
     "fp8_linear_fwd", "fp8_linear_bwd", "prepare", "Prepared",
+    "NORM_RMS", "NORM_LAYER", "fp8_norm_residual_fwd", "fp8_norm_residual_workspace_bytes", "fp8_norm_residual_bwd",
+    "fp8_moe_capacity", "fp8_moe_workspace_bytes", "fp8_moe_plan", "fp8_moe_sort_cast", "fp8_moe_sort_codes",
+    "fp8_moe_sort_bf16", "fp8_moe_combine", "fp8_moe_weight_grad", "fp8_grouped_gemm", "fp8_grouped_wgrad",
 ]
 
 E4M3 = 0
 E5M2 = 1
+NORM_RMS = 0
+NORM_LAYER = 1
 OUT_BF16 = 0
 OUT_FP32 = 1
 
@@ -48,6 +53,7 @@ _lib = None
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int32
+F32 = ctypes.c_float
 INT = ctypes.c_int
 SZ = ctypes.c_size_t
 
@@ -66,6 +72,20 @@ _SIGS = {
     "fp8_transpose": ([P, I64, I64, P, P, P], INT),
     "fp8_linear_fwd": ([P, P, P, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, P, P], INT),
     "fp8_linear_bwd": ([P, I64, I64, I64, P, P, P, P, P, P, P, SZ, P, P, P, P, P, P, INT, P], INT),
+    "fp8_norm_residual_fwd": ([P, P, P, P, I64, P, F32, P, P, P, P, P, P, P, P, INT, P, P, INT, F32, I64, I64, P], INT),
+    "fp8_norm_residual_workspace_bytes": ([I64, I64, I64], SZ),
+    "fp8_norm_residual_bwd": ([P, P, P, P, P, P, I64, F32, P, P, P, P, P, P, P, P, P, P, P, P, SZ, INT, I64, I64, P],
+                              INT),
+    "fp8_moe_capacity": ([I64, I64, I64, I64], I64),
+    "fp8_moe_workspace_bytes": ([I64, I64, I64], SZ),
+    "fp8_moe_plan": ([P, I64, I64, I64, I64, I64, P, P, P, P, SZ, P], INT),
+    "fp8_moe_sort_cast": ([P, I64, P, I64, I64, P, P, INT, P, P, P, P, I64, P], INT),
+    "fp8_moe_sort_codes": ([P, I64, P, I64, I64, P, P, I64, P], INT),
+    "fp8_moe_sort_bf16": ([P, I64, P, I64, I64, P, P, I64, P], INT),
+    "fp8_moe_combine": ([P, I64, P, P, I64, I64, P, I64, P], INT),
+    "fp8_moe_weight_grad": ([P, P, I64, P, I64, I64, P, I64, P], INT),
+    "fp8_grouped_gemm": ([P, INT, P, I64, P, INT, P, I64, I64, P, I64, P, I64, INT, I64, I64, I64, P], INT),
+    "fp8_grouped_wgrad": ([P, INT, P, I64, P, INT, P, I64, P, I64, P, INT, I64, I64, I64, P], INT),
 }
 
 
@@ -172,6 +192,7 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
+_I32 = (torch.int32,)
 
 
 def _want(t, dtypes, name, contiguous=True, shape=None, min_numel=None, required=False):
@@ -406,3 +427,200 @@ def fp8_linear_bwd(dy, K, dy_scale, dy_amax, dy8, dy8_t, dy_scale_inv, dbias, wo
                                 _ptr(dy_scale_inv), _ptr(dbias), _ptr(workspace), ws_bytes, _ptr(x8_t),
                                 _ptr(x_scale_inv), _ptr(w8_t), _ptr(w_scale_inv), _ptr(dx), _ptr(dw),
                                 _out_dtype(dw), _stream(stream))
+
+
+# ------------------------------------------------------- the operators around the linear layer
+
+def _norm_shapes(M, H, w_post, b_post, gate, w_pre):
+    _want(w_post, _BF16, "w_post", shape=(H,))
+    _want(b_post, _BF16, "b_post", shape=(H,))
+    _want(w_pre, _BF16, "w_pre", shape=(H,))
+    if gate is None:
+        return 0
+    _want(gate, _BF16, "gate")
+    if gate.dim() != 2 or gate.shape[1] != H or gate.shape[0] < 1 or M % gate.shape[0] != 0:
+        raise ValueError(f"gate must be [G, {H}] with G dividing the {M} rows, got {tuple(gate.shape)}")
+    return gate.shape[0]
+
+
+def _stats_numel(kind, M):
+    return 2 * M if int(kind) == NORM_LAYER else M
+
+
+def fp8_norm_residual_fwd(block_out, w_post, b_post, gate, resid, alpha, x, post_stats, w_pre, b_pre, pre_stats, h,
+                          h8=None, scale=None, fmt=E4M3, scale_inv_out=None, amax_slot=None, kind=NORM_RMS, eps=1e-5,
+                          stream=None):
+    """x = alpha * resid + gate * (norm(block_out) * w_post + b_post), h = norm(x) * w_pre + b_pre as bfloat16
+    ``h`` and / or FP8 codes ``h8`` (see include/fp8ds.h for what may be None).
+
+    ``post_stats`` / ``pre_stats``: float32, rows values (RMS) or 2 * rows (layer: 1 / deviation, then mean)."""
+    ref, name = (resid, "resid") if block_out is None else (block_out, "block_out")
+    _want(ref, _BF16, name, required=True)
+    M, H = ref.shape
+    _want(resid, _BF16, "resid", shape=(M, H))
+    _want(x, _BF16, "x", shape=(M, H), required=block_out is not None)
+    G = _norm_shapes(M, H, w_post, b_post, gate, w_pre)
+    _want(b_pre, _BF16, "b_pre", shape=(H,))
+    _want(post_stats, _F32, "post_stats", min_numel=_stats_numel(kind, M))
+    _want(pre_stats, _F32, "pre_stats", min_numel=_stats_numel(kind, M))
+    _want(h, _BF16, "h", shape=(M, H))
+    _want(h8, _U8, "h8", shape=(M, H))
+    _scalars(scale=scale, scale_inv_out=scale_inv_out, amax_slot=amax_slot)
+    _invoke("fp8_norm_residual_fwd", _ptr(block_out), _ptr(w_post), _ptr(b_post), _ptr(gate), G, _ptr(resid),
+            float(alpha), _ptr(x), _ptr(post_stats), _ptr(w_pre), _ptr(b_pre), _ptr(pre_stats), _ptr(h), _ptr(h8),
+            _ptr(scale), int(fmt), _ptr(scale_inv_out), _ptr(amax_slot), int(kind), float(eps), M, H, _stream(stream))
+
+
+def fp8_norm_residual_workspace_bytes(rows: int, width: int, n_gates: int) -> int:
+    return int(lib().fp8_norm_residual_workspace_bytes(int(rows), int(width), int(n_gates)))
+
+
+def fp8_norm_residual_bwd(dh, dx, block_out, w_post, b_post, gate, alpha, x, post_stats, w_pre, pre_stats, d_block,
+                          d_resid, dw_post, db_post, dgate, dw_pre, db_pre, workspace, kind=NORM_RMS, stream=None):
+    """Gradients of fp8_norm_residual_fwd: ``dh`` of h, ``dx`` of x (either may be None), from the x and the
+    statistics that the forward wrote.  ``workspace``: ``fp8_norm_residual_workspace_bytes(rows, width, gates)``."""
+    ref = dh if dh is not None else dx
+    _want(ref, _BF16, "dh" if dh is not None else "dx", required=True)
+    M, H = ref.shape
+    for t, nm in ((dx, "dx"), (block_out, "block_out"), (x, "x"), (d_block, "d_block"), (d_resid, "d_resid")):
+        _want(t, _BF16, nm, shape=(M, H))
+    G = _norm_shapes(M, H, w_post, b_post, gate, w_pre)
+    _want(post_stats, _F32, "post_stats", min_numel=_stats_numel(kind, M))
+    _want(pre_stats, _F32, "pre_stats", min_numel=_stats_numel(kind, M))
+    for t, nm in ((dw_post, "dw_post"), (db_post, "db_post"), (dw_pre, "dw_pre"), (db_pre, "db_pre")):
+        _want(t, _F32, nm, shape=(H,))
+    _want(dgate, _F32, "dgate", shape=(max(G, 1), H))
+    ws_bytes = _workspace_bytes(workspace)
+    _invoke("fp8_norm_residual_bwd", _ptr(dh), _ptr(dx), _ptr(block_out), _ptr(w_post), _ptr(b_post), _ptr(gate), G,
+            float(alpha), _ptr(x), _ptr(post_stats), _ptr(w_pre), _ptr(pre_stats), _ptr(d_block), _ptr(d_resid),
+            _ptr(dw_post), _ptr(db_post), _ptr(dgate), _ptr(dw_pre), _ptr(db_pre), _ptr(workspace), ws_bytes,
+            int(kind), M, H, _stream(stream))
+
+
+def fp8_moe_capacity(T: int, top: int, E: int, align: int = 16) -> int:
+    """Rows of the sorted buffers that hold any routing of T tokens to ``top`` of E experts each."""
+    n = int(lib().fp8_moe_capacity(int(T), int(top), int(E), int(align)))
+    if n < 0:
+        raise ValueError(f"no plan for T={T}, top={top}, E={E}, align={align} (1 <= E <= 1024, align a multiple of 16 "
+                         "up to 1024)")
+    return n
+
+
+def fp8_moe_workspace_bytes(T: int, top: int, E: int) -> int:
+    return int(lib().fp8_moe_workspace_bytes(int(T), int(top), int(E)))
+
+
+def fp8_moe_plan(experts, E: int, align: int, offsets, src, slot, workspace=None, stream=None):
+    """Sort the choices ``experts`` [T, top] (int32; outside [0, E): dropped) by expert: ``offsets`` [E + 1],
+    ``src`` [capacity], ``slot`` [T, top] (see include/fp8ds.h)."""
+    _want(experts, _I32, "experts", required=True)
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, top]")
+    T, k = experts.shape
+    _want(offsets, _I32, "offsets", shape=(int(E) + 1,), required=True)
+    _want(src, _I32, "src", required=True)
+    _want(slot, _I32, "slot", shape=(T, k), required=True)
+    ws_bytes = _workspace_bytes(workspace)
+    _invoke("fp8_moe_plan", _ptr(experts), T, k, int(E), int(align), src.numel(), _ptr(offsets), _ptr(src), _ptr(slot),
+            _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def _sort_shapes(x, dtypes, src, top, weights, out, out_dtypes, out_t):
+    _want(x, dtypes, "x", required=True)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, width]")
+    T, H = x.shape
+    _want(src, _I32, "src", required=True)
+    cap = src.numel()
+    _want(weights, _F32, "weights", shape=(T, int(top)))
+    _want(out, out_dtypes, "out", shape=(cap, H), required=True)
+    _want(out_t, _U8, "out_t", shape=(H, cap))
+    return T, H, cap
+
+
+def fp8_moe_sort_cast(x, src, top: int, weights, scale, fmt, out, out_t=None, scale_inv_out=None, amax_slot=None,
+                      stream=None):
+    """Rows of bfloat16 ``x`` in expert order, times ``weights`` (or None), as FP8 codes and their transpose."""
+    T, H, cap = _sort_shapes(x, _BF16, src, top, weights, out, _U8, out_t)
+    _scalars(scale=scale, scale_inv_out=scale_inv_out, amax_slot=amax_slot)
+    _invoke("fp8_moe_sort_cast", _ptr(x), T, _ptr(src), cap, int(top), _ptr(weights), _ptr(scale), int(fmt), _ptr(out),
+            _ptr(out_t), _ptr(scale_inv_out), _ptr(amax_slot), H, _stream(stream))
+
+
+def fp8_moe_sort_codes(x8, src, top: int, out, out_t=None, stream=None):
+    """Rows of FP8 codes in expert order, and their transpose (codes copied; padding rows are zero)."""
+    T, H, cap = _sort_shapes(x8, _U8, src, top, None, out, _U8, out_t)
+    _invoke("fp8_moe_sort_codes", _ptr(x8), T, _ptr(src), cap, int(top), _ptr(out), _ptr(out_t), H, _stream(stream))
+
+
+def fp8_moe_sort_bf16(x, src, top: int, weights, out, stream=None):
+    """Rows of bfloat16 ``x`` in expert order, times ``weights`` (or None)."""
+    T, H, cap = _sort_shapes(x, _BF16, src, top, weights, out, _BF16, None)
+    _invoke("fp8_moe_sort_bf16", _ptr(x), T, _ptr(src), cap, int(top), _ptr(weights), _ptr(out), H, _stream(stream))
+
+
+def _back_shapes(ys, slot):
+    _want(ys, _BF16, "ys", required=True)
+    _want(slot, _I32, "slot", required=True)
+    if ys.dim() != 2 or slot.dim() != 2:
+        raise ValueError("ys must be [capacity, width] and slot [T, top]")
+    return (*ys.shape, *slot.shape)
+
+
+def fp8_moe_combine(ys, slot, weights, y, stream=None):
+    """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights None: 1)."""
+    cap, H, T, k = _back_shapes(ys, slot)
+    _want(weights, _F32, "weights", shape=(T, k))
+    _want(y, _BF16, "y", shape=(T, H), required=True)
+    _invoke("fp8_moe_combine", _ptr(ys), cap, _ptr(slot), _ptr(weights), T, k, _ptr(y), H, _stream(stream))
+
+
+def fp8_moe_weight_grad(dy, ys, slot, dweights, stream=None):
+    """dweights[t, j] = <dy[t], ys[slot[t, j]]>, 0 for a dropped choice."""
+    cap, H, T, k = _back_shapes(ys, slot)
+    _want(dy, _BF16, "dy", shape=(T, H), required=True)
+    _want(dweights, _F32, "dweights", shape=(T, k), required=True)
+    _invoke("fp8_moe_weight_grad", _ptr(dy), _ptr(ys), cap, _ptr(slot), T, k, _ptr(dweights), H, _stream(stream))
+
+
+def _rows_dense(**kw):
+    for name, t in kw.items():
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name} rows must be contiguous")
+
+
+def fp8_grouped_gemm(A, fa, a_scale_inv, B, fb, b_scale_inv, offsets, D, stream=None):
+    """D[r] = A[r] B[e]^T * a_scale_inv * b_scale_inv for the rows r in [offsets[e], offsets[e + 1]):
+    A [cap, K] and B [E, N, K] FP8 codes (B may be a strided view), D [cap, N] bfloat16 or float32."""
+    _want(A, _U8, "A", contiguous=False, required=True)
+    _want(B, _U8, "B", contiguous=False, required=True)
+    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
+        raise ValueError("A [cap, K] and B [E, N, K] must share K")
+    cap, K = A.shape
+    E, N = B.shape[:2]
+    _want(offsets, _I32, "offsets", shape=(E + 1,), required=True)
+    if tuple(D.shape) != (cap, N):
+        raise ValueError(f"D must be [{cap}, {N}]")
+    _rows_dense(A=A, B=B, D=D)
+    dtype = _out_dtype(D)
+    _scalars(a_scale_inv=a_scale_inv, b_scale_inv=b_scale_inv)
+    _invoke("fp8_grouped_gemm", _ptr(A), int(fa), _ptr(a_scale_inv), A.stride(0), _ptr(B), int(fb), _ptr(b_scale_inv),
+            B.stride(1), B.stride(0), _ptr(offsets), E, _ptr(D), D.stride(0), dtype, cap, N, K, _stream(stream))
+
+
+def fp8_grouped_wgrad(At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, stream=None):
+    """dW[e] = At[:, rows of e] Bt[:, rows of e]^T * a_scale_inv * b_scale_inv: At [N, cap] and Bt [K, cap] FP8
+    codes (the transposes of the sorted rows), dW [E, N, K] bfloat16 or float32."""
+    _want(At, _U8, "At", contiguous=False, required=True)
+    _want(Bt, _U8, "Bt", contiguous=False, required=True)
+    if At.dim() != 2 or Bt.dim() != 2 or At.shape[1] != Bt.shape[1]:
+        raise ValueError("At [N, cap] and Bt [K, cap] must share the sorted rows")
+    N, cap = At.shape
+    K = Bt.shape[0]
+    _want(offsets, _I32, "offsets", required=True)
+    E = offsets.numel() - 1
+    _want(dW, (torch.bfloat16, torch.float32), "dW", shape=(E, N, K), required=True)
+    _rows_dense(At=At, Bt=Bt)
+    _scalars(a_scale_inv=a_scale_inv, b_scale_inv=b_scale_inv)
+    _invoke("fp8_grouped_wgrad", _ptr(At), int(fa), _ptr(a_scale_inv), At.stride(0), _ptr(Bt), int(fb),
+            _ptr(b_scale_inv), Bt.stride(0), _ptr(offsets), E, _ptr(dW), _out_dtype(dW), cap, N, K, _stream(stream))

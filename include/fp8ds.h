@@ -49,6 +49,11 @@ typedef enum {
 } fp8ds_out_dtype;
 
 typedef enum {
+    FP8DS_NORM_RMS = 0,  /* v * rstd, rstd = 1 / sqrt(mean(v^2) + eps)                        */
+    FP8DS_NORM_LAYER = 1 /* (v - mean) * rstd, rstd = 1 / sqrt(mean((v - mean)^2) + eps)      */
+} fp8ds_norm;
+
+typedef enum {
     FP8DS_OK = 0,
     FP8DS_ERR_NULL = -1,      /* a required pointer is NULL                        */
     FP8DS_ERR_SHAPE = -2,     /* a size is negative or violates a stated multiple  */
@@ -304,6 +309,143 @@ int fp8_linear_bwd(const uint16_t *dy, int64_t M, int64_t N, int64_t K,
                    const uint8_t *x8_t, const float *x_scale_inv,
                    const uint8_t *w8_t, const float *w_scale_inv,
                    uint16_t *dx, void *dw, int dw_dtype, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * The operators around the linear layer: what a transformer block of experts trained in FP8 runs
+ * between its linear layers.
+ * ---------------------------------------------------------------------------------------------
+ *
+ * fp8_norm_residual_fwd -- the norms before and after a block, fused with the block's gate and the
+ * residual scale; the next linear layer's input leaves as bfloat16, as FP8 codes, or both.
+ *
+ *   n = norm(block_out) * w_post + b_post          (w_post NULL: n = block_out)
+ *   x = bfloat16(alpha * resid + gate * n)         (gate NULL: 1; resid NULL: 0)
+ *   h = norm(x) * w_pre + b_pre                    (of the rounded x; w_pre NULL: not formed)
+ *   h8 = saturating round-to-nearest-even code (fmt) of h * (*scale); amax_slot, scale_inv_out as
+ *        fp8_cast_amax, with the amax of h in float32 before the scale
+ *
+ * block_out, resid, x, h: [rows, width] bfloat16.  w_*, b_*: [width] bfloat16; b_* for layer norms
+ * only.  gate: [n_gates, width] bfloat16, gate g for rows [g, g + 1) * rows / n_gates (1: one gate
+ * per channel; one per sample; one per row), n_gates == 0 iff gate is NULL, rows % n_gates == 0.
+ * block_out NULL: h is formed from resid itself (the first norm of a model): then w_post, gate and
+ * x must be NULL and alpha is not applied.  post_stats, pre_stats: NULL, or rstd [rows] float32,
+ * followed for layer norms by the means [rows]: what the backward reads.  x may be resid's buffer.
+ * Sums and statistics are float32; a layer norm's variance is summed about the mean.  kind is an
+ * fp8ds_norm; eps >= 0; width <= 16384.  rows or width == 0 launches nothing.
+ */
+int fp8_norm_residual_fwd(const uint16_t *block_out, const uint16_t *w_post, const uint16_t *b_post,
+                          const uint16_t *gate, int64_t n_gates, const uint16_t *resid, float alpha,
+                          uint16_t *x, float *post_stats, const uint16_t *w_pre, const uint16_t *b_pre,
+                          float *pre_stats, uint16_t *h, uint8_t *h8, const float *scale, int fmt,
+                          float *scale_inv_out, float *amax_slot, int kind, float eps, int64_t rows,
+                          int64_t width, hipStream_t stream);
+
+/* HOST-only: workspace bytes of fp8_norm_residual_bwd (partial column sums; no initialisation). */
+size_t fp8_norm_residual_workspace_bytes(int64_t rows, int64_t width, int64_t n_gates);
+
+/*
+ * fp8_norm_residual_bwd -- gradients of fp8_norm_residual_fwd.
+ *
+ *   d       = dx + (gradient of norm(x) * w_pre + b_pre through dh)     dh or dx may be NULL: 0
+ *   d_resid = alpha * d;  dgate = sum over the gate's rows of d * n;  dn = gate * d
+ *   d_block = gradient of norm(block_out) * w_post + b_post through dn
+ *   dw_pre, db_pre, dw_post, db_post: column sums of dh * hat(x), dh, dn * hat(block_out), dn
+ *
+ * x, post_stats, pre_stats: what the forward wrote (with block_out NULL there, pass its resid as x
+ * and block_out NULL here: d_resid = d).  d_block, d_resid: bfloat16 [rows, width] (d_resid may be
+ * NULL when block_out is given); dw_*, db_*: float32 [width], dgate: float32 [n_gates, width], each
+ * may be NULL.  16-byte aligned, the float32 outputs too.  The column sums are float32 in a fixed
+ * order: the same run to run.  workspace: 16-byte aligned, calls that overlap in time must not
+ * share it.  rows == 0 writes zero sums.
+ */
+int fp8_norm_residual_bwd(const uint16_t *dh, const uint16_t *dx, const uint16_t *block_out,
+                          const uint16_t *w_post, const uint16_t *b_post, const uint16_t *gate, int64_t n_gates,
+                          float alpha, const uint16_t *x, const float *post_stats, const uint16_t *w_pre,
+                          const float *pre_stats, uint16_t *d_block, uint16_t *d_resid, float *dw_post,
+                          float *db_post, float *dgate, float *dw_pre, float *db_pre, void *workspace,
+                          size_t workspace_bytes, int kind, int64_t rows, int64_t width, hipStream_t stream);
+
+/*
+ * fp8_moe_plan -- where every token's choices of experts go when they are sorted by expert.
+ *
+ * experts: [T, top] int32; a value outside [0, E) is a dropped choice that goes nowhere.  The sort
+ * is stable, and every expert's rows are padded to a multiple of `align`:
+ *   offsets [E + 1]  first sorted row of each expert, then the end of the last
+ *   src [cap]        the choice (t * top + j) a sorted row holds, -1 for padding and past the end
+ *   slot [T, top]    the sorted row of a choice, -1 for a dropped one
+ * cap: rows of the sorted buffers, a multiple of 16, at least fp8_moe_capacity(T, top, E, align)
+ * (HOST-only: the most rows any routing needs; -1 for sizes outside the limits).  workspace: at
+ * least fp8_moe_workspace_bytes(T, top, E) bytes, no initialisation (0 bytes for small T: may be
+ * NULL).  Limits: 1 <= E <= 1024, align a multiple of 16 up to 1024, T * top and cap in 31 bits.
+ */
+int64_t fp8_moe_capacity(int64_t T, int64_t top, int64_t E, int64_t align);
+size_t fp8_moe_workspace_bytes(int64_t T, int64_t top, int64_t E);
+int fp8_moe_plan(const int32_t *experts, int64_t T, int64_t top, int64_t E, int64_t align, int64_t cap,
+                 int32_t *offsets, int32_t *src, int32_t *slot, void *workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+
+/*
+ * fp8_moe_sort_cast, fp8_moe_sort_codes, fp8_moe_sort_bf16 -- token rows in expert order.
+ *
+ *   v[row] = x[src[row] / top] * weights[src[row]]     (weights NULL: 1; src -1: a row of zeros)
+ *   cast:  out = code (fmt) of v * (*scale), one float32 product each; amax and scale_inv as fp8_cast_amax with
+ *          the amax of v;  codes: the FP8 codes of x8 themselves;  bf16: v rounded to bfloat16
+ *   out_t[c, row] = out[row, c]        (NULL: not written) the weight gradient's operand
+ *
+ * x: [T, width], out: [cap, width], out_t: [width, cap]; weights: [T, top] float32.  width and cap
+ * are multiples of 16.  A src outside [0, T * top) counts as -1.  With weights and dy in x this is
+ * the gradient of fp8_moe_combine in expert order.
+ */
+int fp8_moe_sort_cast(const uint16_t *x, int64_t T, const int32_t *src, int64_t cap, int64_t top,
+                      const float *weights, const float *scale, int fmt, uint8_t *out, uint8_t *out_t,
+                      float *scale_inv_out, float *amax_slot, int64_t width, hipStream_t stream);
+int fp8_moe_sort_codes(const uint8_t *x8, int64_t T, const int32_t *src, int64_t cap, int64_t top, uint8_t *out,
+                       uint8_t *out_t, int64_t width, hipStream_t stream);
+int fp8_moe_sort_bf16(const uint16_t *x, int64_t T, const int32_t *src, int64_t cap, int64_t top,
+                      const float *weights, uint16_t *out, int64_t width, hipStream_t stream);
+
+/*
+ * fp8_moe_combine -- the experts' rows back in token order:
+ *   y[t] = sum over j of weights[t, j] * ys[slot[t, j]]    (float32, j ascending, bfloat16 y)
+ * weights NULL: 1 (the gradient of the sorts).  A slot outside [0, cap) contributes nothing,
+ * whatever its weight holds; a token without any gives zeros.  ys: [cap, width], y: [T, width].
+ *
+ * fp8_moe_weight_grad -- dweights[t, j] = sum over columns of dy[t] * ys[slot[t, j]] (float32), 0
+ * for a slot outside [0, cap).  width % 16 == 0 in both.
+ */
+int fp8_moe_combine(const uint16_t *ys, int64_t cap, const int32_t *slot, const float *weights, int64_t T,
+                    int64_t top, uint16_t *y, int64_t width, hipStream_t stream);
+int fp8_moe_weight_grad(const uint16_t *dy, const uint16_t *ys, int64_t cap, const int32_t *slot, int64_t T,
+                        int64_t top, float *dweights, int64_t width, hipStream_t stream);
+
+/*
+ * fp8_grouped_gemm -- the experts' FP8 products over sorted rows: for every expert e and row r in
+ * [offsets[e], offsets[e + 1])
+ *
+ *   D[r, n] = (sum_k A[r, k] * B[e][n, k]) * (*a_scale_inv) * (*b_scale_inv)
+ *
+ * A: [cap, K] codes, row stride lda.  B[e]: [N, K] codes at B + e * stride_b, row stride ldb (a
+ * stack [E, N, K], or the cast's transpose [N, E * K] of a stack [E * K, N]: ldb = E * K, stride_b
+ * = K), one scale for the whole stack.  D: [cap, N] bfloat16 or float32, row stride ldd; rows
+ * outside every expert's are not written.  offsets: [E + 1] int32 on the device, multiples of 16
+ * (held to [0, cap] and rounded down to multiples of 16 as they are read).  K % 16 == 0; lda, ldb
+ * % 16 == 0, >= K and below 2^23; stride_b % 16 == 0; A, B 16-byte aligned.  With the output
+ * gradient as A and the weights' transpose as B this is the input gradient.
+ *
+ * fp8_grouped_wgrad -- the experts' weight gradients: dW[e][n, k] = (sum over e's rows r of
+ * At[n, r] * Bt[k, r]) * (*a_scale_inv) * (*b_scale_inv), zeros for an expert without rows.
+ * At: [N, cap], Bt: [K, cap] codes with row strides lda, ldb >= cap (multiples of 16, below 2^23),
+ * cap % 16 == 0.  dW: [E, N, K] bfloat16 or float32, dense.
+ *
+ * Products accumulate in float32 on the matrix cores, in a fixed order.
+ */
+int fp8_grouped_gemm(const uint8_t *A, int fa, const float *a_scale_inv, int64_t lda, const uint8_t *B, int fb,
+                     const float *b_scale_inv, int64_t ldb, int64_t stride_b, const int32_t *offsets, int64_t E,
+                     void *D, int64_t ldd, int out_dtype, int64_t cap, int64_t N, int64_t K, hipStream_t stream);
+int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64_t lda, const uint8_t *Bt, int fb,
+                      const float *b_scale_inv, int64_t ldb, const int32_t *offsets, int64_t E, void *dW,
+                      int out_dtype, int64_t cap, int64_t N, int64_t K, hipStream_t stream);
 
 #ifdef __cplusplus
 }
