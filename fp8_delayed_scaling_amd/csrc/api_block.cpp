@@ -235,7 +235,7 @@ int fp8_grouped_gemm(const uint8_t *A, int fa, const float *a_scale_inv, int64_t
                                K, K);
         st != FP8DS_OK)
         return st;
-    if (ldd < N || !size_ok(cap, ldd) || (K > 0 && !size_ok(E, stride_b))) return FP8DS_ERR_SHAPE;
+    if (ldd < N || ldd >= fp8ds::kGroupedMaxLd || !size_ok(cap, ldd) || (K > 0 && !size_ok(E, stride_b))) return FP8DS_ERR_SHAPE;
     if (K > 0 && stride_b % 16 != 0) return FP8DS_ERR_ALIGN;
     if (!fp8ds::grouped_gemm_fits(cap, E, N)) return FP8DS_ERR_SHAPE;
     if (cap == 0 || N == 0 || E == 0) return FP8DS_OK;
@@ -253,7 +253,7 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
                                K, cap);
         st != FP8DS_OK)
         return st;
-    if (!size_ok(N, K) || !size_ok(E, N * K) || !fp8ds::grouped_wgrad_fits(E, N, K)) return FP8DS_ERR_SHAPE;
+    if (!size_ok(N, K) || K >= fp8ds::kGroupedMaxLd || !size_ok(E, N * K) || !fp8ds::grouped_wgrad_fits(E, N, K)) return FP8DS_ERR_SHAPE;
     if (N == 0 || K == 0 || E == 0) return FP8DS_OK;
     if (offsets == nullptr || dW == nullptr || a_scale_inv == nullptr || b_scale_inv == nullptr) return FP8DS_ERR_NULL;
     if (cap > 0 && (At == nullptr || Bt == nullptr)) return FP8DS_ERR_NULL;

@@ -4,12 +4,20 @@
 //   weight gradient            D[e] = A[:, rows of e] B[:, rows of e]^T * (the same)
 //
 // offsets[e] .. offsets[e + 1] are expert e's rows, read on the device: the host never learns
-// them, so the grid covers the largest number of tiles any routing can give and the blocks past
-// the actual tiles end at once.  Both operands are K-contiguous and accumulate in float32; the one
-// product order per output is fixed, so results do not depend on the routing of other experts.
-// Offsets are held to [0, cap] and to multiples of 16 as they are read, so no content of the
-// buffer makes an access out of bounds.
+// them.  Both operands are K-contiguous and accumulate in float32; the one product order per output
+// is fixed, so results do not depend on the routing of other experts.  Offsets are held to [0, cap]
+// and to multiples of 16 as they are read, so no content of the buffer makes an access out of
+// bounds.
+//
+// One block of four waves (2 x 2, each up to 128 x 128 made of v_mfma_f32_16x16x128_f8f6f4 tiles)
+// runs on each CU and takes tiles of up to 256 rows of A by 256 rows of B, one after the other: the
+// first loads of a tile are in flight while the tile before is written.  An expert's rows are
+// shared evenly among its tiles, in steps of 32 (16 for each row of waves); a tile runs only the
+// 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the tile's extent: rows
+// past it, and the 16-byte pieces of the last K step past K (their offset is moved out of the
+// bound), arrive as zeros without touching memory.
 #include <climits>
+#include <type_traits>
 
 #include "../../include/fp8ds.h"
 #include "device_common.h"
@@ -19,171 +27,448 @@ namespace fp8ds {
 
 namespace {
 
-constexpr int kT = 128;                      // tile rows and columns
+constexpr int kTm = 256, kTn = 256;          // most rows of a tile, its columns (rows of B)
 constexpr int kStep = 128;                   // K bytes per step
 constexpr int kThreads = 256;
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+constexpr int kCUs = 256;                    // blocks of a launch: one per CU
+constexpr int kXcds = 8;                     // blocks are dealt round-robin to the XCDs
+constexpr int kSlot = 256 * kStep;           // one K step of an operand in LDS
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every tile's extent (below 2^31 bytes)
+constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
 
-__device__ __forceinline__ int offset_at(const Grouped &g, int e) {
-    return min(max(g.offsets[e], 0), g.cap) & ~15;
+// vmcnt-only wait, and a workgroup barrier without a fence (a fenced one would wait for every load
+// in flight); the empty asm statements keep memory accesses on their side.
+#define FP8DS_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(0xF70 | ((n) & 0xF) | (((n) >> 4) << 14))
+#define FP8DS_WAIT_VM_LGKM(n) __builtin_amdgcn_s_waitcnt(0x070 | ((n) & 0xF) | (((n) >> 4) << 14))   // and lgkmcnt(0)
+#define FP8DS_WAIT_ALL() __builtin_amdgcn_s_waitcnt(0x0070)     // vmcnt(0) lgkmcnt(0)
+#define FP8DS_BARRIER()                          \
+    do {                                         \
+        asm volatile("" ::: "memory");           \
+        __builtin_amdgcn_s_barrier();            \
+        asm volatile("" ::: "memory");           \
+    } while (0)
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Rows of each of the tiles that share n rows: ceil(n / 256) tiles, the same multiple of 32 each
+// (the last may have fewer, never none).
+__host__ __device__ constexpr int tile_rows(int n) {
+    const int tiles = (n + kTm - 1) / kTm, blocks = (n + 31) / 32;
+    return tiles > 0 ? (blocks + tiles - 1) / tiles * 32 : 0;
 }
 
-// The expert and first row of row tile `tile`, counting every expert's tiles of `tm` rows in
-// order: each wave sums 64 experts' tile counts at a time.  False past the last tile.
-__device__ __forceinline__ bool find_tile(const Grouped &g, int tile, int tm, int &e, int &row, int &end) {
-    const int lane = threadIdx.x & 63;
-    int seen = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-        const int i = e0 + lane;
-        int lo = 0, hi = 0;
-        if (i < g.E) {
-            lo = offset_at(g, i);
-            hi = offset_at(g, i + 1);
-        }
-        const int n = hi > lo ? (hi - lo + tm - 1) / tm : 0;
-        int incl = n;
+// A tile's operands and output, uniform over the block.
+struct Tile {
+    const uint8_t *A, *B;
+    void *D;
+    int rows, cols, K;
+};
+
+// Scalar loads: the offsets are not written while the kernel runs, and a vector load would wait
+// for every store in flight before it.
+__device__ __forceinline__ int offset_at(const Grouped &g, int e) {
+    const auto *o = reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uint64_t>(g.offsets));
+    return min(max(o[uniform(e)], 0), g.cap) & ~15;
+}
+
+// The forward's tiles: expert e has ceil(rows / 256) * tiles_n.  Each XCD takes a contiguous range
+// of them, in which an expert's row tiles run fastest, so that blocks which share B's rows run on
+// one XCD at one time and B comes from HBM once.  A block finds its first tile with the sums of 64
+// experts' tile counts at a time, and walks on from there.
+template <int OUT>
+struct RowTiles {
+    const Grouped &g;
+    int tiles_n, tile, end;          // the block's next tile, the end of its XCD's range
+    int e, before, first, last;      // an expert at or before that tile's, the tiles before it, its rows
+    static __device__ __forceinline__ int count(int lo, int hi) { return hi > lo ? (hi - lo + kTm - 1) / kTm : 0; }
+    __device__ __forceinline__ int counts(int e0) const {
+        const int i = e0 + (threadIdx.x & 63);
+        if (i >= g.E) return 0;
+        return count(min(max(g.offsets[i], 0), g.cap) & ~15, min(max(g.offsets[i + 1], 0), g.cap) & ~15);
+    }
+    static __device__ __forceinline__ int scan(int n) {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(incl, off, 64);
-            if (lane >= off) incl += v;
+            const int v = __shfl_up(n, off, 64);
+            if (lane >= off) n += v;
         }
-        const uint64_t past = __ballot(seen + incl > tile);
-        if (past != 0) {
-            const int l = __builtin_ctzll(past);
-            e = __builtin_amdgcn_readfirstlane(e0 + l);
-            row = __builtin_amdgcn_readfirstlane(__shfl(lo + (tile - seen - (incl - n)) * tm, l, 64));
-            end = __builtin_amdgcn_readfirstlane(__shfl(hi, l, 64));
+        return n;
+    }
+    __device__ __forceinline__ RowTiles(const Grouped &g_, int tiles_n_) : g(g_), tiles_n(tiles_n_) {
+        int total = 0;
+        for (int e0 = 0; e0 < g.E; e0 += 64) total += uniform(__shfl(scan(counts(e0)), 63, 64));
+        total *= tiles_n;
+        const int xcd = blockIdx.x % kXcds, q8 = total / kXcds, r8 = total % kXcds;
+        const int begin = xcd * q8 + min(xcd, r8);
+        end = begin + q8 + (xcd < r8 ? 1 : 0);
+        tile = begin + blockIdx.x / kXcds;
+        e = before = first = last = 0;
+        if (tile >= end) return;
+        int seen = 0;
+        for (int e0 = 0; e0 < g.E; e0 += 64) {
+            const int n = counts(e0), incl = scan(n);
+            const uint64_t past = __ballot((seen + incl) * tiles_n > tile);
+            if (past != 0) {
+                const int l = __builtin_ctzll(past);
+                e = uniform(e0 + l);
+                before = (seen + uniform(__shfl(incl - n, l, 64))) * tiles_n;
+                break;
+            }
+            seen += uniform(__shfl(incl, 63, 64));
+        }
+        first = offset_at(g, e);
+        last = offset_at(g, e + 1);
+    }
+    // the block's next tile; false when there is none
+    __device__ __forceinline__ bool operator()(Tile &t) {
+        if (tile >= end) return false;
+        int row_tiles = count(first, last);
+        while (before + row_tiles * tiles_n <= tile && e + 1 < g.E) {
+            before += row_tiles * tiles_n;
+            ++e;
+            first = last;
+            last = offset_at(g, e + 1);
+            row_tiles = count(first, last);
+        }
+        const int in = tile - before, tn = in / row_tiles, h = tile_rows(last - first), row = first + (in - tn * row_tiles) * h;
+        constexpr int kEsz = OUT == 0 ? 2 : 4;
+        t = Tile{g.A + (int64_t)row * g.lda, g.B + (int64_t)e * g.stride_b + (int64_t)tn * kTn * g.ldb,
+                 static_cast<uint8_t *>(g.D) + ((int64_t)row * g.ldd + tn * kTn) * kEsz, min(h, last - row),
+                 min(kTn, g.N - tn * kTn), g.K};
+        tile += gridDim.x / kXcds;
+        return true;
+    }
+};
+
+// The weight gradient's tiles.  Every XCD takes an eighth of each expert's tiles, whatever the
+// routing: the ranges of B that an XCD reads stay in its L2, A is read by all of them.  Which
+// eighth moves with the expert, and which of the XCD's blocks takes a tile moves from one round of
+// tiles to the next, so that remainders and experts of uneven length spread.
+template <int OUT>
+struct ExpertTiles {
+    const Grouped &g;
+    int tiles_m, tiles_n, h, round;
+    __device__ __forceinline__ ExpertTiles(const Grouped &g_, int tiles_m_, int tiles_n_)
+        : g(g_), tiles_m(tiles_m_), tiles_n(tiles_n_), h(tile_rows(g_.N)), round(0) {}
+    __device__ __forceinline__ bool operator()(Tile &t) {
+        const int per = tiles_m * tiles_n, chunk = (per + kXcds - 1) / kXcds;
+        const int slots = gridDim.x / kXcds, xcd = blockIdx.x % kXcds;
+        for (;; ++round) {
+            const int64_t at = (int64_t)round * slots + (blockIdx.x / kXcds + round * 11) % slots;
+            if (at >= (int64_t)g.E * chunk) {
+                if ((int64_t)round * slots >= (int64_t)g.E * chunk) return false;
+                continue;
+            }
+            const int e = (int)(at / chunk), in = (int)(at - (int64_t)e * chunk) + ((xcd + e) % kXcds) * chunk;
+            if (in >= per) continue;
+            ++round;
+            const int tn = in / tiles_m, tm = in - tn * tiles_m;
+            const int lo = offset_at(g, e), len = max(0, offset_at(g, e + 1) - lo);
+            constexpr int kEsz = OUT == 0 ? 2 : 4;
+            t = Tile{g.A + (int64_t)tm * h * g.lda + lo, g.B + (int64_t)tn * kTn * g.ldb + lo,
+                     static_cast<uint8_t *>(g.D) + ((int64_t)e * g.stride_d + (int64_t)tm * h * g.ldd + tn * kTn) * kEsz,
+                     min(h, g.N - tm * h), min(kTn, g.K - tn * kTn), len};
             return true;
         }
-        seen += __shfl(incl, 63, 64);
     }
-    return false;
+};
+
+// Swizzles: the 16-byte piece c of an operand's row r sits at piece c ^ swz(r) of its 128 bytes, so
+// that the 16 lanes of one phase of a fragment read (lanes 0-3, 12-15, 20-23, 24-27 and so on: two
+// K groups) hit distinct banks.  A's fragments are 16 consecutive rows.  B's rows are taken in the
+// order that the output wants: a lane's accumulators of fragment q hold four consecutive m, and for
+// bfloat16 the fragments 2 p and 2 p + 1 interleave, so that its eight values of both are
+// consecutive columns and one store instruction writes 64 contiguous bytes of 16 rows, as it does
+// for float32 in plain order.
+__device__ __forceinline__ int swz_a(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+template <int OUT> __device__ __forceinline__ int swz_b(int r) {
+    if constexpr (OUT != 0) return swz_a(r);
+    const int h = (r >> 3) & 3;
+    return ((r >> 1) & 1) ^ (((h ^ (h >> 1)) & 1) << 2) ^ (h & 2);
+}
+template <int OUT> __device__ __forceinline__ int col_of(int q, int m) {
+    return OUT == 0 ? (q >> 1) * 32 + (m >> 2) * 8 + (q & 1) * 4 + (m & 3) : q * 16 + m;
 }
 
-// One 128 x 128 tile of A B^T: rows_a / rows_b rows are inside, K a multiple of 16 (the rest of
-// the last step counts as zero codes).  Four waves of 64 x 64.
+constexpr int kEarly = 4;       // loads of a step's A that are issued at the end of the step before
+
+// A block's work on its tiles.  LDS holds two K steps of A and three of B, 160 KB in all.  Step j
+// multiplies A_j, its fragments read one 16-row block ahead of the MFMAs, by B_j, whose fragments
+// were read into registers during step j - 1; it reads the fragments of B_{j+1}, loads A_{j+1} into
+// the slot that A_{j-1} used and then B_{j+3} into B_j's, and before its last block waits for all
+// but the latter: A is read by several tiles at a time and comes from L2, B from HBM.
 template <int FA, int FB, int OUT>
-__device__ __forceinline__ void tile_product(const uint8_t *__restrict__ A, int64_t lda, int rows_a,
-                                             const uint8_t *__restrict__ B, int64_t ldb, int rows_b, int K, float sa,
-                                             float sb, void *__restrict__ D, int64_t ldd) {
-    __shared__ __align__(16) uint8_t lds[2][2][kT * kStep];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
-    const int lrow = tid >> 3, part = tid & 7;    // rows lrow + 32 i, 16-byte piece `part`
-    u32x4 ra[4], rb[4];
-    auto load = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = lrow + 32 * i;
-            ra[i] = rb[i] = u32x4{0u, 0u, 0u, 0u};
-            if (k0 + part * 16 < K) {
-                ra[i] = *reinterpret_cast<const u32x4 *>(A + (int64_t)min(r, rows_a - 1) * lda + k0 + part * 16);
-                rb[i] = *reinterpret_cast<const u32x4 *>(B + (int64_t)min(r, rows_b - 1) * ldb + k0 + part * 16);
-            }
-        }
+struct Worker {
+    uint8_t *sa0, *sa1, *sb0, *sb1, *sb2;
+    int64_t ldd;
+    float sa, sb;
+    int lda, ldb, wave, wm, wn;
+
+    __device__ __forceinline__ Worker(const Grouped &gr, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1, uint8_t *b2)
+        : sa0(a0), sa1(a1), sb0(b0), sb1(b1), sb2(b2), ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb) {
+        wave = uniform((int)threadIdx.x >> 6);
+        wm = wave >> 1; wn = wave & 1;
+    }
+    // The lane, as a value the compiler cannot see through: what depends on it is formed anew for
+    // each tile, not kept in registers (or worse, in memory) from one to the next.
+    static __device__ __forceinline__ int fresh_lane() {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        return lane;
+    }
+    // Load i of a slot: wave w fills its 1 KB block 4 i + w, rows 32 i + 8 w .. + 7; lane l row l / 8,
+    // stored piece l % 8.
+    struct Loads {
+        int ka, kb;              // K byte of the lane's A and B pieces inside a step
+        uint32_t va, vb;         // the lane's offset in a slot's first load
     };
-    auto stash = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = lrow + 32 * i;
-            *reinterpret_cast<u32x4 *>(&lds[buf][0][r * kStep + ((part ^ swz(r)) << 4)]) = ra[i];
-            *reinterpret_cast<u32x4 *>(&lds[buf][1][r * kStep + ((part ^ swz(r)) << 4)]) = rb[i];
-        }
-    };
-    const int r16 = lane & 15, g = lane >> 4;
-    auto frag = [&](const uint8_t *p, int r) -> i32x8 {
-        const u32x4 lo = *reinterpret_cast<const u32x4 *>(p + r * kStep + (((2 * g) ^ swz(r)) << 4));
-        const u32x4 hi = *reinterpret_cast<const u32x4 *>(p + r * kStep + (((2 * g + 1) ^ swz(r)) << 4));
+    __device__ __forceinline__ Loads loads_of(int lane) const {
+        const int row = wave * 8 + (lane >> 3), ka = ((lane & 7) ^ swz_a(row)) * 16, kb = ((lane & 7) ^ swz_b<OUT>(row)) * 16;
+        return Loads{ka, kb, (uint32_t)(row * lda + ka), (uint32_t)(row * ldb + kb)};
+    }
+    // Tiles' extents are below 2^31 bytes.  The descriptor has to be in scalar registers.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const uint8_t *p, int64_t bytes) {
+        const uint64_t a = reinterpret_cast<uint64_t>(p);
+        const uint64_t u = (uint64_t)(uint32_t)uniform((int)a) | (uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32;
+        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, uniform((int)bytes), kBufDesc3);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t *slot, int i, uint32_t off, int j) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(slot + (i * 4 + wave) * 1024), 16, off,
+                                                 (uint32_t)uniform(j * kStep), 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t outside(const Tile &t, int j, int piece) {
+        return j * kStep + piece < t.K ? 0u : kOutside;
+    }
+    static __device__ __forceinline__ i32x8 frag(const uint8_t *p, int o0, int o1) {
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(p + o0);
+        const u32x4 hi = *reinterpret_cast<const u32x4 *>(p + o1);
         i32x8 v;
         v[0] = (int)lo.x; v[1] = (int)lo.y; v[2] = (int)lo.z; v[3] = (int)lo.w;
         v[4] = (int)hi.x; v[5] = (int)hi.y; v[6] = (int)hi.z; v[7] = (int)hi.w;
         return v;
-    };
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int nk = (K + kStep - 1) / kStep;
-    if (nk > 0) {
-        load(0);
-        stash(0);
     }
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        if (kt + 1 < nk) load((kt + 1) * kStep);
-        const uint8_t *as = lds[kt & 1][0], *bs = lds[kt & 1][1];
-        i32x8 fa[4], fb[4];
+
+    // The steps' slots and registers repeat with period 6; a tile starts at the phase that lets its
+    // last step be the sixth.
+    static __device__ __forceinline__ int steps(const Tile &t) { return max(1, (t.K + kStep - 1) / kStep); }   // K = 0: one of zeros
+    static __device__ __forceinline__ int phase(int nk) { return (6 - nk % 6) % 6; }
+    static __device__ __forceinline__ uint8_t *pick(bool c, uint8_t *x, uint8_t *y) { return c ? x : y; }
+    __device__ __forceinline__ uint8_t *slot_a(int p) const { return pick(p & 1, sa1, sa0); }
+    __device__ __forceinline__ uint8_t *slot_b(int p) const { return pick(p % 3 == 0, sb0, pick(p % 3 == 1, sb1, sb2)); }
+
+    // A tile's first loads: A_0 and B_0, then B_1 and B_2.
+    __device__ __forceinline__ void first_loads(const Tile &t) const {
+        const int p = phase(steps(t));
+        const Loads ld = loads_of(fresh_lane());
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+        {
+            uint8_t *a = slot_a(p);
+            const uint32_t oa = outside(t, 0, ld.ka);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fa[i] = frag(as, wm * 64 + i * 16 + r16);
-            fb[i] = frag(bs, wn * 64 + i * 16 + r16);
+            for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | oa) + i * 32 * lda, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 3; ++j) {
+            uint8_t *b = slot_b(p + j);
+            const uint32_t ob = outside(t, j, ld.kb);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i], acc[i][j], FB, FA, 0, 0, 0, 0);
-        if (kt + 1 < nk) stash((kt + 1) & 1);
-        __syncthreads();
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | ob) + i * 32 * ldb, j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
-    // lane l holds D[16 i + l % 16][16 j + 4 (l / 16) + u] in element u of acc[i][j]
-    constexpr int kEsz = OUT == 0 ? 2 : 4;
-    const bool vec4 = ((reinterpret_cast<uintptr_t>(D) & (uintptr_t)(4 * kEsz - 1)) == 0) && (ldd % 4 == 0);
+
+    // Products of a tile of at most 32 NB rows, then the next tile's first loads, then the output.
+    template <int NB>
+    __device__ __forceinline__ void run(const Tile &t, const Tile &next, bool more) const {
+        f32x4 acc[NB][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = wm * 64 + i * 16 + r16;
-        if (row >= rows_a) continue;
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int col = wn * 64 + j * 16 + g * 4;
-            float v[4];
+            for (int q = 0; q < 8; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int nk = steps(t);
+        const int lane = fresh_lane(), r16 = lane & 15, g = lane >> 4;
+        const Loads ld = loads_of(lane);
+        // fragments: 16-row block i of A, B's rows 32 p + col_of(h, r16) for q = 2 p + h, one swizzle for each h;
+        // the second piece of the lane's 32 bytes is the first's neighbour
+        const int oa = (wm * 16 + r16) * kStep + (((2 * g) ^ swz_a(r16)) << 4);
+        const int rb0 = col_of<OUT>(0, r16), rb1 = col_of<OUT>(1, r16);
+        const int ob0 = (wn * 128 + rb0) * kStep + (((2 * g) ^ swz_b<OUT>(rb0)) << 4);
+        const int ob1 = (wn * 128 + rb1) * kStep + (((2 * g) ^ swz_b<OUT>(rb1)) << 4);
+        auto frag_a = [&](const uint8_t *slot, int i) { return frag(slot + i * 32 * kStep, oa, oa ^ 16); };
+        auto frag_b = [&](const uint8_t *slot, int q) {
+            return q & 1 ? frag(slot + (q >> 1) * 32 * kStep, ob1, ob1 ^ 16) : frag(slot + (q >> 1) * 32 * kStep, ob0, ob0 ^ 16);
+        };
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+        i32x8 fb0[8], fb1[8], fa[2];
+        constexpr int kBlocks = NB - 1;
+        auto mfma = [&](int i, const i32x8 &a, const i32x8 (&b)[8]) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = dequant_bias(acc[i][j][u], sa, sb, 0.f);
-            const int64_t o = (int64_t)row * ldd + col;
-            if (vec4 && col + 3 < rows_b) {
-                if constexpr (OUT == 0)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(D) + o) =
-                        u32x2{f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
-                else
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(D) + o) = f32x4{v[0], v[1], v[2], v[3]};
-            } else {
+            for (int q = 0; q < 8; ++q)
+                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[q], a, acc[i][q], FB, FA, 0, 0, 0, 0);
+        };
+        // P: the phase's parity; block i's A fragment is fa[(P NB + i) % 2]
+        auto step = [&](auto pc, int j, uint8_t *a_cur, uint8_t *a_nxt, uint8_t *b_nxt, uint8_t *b_free, const i32x8 (&fbc)[8],
+                        i32x8 (&fbn)[8]) {
+            constexpr int P = decltype(pc)::value, kRest = NB > kEarly ? NB - kEarly : 0;
+            const uint32_t out_a = outside(t, j + 1, ld.ka), out_b = outside(t, j + 3, ld.kb);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (col + u < rows_b) {
-                        if constexpr (OUT == 0) static_cast<uint16_t *>(D)[o + u] = f32_to_bf16_rne(v[u]);
-                        else static_cast<float *>(D)[o + u] = v[u];
-                    }
+            for (int i = 0; i < kBlocks; ++i) {
+                fa[(P * NB + i + 1) & 1] = frag_a(a_cur, i + 1);
+#pragma unroll
+                for (int q = 8 * i / kBlocks; q < 8 * (i + 1) / kBlocks; ++q) fbn[q] = frag_b(b_nxt, q);
+                // the rest of A_{j+1} in the first block, B_{j+3} over all
+                if (i == 0) {
+#pragma unroll
+                    for (int n = kEarly; n < kEarly + kRest; ++n) load(rs_a, a_nxt, n, (ld.va | out_a) + n * 32 * lda, j + 1);
+                }
+                __builtin_amdgcn_sched_barrier(0x7cf);      // loads into LDS stay in this order
+#pragma unroll
+                for (int n = 8 * i / kBlocks; n < 8 * (i + 1) / kBlocks; ++n) load(rs_b, b_free, n, (ld.vb | out_b) + n * 32 * ldb, j + 3);
+                mfma(i, fa[(P * NB + i) & 1], fbc);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            asm volatile("" ::: "memory");
+            FP8DS_WAIT_VM_LGKM(8);
+            FP8DS_BARRIER();
+            __builtin_amdgcn_sched_barrier(0);
+            const i32x8 last = fa[(P * NB + NB - 1) & 1];
+            fa[(P * NB + NB) & 1] = frag_a(a_nxt, 0);
+            const uint32_t oa2 = outside(t, j + 2, ld.ka);
+#pragma unroll
+            for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a_cur, n, (ld.va | oa2) + n * 32 * lda, j + 2);
+            mfma(NB - 1, last, fbc);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const int p = phase(nk);
+        asm volatile("" ::: "memory");
+        FP8DS_WAIT_VM(16);                               // A_0 and B_0
+        FP8DS_BARRIER();
+        {
+            const uint8_t *b = slot_b(p), *a = slot_a(p);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) fb0[q] = fb1[q] = frag_b(b, q);
+            fa[0] = fa[1] = frag_a(a, 0);
         }
+        FP8DS_WAIT_VM_LGKM(16);
+        FP8DS_BARRIER();
+        __builtin_amdgcn_sched_barrier(0);
+        {
+            uint8_t *a = slot_a(p + 1);
+            const uint32_t out_a = outside(t, 1, ld.ka);
+#pragma unroll
+            for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a, n, (ld.va | out_a) + n * 32 * lda, 1);
+        }
+        const std::integral_constant<int, 0> even{};
+        const std::integral_constant<int, 1> odd{};
+        int j = -p;
+        do {
+            if (j >= 0) step(even, j, sa0, sa1, sb1, sb0, fb0, fb1);
+            if (j + 1 >= 0) step(odd, j + 1, sa1, sa0, sb2, sb1, fb1, fb0);
+            if (j + 2 >= 0) step(even, j + 2, sa0, sa1, sb0, sb2, fb0, fb1);
+            if (j + 3 >= 0) step(odd, j + 3, sa1, sa0, sb1, sb0, fb1, fb0);
+            if (j + 4 >= 0) step(even, j + 4, sa0, sa1, sb2, sb1, fb0, fb1);
+            step(odd, j + 5, sa1, sa0, sb0, sb2, fb1, fb0);
+            j += 6;
+        } while (j < nk);
+        FP8DS_WAIT_ALL();                                // every load into the slots has landed
+        FP8DS_BARRIER();
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) first_loads(next);
+        store<NB>(t, acc);
+    }
+
+    // lane l holds row 32 i + 16 wm + l % 16, columns col_of(q, 4 (l / 16) + u), in element u of acc[i][q]
+    template <int NB>
+    __device__ __forceinline__ void store(const Tile &t, const f32x4 (&acc)[NB][8]) const {
+        constexpr int kEsz = OUT == 0 ? 2 : 4, kPer = 16 / kEsz;      // elements of a 16-byte store
+        const bool vec = (reinterpret_cast<uintptr_t>(t.D) & 15) == 0 && ldd % kPer == 0 && t.cols % kPer == 0;
+        const int lane = fresh_lane(), col0 = wn * 128 + col_of<OUT>(0, 4 * (lane >> 4)), row = wm * 16 + (lane & 15);
+        const uint32_t at = (uint32_t)((row * (int)ldd + col0) * kEsz);      // 32 rows are less than 2^30 bytes
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const auto rs = bounded(static_cast<const uint8_t *>(t.D) + (int64_t)(i * 32) * ldd * kEsz, 0x7fffffff);
+            const uint32_t here = i * 32 + row < t.rows ? at : kOutside;
+#pragma unroll
+            for (int p = 0; p < 32 / kPer; ++p) {
+                u32x4 w;
+                if constexpr (OUT == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            w[2 * h + u] = f32x2_to_bf16x2_rne(dequant_bias(acc[i][2 * p + h][2 * u], sa, sb, 0.f),
+                                                               dequant_bias(acc[i][2 * p + h][2 * u + 1], sa, sb, 0.f));
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) w[u] = __float_as_uint(dequant_bias(acc[i][p][u], sa, sb, 0.f));
+                }
+                if (vec) {
+                    const uint32_t o = col0 + p * kPer * 4 < t.cols ? here + (uint32_t)(p * kPer * 4 * kEsz) : kOutside;
+                    __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)o, 0, 0);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) {
+                        const uint32_t o = col0 + p * kPer * 4 + u < t.cols ? here + (uint32_t)((p * kPer * 4 + u) * kEsz) : kOutside;
+                        if constexpr (OUT == 0)
+                            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[u >> 1] >> (16 * (u & 1))), rs, (int)o, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b32(w[u], rs, (int)o, 0, 0);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
+// FINE: a variant for every height from 128 rows on (an expert's rows have any); else two.
+template <int FA, int FB, int OUT, bool FINE, class Tiles>
+__device__ __forceinline__ void run_tiles(const Grouped &g, Tiles &&tiles) {
+    __shared__ __align__(16) uint8_t sa0[kSlot];
+    __shared__ __align__(16) uint8_t sa1[kSlot];
+    __shared__ __align__(16) uint8_t sb0[kSlot];
+    __shared__ __align__(16) uint8_t sb1[kSlot];
+    __shared__ __align__(16) uint8_t sb2[kSlot];
+    Tile t, next;
+    if (!tiles(t)) return;
+    const Worker<FA, FB, OUT> w(g, sa0, sa1, sb0, sb1, sb2);
+    w.first_loads(t);
+    for (bool more = true; more; t = next) {
+        more = tiles(next);
+        const int nb = (t.rows + 31) / 32;
+        if (FINE && nb <= 2) w.template run<2>(t, next, more);
+        else if (nb <= 4) w.template run<4>(t, next, more);
+        else if (FINE && nb == 5) w.template run<5>(t, next, more);
+        else if (FINE && nb == 6) w.template run<6>(t, next, more);
+        else if (FINE && nb == 7) w.template run<7>(t, next, more);
+        else w.template run<8>(t, next, more);
     }
 }
 
 }  // namespace
 
 template <int FA, int FB, int OUT>
-__global__ __launch_bounds__(kThreads) void k_grouped_gemm(const Grouped g, int tiles_n) {
-    const int tile = blockIdx.x / tiles_n, tn = blockIdx.x - tile * tiles_n;
-    int e, row, end;
-    if (!find_tile(g, tile, kT, e, row, end)) return;
-    constexpr int kEsz = OUT == 0 ? 2 : 4;
-    tile_product<FA, FB, OUT>(g.A + (int64_t)row * g.lda, g.lda, min(kT, end - row),
-                              g.B + (int64_t)e * g.stride_b + (int64_t)tn * kT * g.ldb, g.ldb, min(kT, g.N - tn * kT), g.K,
-                              *g.a_sinv, *g.b_sinv,
-                              static_cast<uint8_t *>(g.D) + ((int64_t)row * g.ldd + tn * kT) * kEsz, g.ldd);
+__global__ __launch_bounds__(kThreads, 1) void k_grouped_gemm(const Grouped g, int tiles_n) {
+    run_tiles<FA, FB, OUT, true>(g, RowTiles<OUT>(g, tiles_n));
 }
 
 template <int FA, int FB, int OUT>
-__global__ __launch_bounds__(kThreads) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
-    const int per = tiles_m * tiles_n, e = blockIdx.x / per, in = blockIdx.x - e * per;
-    const int tm = in / tiles_n, tn = in - tm * tiles_n;
-    const int lo = offset_at(g, e), len = max(0, offset_at(g, e + 1) - lo);
-    constexpr int kEsz = OUT == 0 ? 2 : 4;
-    tile_product<FA, FB, OUT>(g.A + (int64_t)tm * kT * g.lda + lo, g.lda, min(kT, g.N - tm * kT),
-                              g.B + (int64_t)tn * kT * g.ldb + lo, g.ldb, min(kT, g.K - tn * kT), len, *g.a_sinv,
-                              *g.b_sinv,
-                              static_cast<uint8_t *>(g.D) + ((int64_t)e * g.stride_d + (int64_t)tm * kT * g.ldd + tn * kT) * kEsz,
-                              g.ldd);
+__global__ __launch_bounds__(kThreads, 1) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
+    run_tiles<FA, FB, OUT, false>(g, ExpertTiles<OUT>(g, tiles_m, tiles_n));
 }
 
 #define FP8DS_GROUPED_SWITCH(CALL)                                                                         \
@@ -199,21 +484,22 @@ __global__ __launch_bounds__(kThreads) void k_grouped_wgrad(const Grouped g, int
     }
 
 // The largest number of row tiles: every expert with rows adds at most one partial tile.
-static int64_t most_row_tiles(int64_t cap, int64_t E, int64_t tm) {
+static int64_t most_row_tiles(int64_t cap, int64_t E) {
     const int64_t used = (cap + 15) / 16;
-    return cap / tm + (E < used ? E : used);
+    return cap / kTm + (E < used ? E : used);
 }
-bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) {
-    return most_row_tiles(cap, E, kT) <= INT_MAX / ((N + kT) / kT);
-}
+// tiles are numbered in 31 bits
+bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) { return most_row_tiles(cap, E) <= INT_MAX / ((N + kTn) / kTn); }
 bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K) {
-    const int64_t per = ((N + kT) / kT) * ((K + kT) / kT);   // at most 2^48
+    const int64_t per = ((N + kTm) / kTm) * ((K + kTn) / kTn);   // at most 2^47
     return E <= INT_MAX / per;
 }
+// One block per CU, fewer for fewer tiles, a multiple of the XCDs.
+static unsigned blocks_for(int64_t tiles) { return (unsigned)((tiles < kCUs ? tiles + kXcds - 1 : kCUs) / kXcds * kXcds); }
 
 hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
-    const int tiles_n = (g.N + kT - 1) / kT;
-    const dim3 grid((unsigned)(most_row_tiles(g.cap, g.E, kT) * tiles_n));
+    const int tiles_n = (g.N + kTn - 1) / kTn;
+    const unsigned grid = blocks_for(most_row_tiles(g.cap, g.E) * tiles_n);
 #define FP8DS_GG(FA_, FB_, O_) k_grouped_gemm<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n)
     FP8DS_GROUPED_SWITCH(FP8DS_GG)
 #undef FP8DS_GG
@@ -221,8 +507,8 @@ hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, 
 }
 
 hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
-    const int tiles_m = (g.N + kT - 1) / kT, tiles_n = (g.K + kT - 1) / kT;
-    const dim3 grid((unsigned)((int64_t)g.E * tiles_m * tiles_n));
+    const int tiles_m = (g.N + kTm - 1) / kTm, tiles_n = (g.K + kTn - 1) / kTn;
+    const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n);
 #define FP8DS_GW(FA_, FB_, O_) k_grouped_wgrad<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n)
     FP8DS_GROUPED_SWITCH(FP8DS_GW)
 #undef FP8DS_GW
