@@ -174,21 +174,17 @@ struct ExpertTiles {
     }
 };
 
-// Swizzles: the 16-byte piece c of an operand's row r sits at piece c ^ swz(r) of its 128 bytes, so
-// that the 16 lanes of one phase of a fragment read (lanes 0-3, 12-15, 20-23, 24-27 and so on: two
-// K groups) hit distinct banks.  A's fragments are 16 consecutive rows.  B's rows are taken in the
-// order that the output wants: a lane's accumulators of fragment q hold four consecutive m, and for
-// bfloat16 the fragments 2 p and 2 p + 1 interleave, so that its eight values of both are
-// consecutive columns and one store instruction writes 64 contiguous bytes of 16 rows, as it does
-// for float32 in plain order.
-__device__ __forceinline__ int swz_a(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-template <int OUT> __device__ __forceinline__ int swz_b(int r) {
-    if constexpr (OUT != 0) return swz_a(r);
-    const int h = (r >> 3) & 3;
-    return ((r >> 1) & 1) ^ (((h ^ (h >> 1)) & 1) << 2) ^ (h & 2);
-}
+// The 16-byte piece c of row r of a slot sits at piece c ^ swz(r) of its 128 bytes, so that the 16
+// lanes of one phase of a fragment read (lanes 0-3, 12-15, 20-23, 24-27 and so on: two K groups) hit
+// distinct banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// B's rows lie in a slot in the order that the output wants.  Row 128 n + 16 q + m is row m of wave
+// column n's fragment q and holds the column col_of(q, m) of its 128: a lane, which has one m, then
+// has 16 bytes of consecutive columns of a row in its accumulators of 8 (bfloat16) or 4 (float32)
+// fragments, and 16 lanes have 256, which one store instruction writes for each of four rows.
 template <int OUT> __device__ __forceinline__ int col_of(int q, int m) {
-    return OUT == 0 ? (q >> 1) * 32 + (m >> 2) * 8 + (q & 1) * 4 + (m & 3) : q * 16 + m;
+    return OUT == 0 ? 8 * m + q : 64 * (q >> 2) + 4 * m + (q & 3);
 }
 
 constexpr int kEarly = 4;       // loads of a step's A that are issued at the end of the step before
@@ -220,12 +216,12 @@ struct Worker {
     // Load i of a slot: wave w fills its 1 KB block 4 i + w, rows 32 i + 8 w .. + 7; lane l row l / 8,
     // stored piece l % 8.
     struct Loads {
-        int ka, kb;              // K byte of the lane's A and B pieces inside a step
+        int k;                   // K byte of the lane's piece inside a step
         uint32_t va, vb;         // the lane's offset in a slot's first load
     };
     __device__ __forceinline__ Loads loads_of(int lane) const {
-        const int row = wave * 8 + (lane >> 3), ka = ((lane & 7) ^ swz_a(row)) * 16, kb = ((lane & 7) ^ swz_b<OUT>(row)) * 16;
-        return Loads{ka, kb, (uint32_t)(row * lda + ka), (uint32_t)(row * ldb + kb)};
+        const int row = wave * 8 + (lane >> 3), k = ((lane & 7) ^ swz(row)) * 16;
+        return Loads{k, (uint32_t)(row * lda + k), (uint32_t)(col_of<OUT>(row >> 4, row & 15) * ldb + k)};
     }
     // Tiles' extents are below 2^31 bytes.  The descriptor has to be in scalar registers.
     static __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const uint8_t *p, int64_t bytes) {
@@ -251,6 +247,8 @@ struct Worker {
 
     // The steps' slots and registers repeat with period 6; a tile starts at the phase that lets its
     // last step be the sixth.
+    // row of B, after the lane's in the first load, that load i takes: slot rows 32 i .. are fragments 2 i and 2 i + 1
+    static __device__ __forceinline__ constexpr int row_b(int i) { return (i >> 2) * 128 + (OUT == 0 ? 2 * (i & 3) : 64 * ((i >> 1) & 1) + 2 * (i & 1)); }
     static __device__ __forceinline__ int steps(const Tile &t) { return max(1, (t.K + kStep - 1) / kStep); }   // K = 0: one of zeros
     static __device__ __forceinline__ int phase(int nk) { return (6 - nk % 6) % 6; }
     static __device__ __forceinline__ uint8_t *pick(bool c, uint8_t *x, uint8_t *y) { return c ? x : y; }
@@ -264,16 +262,16 @@ struct Worker {
         const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
         {
             uint8_t *a = slot_a(p);
-            const uint32_t oa = outside(t, 0, ld.ka);
+            const uint32_t oa = outside(t, 0, ld.k);
 #pragma unroll
             for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | oa) + i * 32 * lda, 0);
         }
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             uint8_t *b = slot_b(p + j);
-            const uint32_t ob = outside(t, j, ld.kb);
+            const uint32_t ob = outside(t, j, ld.k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | ob) + i * 32 * ldb, j);
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | ob) + row_b(i) * ldb, j);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -289,29 +287,23 @@ struct Worker {
         const int nk = steps(t);
         const int lane = fresh_lane(), r16 = lane & 15, g = lane >> 4;
         const Loads ld = loads_of(lane);
-        // fragments: 16-row block i of A, B's rows 32 p + col_of(h, r16) for q = 2 p + h, one swizzle for each h;
-        // the second piece of the lane's 32 bytes is the first's neighbour
-        const int oa = (wm * 16 + r16) * kStep + (((2 * g) ^ swz_a(r16)) << 4);
-        const int rb0 = col_of<OUT>(0, r16), rb1 = col_of<OUT>(1, r16);
-        const int ob0 = (wn * 128 + rb0) * kStep + (((2 * g) ^ swz_b<OUT>(rb0)) << 4);
-        const int ob1 = (wn * 128 + rb1) * kStep + (((2 * g) ^ swz_b<OUT>(rb1)) << 4);
+        // fragments: the second piece of the lane's 32 bytes is the first's neighbour
+        const int o = r16 * kStep + (((2 * g) ^ swz(r16)) << 4), oa = wm * 16 * kStep + o, ob = wn * 128 * kStep + o;
         auto frag_a = [&](const uint8_t *slot, int i) { return frag(slot + i * 32 * kStep, oa, oa ^ 16); };
-        auto frag_b = [&](const uint8_t *slot, int q) {
-            return q & 1 ? frag(slot + (q >> 1) * 32 * kStep, ob1, ob1 ^ 16) : frag(slot + (q >> 1) * 32 * kStep, ob0, ob0 ^ 16);
-        };
+        auto frag_b = [&](const uint8_t *slot, int q) { return frag(slot + q * 16 * kStep, ob, ob ^ 16); };
         const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
         i32x8 fb0[8], fb1[8], fa[2];
         constexpr int kBlocks = NB - 1;
         auto mfma = [&](int i, const i32x8 &a, const i32x8 (&b)[8]) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[q], a, acc[i][q], FB, FA, 0, 0, 0, 0);
+                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[q], acc[i][q], FA, FB, 0, 0, 0, 0);
         };
         // P: the phase's parity; block i's A fragment is fa[(P NB + i) % 2]
         auto step = [&](auto pc, int j, uint8_t *a_cur, uint8_t *a_nxt, uint8_t *b_nxt, uint8_t *b_free, const i32x8 (&fbc)[8],
                         i32x8 (&fbn)[8]) {
             constexpr int P = decltype(pc)::value, kRest = NB > kEarly ? NB - kEarly : 0;
-            const uint32_t out_a = outside(t, j + 1, ld.ka), out_b = outside(t, j + 3, ld.kb);
+            const uint32_t out_a = outside(t, j + 1, ld.k), out_b = outside(t, j + 3, ld.k);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
@@ -325,7 +317,7 @@ struct Worker {
                 }
                 __builtin_amdgcn_sched_barrier(0x7cf);      // loads into LDS stay in this order
 #pragma unroll
-                for (int n = 8 * i / kBlocks; n < 8 * (i + 1) / kBlocks; ++n) load(rs_b, b_free, n, (ld.vb | out_b) + n * 32 * ldb, j + 3);
+                for (int n = 8 * i / kBlocks; n < 8 * (i + 1) / kBlocks; ++n) load(rs_b, b_free, n, (ld.vb | out_b) + row_b(n) * ldb, j + 3);
                 mfma(i, fa[(P * NB + i) & 1], fbc);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -341,7 +333,7 @@ struct Worker {
             __builtin_amdgcn_sched_barrier(0);
             const i32x8 last = fa[(P * NB + NB - 1) & 1];
             fa[(P * NB + NB) & 1] = frag_a(a_nxt, 0);
-            const uint32_t oa2 = outside(t, j + 2, ld.ka);
+            const uint32_t oa2 = outside(t, j + 2, ld.k);
 #pragma unroll
             for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a_cur, n, (ld.va | oa2) + n * 32 * lda, j + 2);
             mfma(NB - 1, last, fbc);
@@ -368,7 +360,7 @@ struct Worker {
         __builtin_amdgcn_sched_barrier(0);
         {
             uint8_t *a = slot_a(p + 1);
-            const uint32_t out_a = outside(t, 1, ld.ka);
+            const uint32_t out_a = outside(t, 1, ld.k);
 #pragma unroll
             for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a, n, (ld.va | out_a) + n * 32 * lda, 1);
         }
@@ -391,42 +383,41 @@ struct Worker {
         store<NB>(t, acc);
     }
 
-    // lane l holds row 32 i + 16 wm + l % 16, columns col_of(q, 4 (l / 16) + u), in element u of acc[i][q]
+    // lane l holds row 32 i + 16 wm + 4 (l / 16) + u, column col_of(q, l % 16), in element u of acc[i][q]
     template <int NB>
     __device__ __forceinline__ void store(const Tile &t, const f32x4 (&acc)[NB][8]) const {
         constexpr int kEsz = OUT == 0 ? 2 : 4, kPer = 16 / kEsz;      // elements of a 16-byte store
         const bool vec = (reinterpret_cast<uintptr_t>(t.D) & 15) == 0 && ldd % kPer == 0 && t.cols % kPer == 0;
-        const int lane = fresh_lane(), col0 = wn * 128 + col_of<OUT>(0, 4 * (lane >> 4)), row = wm * 16 + (lane & 15);
-        const uint32_t at = (uint32_t)((row * (int)ldd + col0) * kEsz);      // 32 rows are less than 2^30 bytes
+        const int lane = fresh_lane(), col0 = wn * 128 + col_of<OUT>(0, lane & 15), row0 = wm * 16 + (lane >> 4) * 4;
+        const uint32_t at = (uint32_t)((row0 * (int)ldd + col0) * kEsz);      // 32 rows are less than 2^30 bytes
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const auto rs = bounded(static_cast<const uint8_t *>(t.D) + (int64_t)(i * 32) * ldd * kEsz, 0x7fffffff);
-            const uint32_t here = i * 32 + row < t.rows ? at : kOutside;
 #pragma unroll
-            for (int p = 0; p < 32 / kPer; ++p) {
-                u32x4 w;
-                if constexpr (OUT == 0) {
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t here = i * 32 + row0 + u < t.rows ? at + (uint32_t)(u * (int)ldd * kEsz) : kOutside;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int p = 0; p < 8 / kPer; ++p) {
+                    u32x4 w;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            w[2 * h + u] = f32x2_to_bf16x2_rne(dequant_bias(acc[i][2 * p + h][2 * u], sa, sb, 0.f),
-                                                               dequant_bias(acc[i][2 * p + h][2 * u + 1], sa, sb, 0.f));
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) w[u] = __float_as_uint(dequant_bias(acc[i][p][u], sa, sb, 0.f));
-                }
-                if (vec) {
-                    const uint32_t o = col0 + p * kPer * 4 < t.cols ? here + (uint32_t)(p * kPer * 4 * kEsz) : kOutside;
-                    __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)o, 0, 0);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u) {
-                        const uint32_t o = col0 + p * kPer * 4 + u < t.cols ? here + (uint32_t)((p * kPer * 4 + u) * kEsz) : kOutside;
+                    for (int h = 0; h < 4; ++h) {
                         if constexpr (OUT == 0)
-                            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[u >> 1] >> (16 * (u & 1))), rs, (int)o, 0, 0);
+                            w[h] = f32x2_to_bf16x2_rne(dequant_bias(acc[i][2 * h][u], sa, sb, 0.f), dequant_bias(acc[i][2 * h + 1][u], sa, sb, 0.f));
                         else
-                            __builtin_amdgcn_raw_buffer_store_b32(w[u], rs, (int)o, 0, 0);
+                            w[h] = __float_as_uint(dequant_bias(acc[i][4 * p + h][u], sa, sb, 0.f));
+                    }
+                    if (vec) {
+                        const uint32_t off = col0 + p * 64 < t.cols ? here + (uint32_t)(p * 64 * kEsz) : kOutside;
+                        __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) {
+                            const uint32_t off = col0 + p * 64 + e < t.cols ? here + (uint32_t)((p * 64 + e) * kEsz) : kOutside;
+                            if constexpr (OUT == 0)
+                                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e >> 1] >> (16 * (e & 1))), rs, (int)off, 0, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b32(w[e], rs, (int)off, 0, 0);
+                        }
                     }
                 }
             }
