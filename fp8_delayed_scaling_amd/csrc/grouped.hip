@@ -9,13 +9,16 @@
 // and to multiples of 16 as they are read, so no content of the buffer makes an access out of
 // bounds.
 //
-// One block of four waves (2 x 2, each up to 128 x 128 made of v_mfma_f32_16x16x128_f8f6f4 tiles)
-// runs on each CU and takes tiles of up to 256 rows of A by 256 rows of B, one after the other: the
-// first loads of a tile are in flight while the tile before is written.  An expert's rows are
-// shared evenly among its tiles, in steps of 32 (16 for each row of waves); a tile runs only the
-// 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the tile's extent: rows
-// past it, and the 16-byte pieces of the last K step past K (their offset is moved out of the
-// bound), arrive as zeros without touching memory.
+// Two kernels, both of four waves (2 x 2, each up to 128 x 128 made of v_mfma_f32_16x16x128_f8f6f4
+// tiles) that take one tile after the other, the first loads of a tile in flight while the tile
+// before is written:
+//   Wide    up to 256 rows of A by 256 rows of B, one block on each CU: the fewest bytes per product
+//   Paired  up to 128 rows by 256, two blocks on each CU, which fill each other's waits: for short
+//           contractions, small problems and few rows per expert
+// An expert's rows are shared evenly among its tiles, in steps of 32 (16 for each row of waves); a
+// tile runs only the 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the
+// tile's extent: rows past it, and the 16-byte pieces of the last K step past K (their offset is
+// moved out of the bound), arrive as zeros without touching memory.
 #include <climits>
 #include <type_traits>
 
@@ -27,19 +30,20 @@ namespace fp8ds {
 
 namespace {
 
-constexpr int kTm = 256, kTn = 256;          // most rows of a tile, its columns (rows of B)
+constexpr int kWide = 256, kPaired = 128;    // most rows of a tile
+constexpr int kTn = 256;                     // its columns (rows of B)
 constexpr int kStep = 128;                   // K bytes per step
 constexpr int kThreads = 256;
-constexpr int kCUs = 256;                    // blocks of a launch: one per CU
+constexpr int kCUs = 256;
 constexpr int kXcds = 8;                     // blocks are dealt round-robin to the XCDs
-constexpr int kSlot = 256 * kStep;           // one K step of an operand in LDS
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every tile's extent (below 2^31 bytes)
+constexpr int kStreaming = 2;                // nontemporal: outputs leave L2 first (weight gradient 595 -> 469 us)
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
 
 // vmcnt-only wait, and a workgroup barrier without a fence (a fenced one would wait for every load
 // in flight); the empty asm statements keep memory accesses on their side.
 #define FP8DS_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(0xF70 | ((n) & 0xF) | (((n) >> 4) << 14))
-#define FP8DS_WAIT_VM_LGKM(n) __builtin_amdgcn_s_waitcnt(0x070 | ((n) & 0xF) | (((n) >> 4) << 14))   // and lgkmcnt(0)
+#define FP8DS_WAIT_LGKM() __builtin_amdgcn_s_waitcnt(0xC07F)
 #define FP8DS_WAIT_ALL() __builtin_amdgcn_s_waitcnt(0x0070)     // vmcnt(0) lgkmcnt(0)
 #define FP8DS_BARRIER()                          \
     do {                                         \
@@ -50,10 +54,19 @@ constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds ch
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Rows of each of the tiles that share n rows: ceil(n / 256) tiles, the same multiple of 32 each
-// (the last may have fewer, never none).
+// Division by a number that is the same for all tiles: opaque, so that no reciprocal is kept from one
+// tile to the next in a register (there is none to spare, and a reload would wait for all stores).
+__device__ __forceinline__ int divide(int n, int d) {
+    asm volatile("" : "+s"(d));
+    return (int)((uint32_t)n / (uint32_t)d);
+}
+__device__ __forceinline__ int modulo(int n, int d) { return n - divide(n, d) * d; }
+
+// Rows of each of the tiles of at most TM rows that share n rows: ceil(n / TM) tiles, the same
+// multiple of 32 each (the last may have fewer, never none).
+template <int TM>
 __host__ __device__ constexpr int tile_rows(int n) {
-    const int tiles = (n + kTm - 1) / kTm, blocks = (n + 31) / 32;
+    const int tiles = (n + TM - 1) / TM, blocks = (n + 31) / 32;
     return tiles > 0 ? (blocks + tiles - 1) / tiles * 32 : 0;
 }
 
@@ -64,6 +77,89 @@ struct Tile {
     int rows, cols, K;
 };
 
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1, 2, 4, 8 inside 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15, then 31
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
+}
+
+// The forward's tiles, an expert's ceil(rows / TM) * tiles_n with its row tiles running fastest.
+// Among 64 experts, tall tiles come first (in every expert all tiles but the last have one height).
+// The tiles are taken in rounds, runs of kRun dealt to the XCDs forwards and backwards in turn, a
+// run to blocks of one XCD: they share B's rows, which come from HBM once, and A's.  Every block so
+// takes a like mixture of heights, and half of the blocks take theirs from the last round to the
+// first: tall tiles, bound by the products, run beside low ones, bound by B's bytes.  (Unevenly
+// routed forward of 64 experts, half of which have under 1 % of the rows: in the experts' order
+// 330 us, tall tiles first 286, this way 275; evenly routed 230.)
+template <int OUT, int TM>
+struct RowTiles {
+    static constexpr int kRun = 8;
+    const Grouped &g;
+    int tiles_n, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
+    __device__ __forceinline__ RowTiles(const Grouped &g_, int tiles_n_) : g(g_), tiles_n(tiles_n_), total(0), round(0), e0(0), before(0) {
+        int lo, hi;
+        for (int e = 0; e < g.E; e += 64) total += count(e, lo, hi);
+        deals = (total + kRun * kXcds - 1) / (kRun * kXcds);
+    }
+    // tiles of the experts e .. e + 63, and the rows of the lane's among them
+    __device__ __forceinline__ int count(int e, int &lo, int &hi) const {
+        const int i = e + (threadIdx.x & 63);
+        lo = hi = 0;
+        if (i < g.E) {
+            lo = min(max(g.offsets[i], 0), g.cap) & ~15;
+            hi = max(lo, min(max(g.offsets[i + 1], 0), g.cap) & ~15);
+        }
+        return uniform(__builtin_amdgcn_readlane(wave_scan((hi - lo + TM - 1) / TM), 63)) * tiles_n;
+    }
+    // the block's next tile; false when there is none
+    __device__ __forceinline__ bool operator()(Tile &t) {
+        const int slots = gridDim.x / kXcds, slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
+        const int rounds = divide(deals * kRun + slots - 1, slots);
+        int tile;
+        for (;; ++round) {
+            if (round >= rounds) return false;
+            const int r = (slot / kRun) & 1 ? rounds - 1 - round : round;
+            const int l = r * slots + (r & 1 ? slots - 1 - slot : slot), deal = l / kRun;
+            tile = (deal * kXcds + (deal & 1 ? kXcds - 1 - xcd : xcd)) * kRun + l % kRun;
+            if (tile < total) break;
+        }
+        ++round;
+        int lo, hi, n = count(e0, lo, hi);
+        while (tile < before) {
+            e0 -= 64;
+            n = count(e0, lo, hi);
+            before -= n;
+        }
+        while (tile >= before + n) {
+            before += n;
+            e0 += 64;
+            n = count(e0, lo, hi);
+        }
+        int at = tile - before, h = TM / 32;
+        const int mine = tile_rows<TM>(hi - lo) / 32;
+        for (; h > 1; --h) {
+            const int of_h = uniform(__builtin_amdgcn_readlane(wave_scan(mine == h ? (hi - lo + TM - 1) / TM : 0), 63)) * tiles_n;
+            if (at < of_h) break;
+            at -= of_h;
+        }
+        const int tiles = mine == h ? (hi - lo + TM - 1) / TM : 0, incl = wave_scan(tiles);
+        const int k = __builtin_ctzll(__ballot(incl * tiles_n > at)), e = e0 + k;
+        const int first = __builtin_amdgcn_readlane(lo, k), end = __builtin_amdgcn_readlane(hi, k);
+        const int row_tiles = __builtin_amdgcn_readlane(tiles, k), in = at - __builtin_amdgcn_readlane(incl - tiles, k) * tiles_n;
+        const int tn = divide(in, row_tiles), row = first + (in - tn * row_tiles) * h * 32;
+        constexpr int kEsz = OUT == 0 ? 2 : 4;
+        t = Tile{g.A + (int64_t)row * g.lda, g.B + (int64_t)e * g.stride_b + (int64_t)tn * kTn * g.ldb,
+                 static_cast<uint8_t *>(g.D) + ((int64_t)row * g.ldd + tn * kTn) * kEsz, min(h * 32, end - row),
+                 min(kTn, g.N - tn * kTn), g.K};
+        return true;
+    }
+};
+
 // Scalar loads: the offsets are not written while the kernel runs, and a vector load would wait
 // for every store in flight before it.
 __device__ __forceinline__ int offset_at(const Grouped &g, int e) {
@@ -71,106 +167,65 @@ __device__ __forceinline__ int offset_at(const Grouped &g, int e) {
     return min(max(o[uniform(e)], 0), g.cap) & ~15;
 }
 
-// The forward's tiles: expert e has ceil(rows / 256) * tiles_n.  Each XCD takes a contiguous range
-// of them, in which an expert's row tiles run fastest, so that blocks which share B's rows run on
-// one XCD at one time and B comes from HBM once.  A block finds its first tile with the sums of 64
-// experts' tile counts at a time, and walks on from there.
-template <int OUT>
-struct RowTiles {
-    const Grouped &g;
-    int tiles_n, tile, end;          // the block's next tile, the end of its XCD's range
-    int e, before, first, last;      // an expert at or before that tile's, the tiles before it, its rows
-    static __device__ __forceinline__ int count(int lo, int hi) { return hi > lo ? (hi - lo + kTm - 1) / kTm : 0; }
-    __device__ __forceinline__ int counts(int e0) const {
-        const int i = e0 + (threadIdx.x & 63);
-        if (i >= g.E) return 0;
-        return count(min(max(g.offsets[i], 0), g.cap) & ~15, min(max(g.offsets[i + 1], 0), g.cap) & ~15);
-    }
-    static __device__ __forceinline__ int scan(int n) {
-        const int lane = threadIdx.x & 63;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(n, off, 64);
-            if (lane >= off) n += v;
-        }
-        return n;
-    }
-    __device__ __forceinline__ RowTiles(const Grouped &g_, int tiles_n_) : g(g_), tiles_n(tiles_n_) {
-        int total = 0;
-        for (int e0 = 0; e0 < g.E; e0 += 64) total += uniform(__shfl(scan(counts(e0)), 63, 64));
-        total *= tiles_n;
-        const int xcd = blockIdx.x % kXcds, q8 = total / kXcds, r8 = total % kXcds;
-        const int begin = xcd * q8 + min(xcd, r8);
-        end = begin + q8 + (xcd < r8 ? 1 : 0);
-        tile = begin + blockIdx.x / kXcds;
-        e = before = first = last = 0;
-        if (tile >= end) return;
-        int seen = 0;
-        for (int e0 = 0; e0 < g.E; e0 += 64) {
-            const int n = counts(e0), incl = scan(n);
-            const uint64_t past = __ballot((seen + incl) * tiles_n > tile);
-            if (past != 0) {
-                const int l = __builtin_ctzll(past);
-                e = uniform(e0 + l);
-                before = (seen + uniform(__shfl(incl - n, l, 64))) * tiles_n;
-                break;
-            }
-            seen += uniform(__shfl(incl, 63, 64));
-        }
-        first = offset_at(g, e);
-        last = offset_at(g, e + 1);
-    }
-    // the block's next tile; false when there is none
-    __device__ __forceinline__ bool operator()(Tile &t) {
-        if (tile >= end) return false;
-        int row_tiles = count(first, last);
-        while (before + row_tiles * tiles_n <= tile && e + 1 < g.E) {
-            before += row_tiles * tiles_n;
-            ++e;
-            first = last;
-            last = offset_at(g, e + 1);
-            row_tiles = count(first, last);
-        }
-        const int in = tile - before, tn = in / row_tiles, h = tile_rows(last - first), row = first + (in - tn * row_tiles) * h;
-        constexpr int kEsz = OUT == 0 ? 2 : 4;
-        t = Tile{g.A + (int64_t)row * g.lda, g.B + (int64_t)e * g.stride_b + (int64_t)tn * kTn * g.ldb,
-                 static_cast<uint8_t *>(g.D) + ((int64_t)row * g.ldd + tn * kTn) * kEsz, min(h, last - row),
-                 min(kTn, g.N - tn * kTn), g.K};
-        tile += gridDim.x / kXcds;
-        return true;
-    }
-};
-
 // The weight gradient's tiles.  Every XCD takes an eighth of each expert's tiles, whatever the
 // routing: the ranges of B that an XCD reads stay in its L2, A is read by all of them.  Which
-// eighth moves with the expert, and which of the XCD's blocks takes a tile moves from one round of
-// tiles to the next, so that remainders and experts of uneven length spread.
+// eighth moves with the expert, so that remainders spread.  Where two to four experts' eighths fill
+// an XCD's blocks, those form as many groups, and each expert goes to the group that has the least
+// work so far (a tile costs its K steps and about three for its output); else the tiles are taken
+// in order, shifted by some blocks in every round.
 template <int OUT>
 struct ExpertTiles {
     const Grouped &g;
-    int tiles_m, tiles_n, h, round;
+    int tiles_m, tiles_n, h, per, chunk, slots, groups, next;      // next: round, or expert with groups
+    int work[4];
     __device__ __forceinline__ ExpertTiles(const Grouped &g_, int tiles_m_, int tiles_n_)
-        : g(g_), tiles_m(tiles_m_), tiles_n(tiles_n_), h(tile_rows(g_.N)), round(0) {}
+        : g(g_), tiles_m(tiles_m_), tiles_n(tiles_n_), h(tile_rows<kPaired>(g_.N)), next(0) {
+        per = tiles_m * tiles_n;
+        chunk = (per + kXcds - 1) / kXcds;
+        slots = gridDim.x / kXcds;
+        groups = slots / chunk;
+        if (groups < 2 || groups > 4 || groups * chunk * 10 < slots * 9) groups = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) work[i] = i < groups ? 0 : INT_MAX;
+    }
     __device__ __forceinline__ bool operator()(Tile &t) {
-        const int per = tiles_m * tiles_n, chunk = (per + kXcds - 1) / kXcds;
-        const int slots = gridDim.x / kXcds, xcd = blockIdx.x % kXcds;
-        for (;; ++round) {
-            const int64_t at = (int64_t)round * slots + (blockIdx.x / kXcds + round * 11) % slots;
-            if (at >= (int64_t)g.E * chunk) {
-                if ((int64_t)round * slots >= (int64_t)g.E * chunk) return false;
-                continue;
+        const int slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
+        int e, in;
+        if (groups > 0) {
+            const int mine = divide(slot, chunk);
+            for (;; ++next) {
+                if (next >= g.E || mine >= groups) return false;
+                const int cost = (max(0, offset_at(g, next + 1) - offset_at(g, next)) + kStep - 1) / kStep + 3;
+                int least = 0, w = work[0];
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    if (work[i] < w) { w = work[i]; least = i; }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i == least) work[i] += cost;
+                e = next;
+                in = slot - mine * chunk + (xcd + e) % kXcds * chunk;
+                if (least == mine && in < per) break;
             }
-            const int e = (int)(at / chunk), in = (int)(at - (int64_t)e * chunk) + ((xcd + e) % kXcds) * chunk;
-            if (in >= per) continue;
-            ++round;
-            const int tn = in / tiles_m, tm = in - tn * tiles_m;
-            const int lo = offset_at(g, e), len = max(0, offset_at(g, e + 1) - lo);
-            constexpr int kEsz = OUT == 0 ? 2 : 4;
-            t = Tile{g.A + (int64_t)tm * h * g.lda + lo, g.B + (int64_t)tn * kTn * g.ldb + lo,
-                     static_cast<uint8_t *>(g.D) + ((int64_t)e * g.stride_d + (int64_t)tm * h * g.ldd + tn * kTn) * kEsz,
-                     min(h, g.N - tm * h), min(kTn, g.K - tn * kTn), len};
-            return true;
+            ++next;
+        } else {
+            const int total = g.E * chunk;                             // 31 bits
+            for (;; ++next) {
+                if (next * slots >= total) return false;
+                const int at = next * slots + modulo(slot + next * 11, slots);
+                e = divide(at, chunk);
+                in = at - e * chunk + (xcd + e) % kXcds * chunk;
+                if (at < total && in < per) break;
+            }
+            ++next;
         }
+        const int tn = divide(in, tiles_m), tm = in - tn * tiles_m;
+        const int lo = offset_at(g, e), len = max(0, offset_at(g, e + 1) - lo);
+        constexpr int kEsz = OUT == 0 ? 2 : 4;
+        t = Tile{g.A + (int64_t)tm * h * g.lda + lo, g.B + (int64_t)tn * kTn * g.ldb + lo,
+                 static_cast<uint8_t *>(g.D) + ((int64_t)e * g.stride_d + (int64_t)tm * h * g.ldd + tn * kTn) * kEsz,
+                 min(h, g.N - tm * h), min(kTn, g.K - tn * kTn), len};
+        return true;
     }
 };
 
@@ -187,22 +242,15 @@ template <int OUT> __device__ __forceinline__ int col_of(int q, int m) {
     return OUT == 0 ? 8 * m + q : 64 * (q >> 2) + 4 * m + (q & 3);
 }
 
-constexpr int kEarly = 4;       // loads of a step's A that are issued at the end of the step before
-
-// A block's work on its tiles.  LDS holds two K steps of A and three of B, 160 KB in all.  Step j
-// multiplies A_j, its fragments read one 16-row block ahead of the MFMAs, by B_j, whose fragments
-// were read into registers during step j - 1; it reads the fragments of B_{j+1}, loads A_{j+1} into
-// the slot that A_{j-1} used and then B_{j+3} into B_j's, and before its last block waits for all
-// but the latter: A is read by several tiles at a time and comes from L2, B from HBM.
+// What both kernels share: the loads, the fragments and the output.
 template <int FA, int FB, int OUT>
-struct Worker {
-    uint8_t *sa0, *sa1, *sb0, *sb1, *sb2;
+struct Work {
     int64_t ldd;
     float sa, sb;
     int lda, ldb, wave, wm, wn;
 
-    __device__ __forceinline__ Worker(const Grouped &gr, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1, uint8_t *b2)
-        : sa0(a0), sa1(a1), sb0(b0), sb1(b1), sb2(b2), ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb) {
+    explicit __device__ __forceinline__ Work(const Grouped &gr)
+        : ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb) {
         wave = uniform((int)threadIdx.x >> 6);
         wm = wave >> 1; wn = wave & 1;
     }
@@ -245,144 +293,9 @@ struct Worker {
         return v;
     }
 
-    // The steps' slots and registers repeat with period 6; a tile starts at the phase that lets its
-    // last step be the sixth.
     // row of B, after the lane's in the first load, that load i takes: slot rows 32 i .. are fragments 2 i and 2 i + 1
     static __device__ __forceinline__ constexpr int row_b(int i) { return (i >> 2) * 128 + (OUT == 0 ? 2 * (i & 3) : 64 * ((i >> 1) & 1) + 2 * (i & 1)); }
     static __device__ __forceinline__ int steps(const Tile &t) { return max(1, (t.K + kStep - 1) / kStep); }   // K = 0: one of zeros
-    static __device__ __forceinline__ int phase(int nk) { return (6 - nk % 6) % 6; }
-    static __device__ __forceinline__ uint8_t *pick(bool c, uint8_t *x, uint8_t *y) { return c ? x : y; }
-    __device__ __forceinline__ uint8_t *slot_a(int p) const { return pick(p & 1, sa1, sa0); }
-    __device__ __forceinline__ uint8_t *slot_b(int p) const { return pick(p % 3 == 0, sb0, pick(p % 3 == 1, sb1, sb2)); }
-
-    // A tile's first loads: A_0 and B_0, then B_1 and B_2.
-    __device__ __forceinline__ void first_loads(const Tile &t) const {
-        const int p = phase(steps(t));
-        const Loads ld = loads_of(fresh_lane());
-        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
-        {
-            uint8_t *a = slot_a(p);
-            const uint32_t oa = outside(t, 0, ld.k);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | oa) + i * 32 * lda, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            uint8_t *b = slot_b(p + j);
-            const uint32_t ob = outside(t, j, ld.k);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | ob) + row_b(i) * ldb, j);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-
-    // Products of a tile of at most 32 NB rows, then the next tile's first loads, then the output.
-    template <int NB>
-    __device__ __forceinline__ void run(const Tile &t, const Tile &next, bool more) const {
-        f32x4 acc[NB][8];
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int nk = steps(t);
-        const int lane = fresh_lane(), r16 = lane & 15, g = lane >> 4;
-        const Loads ld = loads_of(lane);
-        // fragments: the second piece of the lane's 32 bytes is the first's neighbour
-        const int o = r16 * kStep + (((2 * g) ^ swz(r16)) << 4), oa = wm * 16 * kStep + o, ob = wn * 128 * kStep + o;
-        auto frag_a = [&](const uint8_t *slot, int i) { return frag(slot + i * 32 * kStep, oa, oa ^ 16); };
-        auto frag_b = [&](const uint8_t *slot, int q) { return frag(slot + q * 16 * kStep, ob, ob ^ 16); };
-        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
-        i32x8 fb0[8], fb1[8], fa[2];
-        constexpr int kBlocks = NB - 1;
-        auto mfma = [&](int i, const i32x8 &a, const i32x8 (&b)[8]) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[q], acc[i][q], FA, FB, 0, 0, 0, 0);
-        };
-        // P: the phase's parity; block i's A fragment is fa[(P NB + i) % 2]
-        auto step = [&](auto pc, int j, uint8_t *a_cur, uint8_t *a_nxt, uint8_t *b_nxt, uint8_t *b_free, const i32x8 (&fbc)[8],
-                        i32x8 (&fbn)[8]) {
-            constexpr int P = decltype(pc)::value, kRest = NB > kEarly ? NB - kEarly : 0;
-            const uint32_t out_a = outside(t, j + 1, ld.k), out_b = outside(t, j + 3, ld.k);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                fa[(P * NB + i + 1) & 1] = frag_a(a_cur, i + 1);
-#pragma unroll
-                for (int q = 8 * i / kBlocks; q < 8 * (i + 1) / kBlocks; ++q) fbn[q] = frag_b(b_nxt, q);
-                // the rest of A_{j+1} in the first block, B_{j+3} over all
-                if (i == 0) {
-#pragma unroll
-                    for (int n = kEarly; n < kEarly + kRest; ++n) load(rs_a, a_nxt, n, (ld.va | out_a) + n * 32 * lda, j + 1);
-                }
-                __builtin_amdgcn_sched_barrier(0x7cf);      // loads into LDS stay in this order
-#pragma unroll
-                for (int n = 8 * i / kBlocks; n < 8 * (i + 1) / kBlocks; ++n) load(rs_b, b_free, n, (ld.vb | out_b) + row_b(n) * ldb, j + 3);
-                mfma(i, fa[(P * NB + i) & 1], fbc);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            asm volatile("" ::: "memory");
-            FP8DS_WAIT_VM_LGKM(8);
-            FP8DS_BARRIER();
-            __builtin_amdgcn_sched_barrier(0);
-            const i32x8 last = fa[(P * NB + NB - 1) & 1];
-            fa[(P * NB + NB) & 1] = frag_a(a_nxt, 0);
-            const uint32_t oa2 = outside(t, j + 2, ld.k);
-#pragma unroll
-            for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a_cur, n, (ld.va | oa2) + n * 32 * lda, j + 2);
-            mfma(NB - 1, last, fbc);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        const int p = phase(nk);
-        asm volatile("" ::: "memory");
-        FP8DS_WAIT_VM(16);                               // A_0 and B_0
-        FP8DS_BARRIER();
-        {
-            const uint8_t *b = slot_b(p), *a = slot_a(p);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) fb0[q] = fb1[q] = frag_b(b, q);
-            fa[0] = fa[1] = frag_a(a, 0);
-        }
-        FP8DS_WAIT_VM_LGKM(16);
-        FP8DS_BARRIER();
-        __builtin_amdgcn_sched_barrier(0);
-        {
-            uint8_t *a = slot_a(p + 1);
-            const uint32_t out_a = outside(t, 1, ld.k);
-#pragma unroll
-            for (int n = 0; n < (NB < kEarly ? NB : kEarly); ++n) load(rs_a, a, n, (ld.va | out_a) + n * 32 * lda, 1);
-        }
-        const std::integral_constant<int, 0> even{};
-        const std::integral_constant<int, 1> odd{};
-        int j = -p;
-        do {
-            if (j >= 0) step(even, j, sa0, sa1, sb1, sb0, fb0, fb1);
-            if (j + 1 >= 0) step(odd, j + 1, sa1, sa0, sb2, sb1, fb1, fb0);
-            if (j + 2 >= 0) step(even, j + 2, sa0, sa1, sb0, sb2, fb0, fb1);
-            if (j + 3 >= 0) step(odd, j + 3, sa1, sa0, sb1, sb0, fb1, fb0);
-            if (j + 4 >= 0) step(even, j + 4, sa0, sa1, sb2, sb1, fb0, fb1);
-            step(odd, j + 5, sa1, sa0, sb0, sb2, fb1, fb0);
-            j += 6;
-        } while (j < nk);
-        FP8DS_WAIT_ALL();                                // every load into the slots has landed
-        FP8DS_BARRIER();
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) first_loads(next);
-        store<NB>(t, acc);
-    }
-
     // lane l holds row 32 i + 16 wm + 4 (l / 16) + u, column col_of(q, l % 16), in element u of acc[i][q]
     template <int NB>
     __device__ __forceinline__ void store(const Tile &t, const f32x4 (&acc)[NB][8]) const {
@@ -408,7 +321,7 @@ struct Worker {
                     }
                     if (vec) {
                         const uint32_t off = col0 + p * 64 < t.cols ? here + (uint32_t)(p * 64 * kEsz) : kOutside;
-                        __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, kStreaming);
                     } else {
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) {
@@ -426,40 +339,333 @@ struct Worker {
     }
 };
 
-// FINE: a variant for every height from 128 rows on (an expert's rows have any); else two.
-template <int FA, int FB, int OUT, bool FINE, class Tiles>
-__device__ __forceinline__ void run_tiles(const Grouped &g, Tiles &&tiles) {
-    __shared__ __align__(16) uint8_t sa0[kSlot];
-    __shared__ __align__(16) uint8_t sa1[kSlot];
-    __shared__ __align__(16) uint8_t sb0[kSlot];
-    __shared__ __align__(16) uint8_t sb1[kSlot];
-    __shared__ __align__(16) uint8_t sb2[kSlot];
+// Wide.  LDS holds two K steps of A and three of B, 160 KB in all.  Step j
+// multiplies A_j, its fragments read one 16-row block ahead of the MFMAs, by B_j, whose fragments
+// were read into registers during step j - 1; it reads the fragments of B_{j+1}, loads B_{j+3} into
+// B_j's slot, before its last block waits for A_{j+1} and B_{j+2}, and in that block loads A_{j+2}
+// into A_j's slot.  A is read by several tiles at a time and comes from L2, B from HBM.
+template <int FA, int FB, int OUT>
+struct Wide : Work<FA, FB, OUT> {
+    using W = Work<FA, FB, OUT>;
+    using Loads = typename W::Loads;
+    using W::loads_of;
+    using W::fresh_lane;
+    using W::bounded;
+    using W::load;
+    using W::outside;
+    using W::frag;
+    using W::row_b;
+    using W::steps;
+    using W::lda;
+    using W::ldb;
+    using W::wm;
+    using W::wn;
+    using W::store;
+    uint8_t *sa0, *sa1, *sb0, *sb1, *sb2;
+    __device__ __forceinline__ Wide(const Grouped &g, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1, uint8_t *b2)
+        : W(g), sa0(a0), sa1(a1), sb0(b0), sb1(b1), sb2(b2) {}
+    // The steps' slots and registers repeat with period 6; a tile starts at the phase that lets its
+    // last step be the sixth.
+    static __device__ __forceinline__ int phase(int nk) { return (6 - nk % 6) % 6; }
+    static __device__ __forceinline__ uint8_t *pick(bool c, uint8_t *x, uint8_t *y) { return c ? x : y; }
+    __device__ __forceinline__ uint8_t *slot_a(int p) const { return pick(p & 1, sa1, sa0); }
+    __device__ __forceinline__ uint8_t *slot_b(int p) const { return pick(p % 3 == 0, sb0, pick(p % 3 == 1, sb1, sb2)); }
+
+    // A tile's first loads, all five slots: A_0 and B_0, then A_1, B_1 and B_2.
+    __device__ __forceinline__ void first_loads(const Tile &t) const {
+        const int p = phase(steps(t));
+        const Loads ld = loads_of(fresh_lane());
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const uint32_t out = outside(t, j, ld.k);
+            uint8_t *const a = slot_a(p + j), *const b = slot_b(p + j);
+            if (j < 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | out) + i * 32 * lda, j);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out) + row_b(i) * ldb, j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Waits for all loads but the last N before `stores` (at least that many) output stores: those
+    // may be in flight too.
+    template <int N>
+    static __device__ __forceinline__ void wait_before_stores(int stores) {
+        asm volatile("" ::: "memory");
+        if (stores >= 32) FP8DS_WAIT_VM(N + 32);
+        else if (stores >= 16) FP8DS_WAIT_VM(N + 16);
+        else FP8DS_WAIT_VM(N);
+    }
+
+    // Products of a tile of at most 32 NB rows, then the next tile's first loads, then the output.
+    // `stores`: those of the tile before, still in flight.  Returns this tile's.
+    template <int NB, class Tiles>
+    __device__ __forceinline__ int run(const Tile &t, Tiles &tiles, Tile &next, bool &more, int stores) const {
+        f32x4 acc[NB][8];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int nk = steps(t);
+        const int lane = fresh_lane(), r16 = lane & 15, g = lane >> 4;
+        const Loads ld = loads_of(lane);
+        // fragments: the second piece of the lane's 32 bytes is the first's neighbour
+        const int o = r16 * kStep + (((2 * g) ^ swz(r16)) << 4), oa = wm * 16 * kStep + o, ob = wn * 128 * kStep + o;
+        auto frag_a = [&](const uint8_t *slot, int i) { return frag(slot + i * 32 * kStep, oa, oa ^ 16); };
+        auto frag_b = [&](const uint8_t *slot, int q) { return frag(slot + q * 16 * kStep, ob, ob ^ 16); };
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+        i32x8 fb0[8], fb1[8], fa[2];
+        constexpr int kBlocks = NB - 1;
+        auto mfma = [&](int i, const i32x8 &a, const i32x8 (&b)[8]) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[q], acc[i][q], FA, FB, 0, 0, 0, 0);
+        };
+        auto interleave = [](int n) {
+#pragma unroll
+            for (int q = 0; q < n; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            }
+        };
+        // P: the phase's parity; block i's A fragment is fa[(P NB + i) % 2]
+        auto step = [&](auto pc, int j, uint8_t *a_cur, uint8_t *a_nxt, uint8_t *b_nxt, uint8_t *b_free, const i32x8 (&fbc)[8],
+                        i32x8 (&fbn)[8]) {
+            constexpr int P = decltype(pc)::value;
+            const uint32_t out_b = outside(t, j + 3, ld.k);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                fa[(P * NB + i + 1) & 1] = frag_a(a_cur, i + 1);
+#pragma unroll
+                for (int q = 8 * i / kBlocks; q < 8 * (i + 1) / kBlocks; ++q) {
+                    fbn[q] = frag_b(b_nxt, q);
+                    load(rs_b, b_free, q, (ld.vb | out_b) + row_b(q) * ldb, j + 3);
+                }
+                mfma(i, fa[(P * NB + i) & 1], fbc);
+                interleave(8);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (j == 0) wait_before_stores<8>(stores);
+            else FP8DS_WAIT_VM(8);
+            FP8DS_WAIT_LGKM();
+            FP8DS_BARRIER();
+            __builtin_amdgcn_sched_barrier(0);
+            const i32x8 last = fa[(P * NB + NB - 1) & 1];
+            fa[(P * NB + NB) & 1] = frag_a(a_nxt, 0);
+            const uint32_t out_a = outside(t, j + 2, ld.k);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) load(rs_a, a_cur, n, (ld.va | out_a) + n * 32 * lda, j + 2);
+            mfma(NB - 1, last, fbc);
+            interleave(8);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const int p = phase(nk);
+        wait_before_stores<24>(stores);                      // A_0 and B_0
+        FP8DS_BARRIER();
+        {
+            const uint8_t *b = slot_b(p), *a = slot_a(p);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) fb0[q] = fb1[q] = frag_b(b, q);
+            fa[0] = fa[1] = frag_a(a, 0);
+        }
+        FP8DS_WAIT_LGKM();
+        FP8DS_BARRIER();
+        __builtin_amdgcn_sched_barrier(0);
+        const std::integral_constant<int, 0> even{};
+        const std::integral_constant<int, 1> odd{};
+        int j = -p;
+        do {
+            if (j >= 0) step(even, j, sa0, sa1, sb1, sb0, fb0, fb1);
+            if (j + 1 >= 0) step(odd, j + 1, sa1, sa0, sb2, sb1, fb1, fb0);
+            if (j + 2 >= 0) step(even, j + 2, sa0, sa1, sb0, sb2, fb0, fb1);
+            if (j + 3 >= 0) step(odd, j + 3, sa1, sa0, sb1, sb0, fb1, fb0);
+            if (j + 4 >= 0) step(even, j + 4, sa0, sa1, sb2, sb1, fb0, fb1);
+            step(odd, j + 5, sa1, sa0, sb0, sb2, fb1, fb0);
+            j += 6;
+        } while (j < nk);
+        FP8DS_WAIT_ALL();                                    // every load into the slots has landed
+        FP8DS_BARRIER();
+        __builtin_amdgcn_sched_barrier(0);
+        more = tiles(next);                                  // nothing is in flight that its loads would wait for
+        if (more) first_loads(next);
+        this->template store<NB>(t, acc);
+        return NB * (OUT == 0 ? 4 : 8);
+    }
+
+};
+
+// Paired.  LDS holds one K step of A and two of B, 80 KB: two blocks share a
+// CU.  Step j waits for A_j and B_j, reads all their fragments into registers, and after a barrier
+// loads A_{j+1} and B_{j+2} into the slots so freed while its MFMAs run; the other block's MFMAs
+// fill the time of the reads and waits, and its loads that of the output.  A is read by several
+// tiles at a time and comes from L2; B, from HBM, has two steps to arrive.
+template <int FA, int FB, int OUT>
+struct Paired : Work<FA, FB, OUT> {
+    using W = Work<FA, FB, OUT>;
+    using Loads = typename W::Loads;
+    using W::loads_of;
+    using W::fresh_lane;
+    using W::bounded;
+    using W::load;
+    using W::outside;
+    using W::frag;
+    using W::row_b;
+    using W::steps;
+    using W::lda;
+    using W::ldb;
+    using W::wm;
+    using W::wn;
+    using W::store;
+    uint8_t *sa0, *sb0, *sb1;
+    __device__ __forceinline__ Paired(const Grouped &g, uint8_t *a0, uint8_t *b0, uint8_t *b1) : W(g), sa0(a0), sb0(b0), sb1(b1) {}
+    // B's slots alternate; a tile starts with the one that lets its last step use the second.
+    __device__ __forceinline__ uint8_t *slot_b(int p) const {
+        uint8_t *const x = sb0, *const y = sb1;
+        return p & 1 ? y : x;
+    }
+
+    // A tile's first loads: B_0 and A_0, then B_1.
+    __device__ __forceinline__ void first_loads(const Tile &t) const {
+        const int p = steps(t) & 1;
+        const Loads ld = loads_of(fresh_lane());
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+        const uint32_t out0 = outside(t, 0, ld.k), out1 = outside(t, 1, ld.k);
+        uint8_t *b0 = slot_b(p), *b1 = slot_b(p + 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(rs_b, b0, i, (ld.vb | out0) + row_b(i) * ldb, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load(rs_a, sa0, i, (ld.va | out0) + i * 32 * lda, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(rs_b, b1, i, (ld.vb | out1) + row_b(i) * ldb, 1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // Products of a tile of at most 32 NB rows, then the next tile's first loads, then the output.
+    template <int NB, class Tiles>
+    __device__ __forceinline__ int run(const Tile &t, Tiles &tiles, Tile &next, bool &more, int) const {
+        f32x4 acc[NB][8];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int nk = steps(t);
+        const int lane = fresh_lane(), r16 = lane & 15, g = lane >> 4;
+        const Loads ld = loads_of(lane);
+        // fragments: the second piece of the lane's 32 bytes is the first's neighbour
+        const int o = r16 * kStep + (((2 * g) ^ swz(r16)) << 4), oa = wm * 16 * kStep + o, ob = wn * 128 * kStep + o;
+        const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
+        auto step = [&](int j, uint8_t *b) {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+            FP8DS_WAIT_VM(8);                                // all but B_{j+1}
+            FP8DS_BARRIER();
+            __builtin_amdgcn_sched_barrier(0);
+            i32x8 fa[NB], fb[8];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) fa[i] = frag(sa0 + i * 32 * kStep, oa, oa ^ 16);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) fb[q] = frag(b + q * 16 * kStep, ob, ob ^ 16);
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+            FP8DS_WAIT_LGKM();
+            FP8DS_BARRIER();
+            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t out_a = outside(t, j + 1, ld.k), out_b = outside(t, j + 2, ld.k);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) load(rs_a, sa0, i, (ld.va | out_a) + i * 32 * lda, j + 1);
+            __builtin_amdgcn_sched_barrier(0x7cf);           // loads into LDS stay in this order
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out_b) + row_b(i) * ldb, j + 2);
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb[q], acc[i][q], FA, FB, 0, 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < 8 + NB; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x008, NB > 1 ? 2 : 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int j = -(nk & 1);
+        do {
+            if (j >= 0) step(j, sb0);
+            step(j + 1, sb1);
+            j += 2;
+        } while (j < nk);
+        FP8DS_WAIT_ALL();                                    // every load into the slots has landed
+        FP8DS_BARRIER();
+        __builtin_amdgcn_sched_barrier(0);
+        more = tiles(next);
+        if (more) first_loads(next);
+        this->template store<NB>(t, acc);
+        return 0;
+    }
+
+};
+
+template <int FA, int FB, int OUT, class Tiles>
+__device__ __forceinline__ void run_wide(const Grouped &g, Tiles &&tiles) {
+    __shared__ __align__(16) uint8_t sa0[256 * kStep];
+    __shared__ __align__(16) uint8_t sa1[256 * kStep];
+    __shared__ __align__(16) uint8_t sb0[256 * kStep];
+    __shared__ __align__(16) uint8_t sb1[256 * kStep];
+    __shared__ __align__(16) uint8_t sb2[256 * kStep];
     Tile t, next;
     if (!tiles(t)) return;
-    const Worker<FA, FB, OUT> w(g, sa0, sa1, sb0, sb1, sb2);
+    const Wide<FA, FB, OUT> w(g, sa0, sa1, sb0, sb1, sb2);
+    w.first_loads(t);
+    int stores = 0;
+    for (bool more = true; more; t = next) {
+        const int nb = (t.rows + 31) / 32;
+        if (nb <= 2) stores = w.template run<2>(t, tiles, next, more, stores);
+        else if (nb <= 4) stores = w.template run<4>(t, tiles, next, more, stores);
+        else if (nb == 5) stores = w.template run<5>(t, tiles, next, more, stores);
+        else if (nb == 6) stores = w.template run<6>(t, tiles, next, more, stores);
+        else if (nb == 7) stores = w.template run<7>(t, tiles, next, more, stores);
+        else stores = w.template run<8>(t, tiles, next, more, stores);
+    }
+}
+
+template <int FA, int FB, int OUT, class Tiles>
+__device__ __forceinline__ void run_paired(const Grouped &g, Tiles &&tiles) {
+    __shared__ __align__(16) uint8_t sa0[128 * kStep];
+    __shared__ __align__(16) uint8_t sb0[256 * kStep];
+    __shared__ __align__(16) uint8_t sb1[256 * kStep];
+    Tile t, next;
+    if (!tiles(t)) return;
+    const Paired<FA, FB, OUT> w(g, sa0, sb0, sb1);
     w.first_loads(t);
     for (bool more = true; more; t = next) {
-        more = tiles(next);
         const int nb = (t.rows + 31) / 32;
-        if (FINE && nb <= 2) w.template run<2>(t, next, more);
-        else if (nb <= 4) w.template run<4>(t, next, more);
-        else if (FINE && nb == 5) w.template run<5>(t, next, more);
-        else if (FINE && nb == 6) w.template run<6>(t, next, more);
-        else if (FINE && nb == 7) w.template run<7>(t, next, more);
-        else w.template run<8>(t, next, more);
+        if (nb == 1) w.template run<1>(t, tiles, next, more, 0);
+        else if (nb == 2) w.template run<2>(t, tiles, next, more, 0);
+        else if (nb == 3) w.template run<3>(t, tiles, next, more, 0);
+        else w.template run<4>(t, tiles, next, more, 0);
     }
 }
 
 }  // namespace
 
 template <int FA, int FB, int OUT>
-__global__ __launch_bounds__(kThreads, 1) void k_grouped_gemm(const Grouped g, int tiles_n) {
-    run_tiles<FA, FB, OUT, true>(g, RowTiles<OUT>(g, tiles_n));
+__global__ __launch_bounds__(kThreads, 1) void k_grouped_gemm_wide(const Grouped g, int tiles_n) {
+    run_wide<FA, FB, OUT>(g, RowTiles<OUT, kWide>(g, tiles_n));
 }
-
 template <int FA, int FB, int OUT>
-__global__ __launch_bounds__(kThreads, 1) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
-    run_tiles<FA, FB, OUT, false>(g, ExpertTiles<OUT>(g, tiles_m, tiles_n));
+__global__ __launch_bounds__(kThreads, 2) void k_grouped_gemm_paired(const Grouped g, int tiles_n) {
+    run_paired<FA, FB, OUT>(g, RowTiles<OUT, kPaired>(g, tiles_n));
+}
+template <int FA, int FB, int OUT>
+__global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
+    run_paired<FA, FB, OUT>(g, ExpertTiles<OUT>(g, tiles_m, tiles_n));
 }
 
 #define FP8DS_GROUPED_SWITCH(CALL)                                                                         \
@@ -475,31 +681,45 @@ __global__ __launch_bounds__(kThreads, 1) void k_grouped_wgrad(const Grouped g, 
     }
 
 // The largest number of row tiles: every expert with rows adds at most one partial tile.
-static int64_t most_row_tiles(int64_t cap, int64_t E) {
+static int64_t most_row_tiles(int64_t cap, int64_t E, int64_t tm) {
     const int64_t used = (cap + 15) / 16;
-    return cap / kTm + (E < used ? E : used);
+    return cap / tm + (E < used ? E : used);
 }
-// tiles are numbered in 31 bits
-bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) { return most_row_tiles(cap, E) <= INT_MAX / ((N + kTn) / kTn); }
+// Tiles are numbered in 31 bits, positions up to a round of blocks past the last.
+bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) {
+    return most_row_tiles(cap, E, kPaired) <= (INT_MAX - (1 << 16)) / ((N + kTn) / kTn);
+}
 bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K) {
-    const int64_t per = ((N + kTm) / kTm) * ((K + kTn) / kTn);   // at most 2^47
-    return E <= INT_MAX / per;
+    const int64_t per = ((N + kPaired) / kPaired) * ((K + kTn) / kTn) + kXcds;   // at most 2^48
+    return E <= (INT_MAX - (1 << 16)) / per;
 }
-// One block per CU, fewer for fewer tiles, a multiple of the XCDs.
-static unsigned blocks_for(int64_t tiles) { return (unsigned)((tiles < kCUs ? tiles + kXcds - 1 : kCUs) / kXcds * kXcds); }
+// One or two blocks per CU, fewer for fewer tiles, a multiple of the XCDs.
+static unsigned blocks_for(int64_t tiles, int64_t most) {
+    return (unsigned)((tiles < most ? tiles + kXcds - 1 : most) / kXcds * kXcds);
+}
+// Wide tiles from 192 rows for each expert on and two rounds of them on all CUs.
+static bool wide_preferred(const Grouped &g, int tiles_n) {
+    return g.cap / g.E >= 192 && (int64_t)g.cap / kWide * tiles_n >= 2 * kCUs;
+}
 
 hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
     const int tiles_n = (g.N + kTn - 1) / kTn;
-    const unsigned grid = blocks_for(most_row_tiles(g.cap, g.E) * tiles_n);
-#define FP8DS_GG(FA_, FB_, O_) k_grouped_gemm<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n)
+    const bool wide = wide_preferred(g, tiles_n);
+    const unsigned grid = wide ? blocks_for(most_row_tiles(g.cap, g.E, kWide) * tiles_n, kCUs)
+                               : blocks_for(most_row_tiles(g.cap, g.E, kPaired) * tiles_n, 2 * kCUs);
+#define FP8DS_GG(FA_, FB_, O_)                                                          \
+    do {                                                                                \
+        if (wide) k_grouped_gemm_wide<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n); \
+        else k_grouped_gemm_paired<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n);    \
+    } while (0)
     FP8DS_GROUPED_SWITCH(FP8DS_GG)
 #undef FP8DS_GG
     return hipGetLastError();
 }
 
 hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
-    const int tiles_m = (g.N + kTm - 1) / kTm, tiles_n = (g.K + kTn - 1) / kTn;
-    const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n);
+    const int tiles_m = (g.N + kPaired - 1) / kPaired, tiles_n = (g.K + kTn - 1) / kTn;
+    const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n, 2 * kCUs);
 #define FP8DS_GW(FA_, FB_, O_) k_grouped_wgrad<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n)
     FP8DS_GROUPED_SWITCH(FP8DS_GW)
 #undef FP8DS_GW
