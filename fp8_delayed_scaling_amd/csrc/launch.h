@@ -67,10 +67,11 @@ struct NormBwd {
     int width;
     // set by the launcher: how the rows are shared out, and the workspace
     int64_t rows_per_gate, unit_rows, units_per_gate, units;
-    float *col_part[4], *gate_part;
+    bool gated;              // more gates than blocks: the partials hold the gate already, dgate is finished
+    float *part[4];
 };
 constexpr int64_t kNormMaxWidth = 16384;
-constexpr int64_t kNormMaxGates = 65531;   // with the four weight and bias sums, one grid row each
+constexpr int64_t kNormMaxGates = 65531;   // with the weights' and biases' sums, one grid row each
 size_t norm_workspace_bytes(int64_t rows, int64_t width, int64_t n_gates);
 hipError_t launch_norm_fwd(const NormFwd &a, int layer, int fmt, hipStream_t st);
 hipError_t launch_norm_bwd(NormBwd a, int layer, int64_t n_gates, void *ws, hipStream_t st);
