@@ -128,6 +128,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(s) -> Optional[int]:
     if s is None:
+        if torch.cuda.is_initialized():      # the current stream's handle, without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -139,16 +141,30 @@ def _check(status: int):
         raise Fp8dsError(status, fp8ds_status_string(status))
 
 
-_tls = threading.local()   # .rec: the list prepare() records into, on this thread only
+class _Tls(threading.local):
+    rec = None             # the list prepare() records into, on this thread only
+
+
+_tls = _Tls()
+_HOST = object()           # stands for the pointer of a tensor that is not on the GPU (see _arg)
 
 
 def _invoke(name: str, *cargs):
     """Call entry point ``name`` with marshalled arguments, or hand them to prepare()."""
-    rec = getattr(_tls, "rec", None)
+    rec = _tls.rec
     if rec is not None:
+        if _HOST in cargs:
+            raise ValueError("tensor arguments must live on the GPU")
         rec.append((name, cargs))
         return
-    _check(getattr(lib(), name)(*cargs))
+    try:
+        status = getattr(_lib or lib(), name)(*cargs)
+    except ctypes.ArgumentError:
+        if _HOST in cargs:
+            raise ValueError("tensor arguments must live on the GPU") from None
+        raise
+    if status != 0:
+        _check(status)
 
 
 class Prepared:
@@ -213,6 +229,29 @@ def _want(t, dtypes, name, contiguous=True, shape=None, min_numel=None, required
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError(f"{name} must hold at least {min_numel} elements, got {t.numel()}")
+
+
+def _arg(t, dtypes, shape, name, required=False):
+    """Check a dense tensor argument of exactly ``shape`` as _want does, and return its pointer.  One
+    that is not on the GPU gives _HOST, which _invoke refuses after all arguments' own checks."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if t.__class__ is int:
+        return t
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _want(t, dtypes, name, shape=shape)
+    return t.data_ptr() if t.is_cuda else _HOST
+
+
+def _some(t, dtypes, least, name):
+    """As _arg, for a dense tensor (or None) of any shape with at least ``least`` elements."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < least:
+        _want(t, dtypes, name, min_numel=least)
+    return t.data_ptr() if t.is_cuda else _HOST
 
 
 def _workspace_bytes(workspace) -> int:
@@ -431,20 +470,14 @@ def fp8_linear_bwd(dy, K, dy_scale, dy_amax, dy8, dy8_t, dy_scale_inv, dbias, wo
 
 # ------------------------------------------------------- the operators around the linear layer
 
-def _norm_shapes(M, H, w_post, b_post, gate, w_pre):
-    _want(w_post, _BF16, "w_post", shape=(H,))
-    _want(b_post, _BF16, "b_post", shape=(H,))
-    _want(w_pre, _BF16, "w_pre", shape=(H,))
+def _gate_arg(gate, M, H):
+    """Pointer and number of the gates."""
     if gate is None:
-        return 0
+        return None, 0
     _want(gate, _BF16, "gate")
     if gate.dim() != 2 or gate.shape[1] != H or gate.shape[0] < 1 or M % gate.shape[0] != 0:
         raise ValueError(f"gate must be [G, {H}] with G dividing the {M} rows, got {tuple(gate.shape)}")
-    return gate.shape[0]
-
-
-def _stats_numel(kind, M):
-    return 2 * M if int(kind) == NORM_LAYER else M
+    return gate.data_ptr() if gate.is_cuda else _HOST, gate.shape[0]
 
 
 def fp8_norm_residual_fwd(block_out, w_post, b_post, gate, resid, alpha, x, post_stats, w_pre, b_pre, pre_stats, h,
@@ -456,19 +489,18 @@ def fp8_norm_residual_fwd(block_out, w_post, b_post, gate, resid, alpha, x, post
     ``post_stats`` / ``pre_stats``: float32, rows values (RMS) or 2 * rows (layer: 1 / deviation, then mean)."""
     ref, name = (resid, "resid") if block_out is None else (block_out, "block_out")
     _want(ref, _BF16, name, required=True)
-    M, H = ref.shape
-    _want(resid, _BF16, "resid", shape=(M, H))
-    _want(x, _BF16, "x", shape=(M, H), required=block_out is not None)
-    G = _norm_shapes(M, H, w_post, b_post, gate, w_pre)
-    _want(b_pre, _BF16, "b_pre", shape=(H,))
-    _want(post_stats, _F32, "post_stats", min_numel=_stats_numel(kind, M))
-    _want(pre_stats, _F32, "pre_stats", min_numel=_stats_numel(kind, M))
-    _want(h, _BF16, "h", shape=(M, H))
-    _want(h8, _U8, "h8", shape=(M, H))
-    _scalars(scale=scale, scale_inv_out=scale_inv_out, amax_slot=amax_slot)
-    _invoke("fp8_norm_residual_fwd", _ptr(block_out), _ptr(w_post), _ptr(b_post), _ptr(gate), G, _ptr(resid),
-            float(alpha), _ptr(x), _ptr(post_stats), _ptr(w_pre), _ptr(b_pre), _ptr(pre_stats), _ptr(h), _ptr(h8),
-            _ptr(scale), int(fmt), _ptr(scale_inv_out), _ptr(amax_slot), int(kind), float(eps), M, H, _stream(stream))
+    shape = ref.shape
+    M, H = shape
+    row = (H,)
+    stats = 2 * M if kind == NORM_LAYER else M
+    p_gate, G = _gate_arg(gate, M, H)
+    _invoke("fp8_norm_residual_fwd", _arg(block_out, _BF16, shape, "block_out"), _arg(w_post, _BF16, row, "w_post"),
+            _arg(b_post, _BF16, row, "b_post"), p_gate, G, _arg(resid, _BF16, shape, "resid"), float(alpha),
+            _arg(x, _BF16, shape, "x", block_out is not None), _some(post_stats, _F32, stats, "post_stats"),
+            _arg(w_pre, _BF16, row, "w_pre"), _arg(b_pre, _BF16, row, "b_pre"), _some(pre_stats, _F32, stats, "pre_stats"),
+            _arg(h, _BF16, shape, "h"), _arg(h8, _U8, shape, "h8"), _some(scale, _F32, 1, "scale"), int(fmt),
+            _some(scale_inv_out, _F32, 1, "scale_inv_out"), _some(amax_slot, _F32, 1, "amax_slot"), int(kind), float(eps),
+            M, H, _stream(stream))
 
 
 def fp8_norm_residual_workspace_bytes(rows: int, width: int, n_gates: int) -> int:
@@ -481,20 +513,19 @@ def fp8_norm_residual_bwd(dh, dx, block_out, w_post, b_post, gate, alpha, x, pos
     statistics that the forward wrote.  ``workspace``: ``fp8_norm_residual_workspace_bytes(rows, width, gates)``."""
     ref = dh if dh is not None else dx
     _want(ref, _BF16, "dh" if dh is not None else "dx", required=True)
-    M, H = ref.shape
-    for t, nm in ((dx, "dx"), (block_out, "block_out"), (x, "x"), (d_block, "d_block"), (d_resid, "d_resid")):
-        _want(t, _BF16, nm, shape=(M, H))
-    G = _norm_shapes(M, H, w_post, b_post, gate, w_pre)
-    _want(post_stats, _F32, "post_stats", min_numel=_stats_numel(kind, M))
-    _want(pre_stats, _F32, "pre_stats", min_numel=_stats_numel(kind, M))
-    for t, nm in ((dw_post, "dw_post"), (db_post, "db_post"), (dw_pre, "dw_pre"), (db_pre, "db_pre")):
-        _want(t, _F32, nm, shape=(H,))
-    _want(dgate, _F32, "dgate", shape=(max(G, 1), H))
+    shape = ref.shape
+    M, H = shape
+    row = (H,)
+    stats = 2 * M if kind == NORM_LAYER else M
+    p_gate, G = _gate_arg(gate, M, H)
     ws_bytes = _workspace_bytes(workspace)
-    _invoke("fp8_norm_residual_bwd", _ptr(dh), _ptr(dx), _ptr(block_out), _ptr(w_post), _ptr(b_post), _ptr(gate), G,
-            float(alpha), _ptr(x), _ptr(post_stats), _ptr(w_pre), _ptr(pre_stats), _ptr(d_block), _ptr(d_resid),
-            _ptr(dw_post), _ptr(db_post), _ptr(dgate), _ptr(dw_pre), _ptr(db_pre), _ptr(workspace), ws_bytes,
-            int(kind), M, H, _stream(stream))
+    _invoke("fp8_norm_residual_bwd", _arg(dh, _BF16, shape, "dh"), _arg(dx, _BF16, shape, "dx"),
+            _arg(block_out, _BF16, shape, "block_out"), _arg(w_post, _BF16, row, "w_post"), _arg(b_post, _BF16, row, "b_post"),
+            p_gate, G, float(alpha), _arg(x, _BF16, shape, "x"), _some(post_stats, _F32, stats, "post_stats"),
+            _arg(w_pre, _BF16, row, "w_pre"), _some(pre_stats, _F32, stats, "pre_stats"), _arg(d_block, _BF16, shape, "d_block"),
+            _arg(d_resid, _BF16, shape, "d_resid"), _arg(dw_post, _F32, row, "dw_post"), _arg(db_post, _F32, row, "db_post"),
+            _arg(dgate, _F32, (max(G, 1), H), "dgate"), _arg(dw_pre, _F32, row, "dw_pre"), _arg(db_pre, _F32, row, "db_pre"),
+            _ptr(workspace), ws_bytes, int(kind), M, H, _stream(stream))
 
 
 def fp8_moe_capacity(T: int, top: int, E: int, align: int = 16) -> int:
@@ -516,71 +547,69 @@ def fp8_moe_plan(experts, E: int, align: int, offsets, src, slot, workspace=None
     _want(experts, _I32, "experts", required=True)
     if experts.dim() != 2:
         raise ValueError("experts must be [T, top]")
-    T, k = experts.shape
-    _want(offsets, _I32, "offsets", shape=(int(E) + 1,), required=True)
+    shape = experts.shape
+    T, k = shape
     _want(src, _I32, "src", required=True)
-    _want(slot, _I32, "slot", shape=(T, k), required=True)
     ws_bytes = _workspace_bytes(workspace)
-    _invoke("fp8_moe_plan", _ptr(experts), T, k, int(E), int(align), src.numel(), _ptr(offsets), _ptr(src), _ptr(slot),
-            _ptr(workspace), ws_bytes, _stream(stream))
+    _invoke("fp8_moe_plan", _arg(experts, _I32, shape, "experts"), T, k, int(E), int(align), src.numel(),
+            _arg(offsets, _I32, (int(E) + 1,), "offsets", True), _arg(src, _I32, src.shape, "src"),
+            _arg(slot, _I32, shape, "slot", True), _ptr(workspace), ws_bytes, _stream(stream))
 
 
-def _sort_shapes(x, dtypes, src, top, weights, out, out_dtypes, out_t):
+def _sort_args(x, dtypes, src, top, weights, out, out_dtypes, out_t):
+    """Sizes T, width and capacity, and the five pointers."""
     _want(x, dtypes, "x", required=True)
+    _want(src, _I32, "src", required=True)
     if x.dim() != 2:
         raise ValueError("x must be [T, width]")
     T, H = x.shape
-    _want(src, _I32, "src", required=True)
     cap = src.numel()
-    _want(weights, _F32, "weights", shape=(T, int(top)))
-    _want(out, out_dtypes, "out", shape=(cap, H), required=True)
-    _want(out_t, _U8, "out_t", shape=(H, cap))
-    return T, H, cap
+    return (T, H, cap, _arg(x, dtypes, x.shape, "x"), _arg(src, _I32, src.shape, "src"),
+            _arg(weights, _F32, (T, int(top)), "weights"), _arg(out, out_dtypes, (cap, H), "out", True),
+            _arg(out_t, _U8, (H, cap), "out_t"))
 
 
 def fp8_moe_sort_cast(x, src, top: int, weights, scale, fmt, out, out_t=None, scale_inv_out=None, amax_slot=None,
                       stream=None):
     """Rows of bfloat16 ``x`` in expert order, times ``weights`` (or None), as FP8 codes and their transpose."""
-    T, H, cap = _sort_shapes(x, _BF16, src, top, weights, out, _U8, out_t)
-    _scalars(scale=scale, scale_inv_out=scale_inv_out, amax_slot=amax_slot)
-    _invoke("fp8_moe_sort_cast", _ptr(x), T, _ptr(src), cap, int(top), _ptr(weights), _ptr(scale), int(fmt), _ptr(out),
-            _ptr(out_t), _ptr(scale_inv_out), _ptr(amax_slot), H, _stream(stream))
+    T, H, cap, p_x, p_src, p_w, p_out, p_out_t = _sort_args(x, _BF16, src, top, weights, out, _U8, out_t)
+    _invoke("fp8_moe_sort_cast", p_x, T, p_src, cap, int(top), p_w, _some(scale, _F32, 1, "scale"), int(fmt), p_out, p_out_t,
+            _some(scale_inv_out, _F32, 1, "scale_inv_out"), _some(amax_slot, _F32, 1, "amax_slot"), H, _stream(stream))
 
 
 def fp8_moe_sort_codes(x8, src, top: int, out, out_t=None, stream=None):
     """Rows of FP8 codes in expert order, and their transpose (codes copied; padding rows are zero)."""
-    T, H, cap = _sort_shapes(x8, _U8, src, top, None, out, _U8, out_t)
-    _invoke("fp8_moe_sort_codes", _ptr(x8), T, _ptr(src), cap, int(top), _ptr(out), _ptr(out_t), H, _stream(stream))
+    T, H, cap, p_x, p_src, _, p_out, p_out_t = _sort_args(x8, _U8, src, top, None, out, _U8, out_t)
+    _invoke("fp8_moe_sort_codes", p_x, T, p_src, cap, int(top), p_out, p_out_t, H, _stream(stream))
 
 
 def fp8_moe_sort_bf16(x, src, top: int, weights, out, stream=None):
     """Rows of bfloat16 ``x`` in expert order, times ``weights`` (or None)."""
-    T, H, cap = _sort_shapes(x, _BF16, src, top, weights, out, _BF16, None)
-    _invoke("fp8_moe_sort_bf16", _ptr(x), T, _ptr(src), cap, int(top), _ptr(weights), _ptr(out), H, _stream(stream))
+    T, H, cap, p_x, p_src, p_w, p_out, _ = _sort_args(x, _BF16, src, top, weights, out, _BF16, None)
+    _invoke("fp8_moe_sort_bf16", p_x, T, p_src, cap, int(top), p_w, p_out, H, _stream(stream))
 
 
-def _back_shapes(ys, slot):
+def _back_args(ys, slot):
+    """Sizes and the two pointers."""
     _want(ys, _BF16, "ys", required=True)
     _want(slot, _I32, "slot", required=True)
     if ys.dim() != 2 or slot.dim() != 2:
         raise ValueError("ys must be [capacity, width] and slot [T, top]")
-    return (*ys.shape, *slot.shape)
+    return (*ys.shape, *slot.shape, _arg(ys, _BF16, ys.shape, "ys"), _arg(slot, _I32, slot.shape, "slot"))
 
 
 def fp8_moe_combine(ys, slot, weights, y, stream=None):
     """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights None: 1)."""
-    cap, H, T, k = _back_shapes(ys, slot)
-    _want(weights, _F32, "weights", shape=(T, k))
-    _want(y, _BF16, "y", shape=(T, H), required=True)
-    _invoke("fp8_moe_combine", _ptr(ys), cap, _ptr(slot), _ptr(weights), T, k, _ptr(y), H, _stream(stream))
+    cap, H, T, k, p_ys, p_slot = _back_args(ys, slot)
+    _invoke("fp8_moe_combine", p_ys, cap, p_slot, _arg(weights, _F32, (T, k), "weights"), T, k, _arg(y, _BF16, (T, H), "y", True),
+            H, _stream(stream))
 
 
 def fp8_moe_weight_grad(dy, ys, slot, dweights, stream=None):
     """dweights[t, j] = <dy[t], ys[slot[t, j]]>, 0 for a dropped choice."""
-    cap, H, T, k = _back_shapes(ys, slot)
-    _want(dy, _BF16, "dy", shape=(T, H), required=True)
-    _want(dweights, _F32, "dweights", shape=(T, k), required=True)
-    _invoke("fp8_moe_weight_grad", _ptr(dy), _ptr(ys), cap, _ptr(slot), T, k, _ptr(dweights), H, _stream(stream))
+    cap, H, T, k, p_ys, p_slot = _back_args(ys, slot)
+    _invoke("fp8_moe_weight_grad", _arg(dy, _BF16, (T, H), "dy", True), p_ys, cap, p_slot, T, k,
+            _arg(dweights, _F32, (T, k), "dweights", True), H, _stream(stream))
 
 
 def _rows_dense(**kw):
@@ -598,14 +627,14 @@ def fp8_grouped_gemm(A, fa, a_scale_inv, B, fb, b_scale_inv, offsets, D, stream=
         raise ValueError("A [cap, K] and B [E, N, K] must share K")
     cap, K = A.shape
     E, N = B.shape[:2]
-    _want(offsets, _I32, "offsets", shape=(E + 1,), required=True)
-    if tuple(D.shape) != (cap, N):
+    p_off = _arg(offsets, _I32, (E + 1,), "offsets", True)
+    if D.shape != (cap, N):
         raise ValueError(f"D must be [{cap}, {N}]")
     _rows_dense(A=A, B=B, D=D)
     dtype = _out_dtype(D)
-    _scalars(a_scale_inv=a_scale_inv, b_scale_inv=b_scale_inv)
-    _invoke("fp8_grouped_gemm", _ptr(A), int(fa), _ptr(a_scale_inv), A.stride(0), _ptr(B), int(fb), _ptr(b_scale_inv),
-            B.stride(1), B.stride(0), _ptr(offsets), E, _ptr(D), D.stride(0), dtype, cap, N, K, _stream(stream))
+    _invoke("fp8_grouped_gemm", _ptr(A), int(fa), _some(a_scale_inv, _F32, 1, "a_scale_inv"), A.stride(0), _ptr(B), int(fb),
+            _some(b_scale_inv, _F32, 1, "b_scale_inv"), B.stride(1), B.stride(0), p_off, E, _ptr(D), D.stride(0), dtype, cap, N,
+            K, _stream(stream))
 
 
 def fp8_grouped_wgrad(At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, stream=None):
@@ -619,8 +648,9 @@ def fp8_grouped_wgrad(At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, str
     K = Bt.shape[0]
     _want(offsets, _I32, "offsets", required=True)
     E = offsets.numel() - 1
-    _want(dW, (torch.bfloat16, torch.float32), "dW", shape=(E, N, K), required=True)
+    _want(dW, (torch.bfloat16, torch.float32), "dW", required=True)
+    p_dw = _arg(dW, (torch.bfloat16, torch.float32), (E, N, K), "dW")
     _rows_dense(At=At, Bt=Bt)
-    _scalars(a_scale_inv=a_scale_inv, b_scale_inv=b_scale_inv)
-    _invoke("fp8_grouped_wgrad", _ptr(At), int(fa), _ptr(a_scale_inv), At.stride(0), _ptr(Bt), int(fb),
-            _ptr(b_scale_inv), Bt.stride(0), _ptr(offsets), E, _ptr(dW), _out_dtype(dW), cap, N, K, _stream(stream))
+    _invoke("fp8_grouped_wgrad", _ptr(At), int(fa), _some(a_scale_inv, _F32, 1, "a_scale_inv"), At.stride(0), _ptr(Bt), int(fb),
+            _some(b_scale_inv, _F32, 1, "b_scale_inv"), Bt.stride(0), _ptr(offsets), E, p_dw, _out_dtype(dW), cap, N, K,
+            _stream(stream))
