@@ -37,7 +37,7 @@ constexpr int kThreads = 256;
 constexpr int kCUs = 256;
 constexpr int kXcds = 8;                     // blocks are dealt round-robin to the XCDs
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every tile's extent (below 2^31 bytes)
-constexpr int kStreaming = 2;                // nontemporal: outputs leave L2 first (weight gradient 595 -> 469 us)
+constexpr int kStreaming = 2;                // nontemporal
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
 
 // vmcnt-only wait, and a workgroup barrier without a fence (a fenced one would wait for every load
@@ -60,13 +60,13 @@ __device__ __forceinline__ int divide(int n, int d) {
     asm volatile("" : "+s"(d));
     return (int)((uint32_t)n / (uint32_t)d);
 }
+__device__ __forceinline__ int divide_any(int n, int d) { return (int)((uint32_t)n / (uint32_t)d); }
 __device__ __forceinline__ int modulo(int n, int d) { return n - divide(n, d) * d; }
 
-// Rows of each of the tiles of at most TM rows that share n rows: ceil(n / TM) tiles, the same
-// multiple of 32 each (the last may have fewer, never none).
-template <int TM>
-__host__ __device__ constexpr int tile_rows(int n) {
-    const int tiles = (n + TM - 1) / TM, blocks = (n + 31) / 32;
+// Rows of each of the tiles of at most tm rows (32, 64, 128 or 256) that share n rows: ceil(n / tm)
+// tiles, the same multiple of 32 each (the last may have fewer, never none).
+__host__ __device__ inline int tile_rows(int n, int tm) {
+    const int tiles = (n + tm - 1) / tm, blocks = (n + 31) / 32;
     return tiles > 0 ? (blocks + tiles - 1) / tiles * 32 : 0;
 }
 
@@ -88,7 +88,7 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// The forward's tiles, an expert's ceil(rows / TM) * tiles_n with its row tiles running fastest.
+// The forward's tiles, an expert's ceil(rows / tile height) * tiles_n with its row tiles running fastest.
 // Among 64 experts, tall tiles come first (in every expert all tiles but the last have one height).
 // The tiles are taken in rounds, runs of kRun dealt to the XCDs forwards and backwards in turn, a
 // run to blocks of one XCD: they share B's rows, which come from HBM once, and A's.  Every block so
@@ -96,16 +96,18 @@ __device__ __forceinline__ int wave_scan(int v) {
 // first: tall tiles, bound by the products, run beside low ones, bound by B's bytes.  (Unevenly
 // routed forward of 64 experts, half of which have under 1 % of the rows: in the experts' order
 // 330 us, tall tiles first 286, this way 275; evenly routed 230.)
-template <int OUT, int TM>
+template <int OUT>
 struct RowTiles {
     static constexpr int kRun = 8;
     const Grouped &g;
-    int tiles_n, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
-    __device__ __forceinline__ RowTiles(const Grouped &g_, int tiles_n_) : g(g_), tiles_n(tiles_n_), total(0), round(0), e0(0), before(0) {
+    int log2_tm, tiles_n, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
+    __device__ __forceinline__ RowTiles(const Grouped &g_, int log2_tm_, int tiles_n_)
+        : g(g_), log2_tm(log2_tm_), tiles_n(tiles_n_), total(0), round(0), e0(0), before(0) {
         int lo, hi;
         for (int e = 0; e < g.E; e += 64) total += count(e, lo, hi);
         deals = (total + kRun * kXcds - 1) / (kRun * kXcds);
     }
+    __device__ __forceinline__ int tiles_of(int n) const { return (n + (1 << log2_tm) - 1) >> log2_tm; }
     // tiles of the experts e .. e + 63, and the rows of the lane's among them
     __device__ __forceinline__ int count(int e, int &lo, int &hi) const {
         const int i = e + (threadIdx.x & 63);
@@ -114,7 +116,7 @@ struct RowTiles {
             lo = min(max(g.offsets[i], 0), g.cap) & ~15;
             hi = max(lo, min(max(g.offsets[i + 1], 0), g.cap) & ~15);
         }
-        return uniform(__builtin_amdgcn_readlane(wave_scan((hi - lo + TM - 1) / TM), 63)) * tiles_n;
+        return uniform(__builtin_amdgcn_readlane(wave_scan(tiles_of(hi - lo)), 63)) * tiles_n;
     }
     // the block's next tile; false when there is none
     __device__ __forceinline__ bool operator()(Tile &t) {
@@ -140,14 +142,16 @@ struct RowTiles {
             e0 += 64;
             n = count(e0, lo, hi);
         }
-        int at = tile - before, h = TM / 32;
-        const int mine = tile_rows<TM>(hi - lo) / 32;
+        int at = tile - before, h = 1 << (log2_tm - 5);
+        const int blocks = (hi - lo + 31) >> 5, n_tiles = tiles_of(hi - lo);
+        int mine = 0;                      // the lane's expert's height: its 32-row blocks shared by its tiles
+        if (n_tiles > 0) mine = divide_any(blocks + n_tiles - 1, n_tiles);
         for (; h > 1; --h) {
-            const int of_h = uniform(__builtin_amdgcn_readlane(wave_scan(mine == h ? (hi - lo + TM - 1) / TM : 0), 63)) * tiles_n;
+            const int of_h = uniform(__builtin_amdgcn_readlane(wave_scan(mine == h ? tiles_of(hi - lo) : 0), 63)) * tiles_n;
             if (at < of_h) break;
             at -= of_h;
         }
-        const int tiles = mine == h ? (hi - lo + TM - 1) / TM : 0, incl = wave_scan(tiles);
+        const int tiles = mine == h ? tiles_of(hi - lo) : 0, incl = wave_scan(tiles);
         const int k = __builtin_ctzll(__ballot(incl * tiles_n > at)), e = e0 + k;
         const int first = __builtin_amdgcn_readlane(lo, k), end = __builtin_amdgcn_readlane(hi, k);
         const int row_tiles = __builtin_amdgcn_readlane(tiles, k), in = at - __builtin_amdgcn_readlane(incl - tiles, k) * tiles_n;
@@ -179,7 +183,7 @@ struct ExpertTiles {
     int tiles_m, tiles_n, h, per, chunk, slots, groups, next;      // next: round, or expert with groups
     int work[4];
     __device__ __forceinline__ ExpertTiles(const Grouped &g_, int tiles_m_, int tiles_n_)
-        : g(g_), tiles_m(tiles_m_), tiles_n(tiles_n_), h(tile_rows<kPaired>(g_.N)), next(0) {
+        : g(g_), tiles_m(tiles_m_), tiles_n(tiles_n_), h(tile_rows(g_.N, kPaired)), next(0) {
         per = tiles_m * tiles_n;
         chunk = (per + kXcds - 1) / kXcds;
         slots = gridDim.x / kXcds;
@@ -248,9 +252,10 @@ struct Work {
     int64_t ldd;
     float sa, sb;
     int lda, ldb, wave, wm, wn;
+    bool streaming;
 
     explicit __device__ __forceinline__ Work(const Grouped &gr)
-        : ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb) {
+        : ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb), streaming(gr.streaming) {
         wave = uniform((int)threadIdx.x >> 6);
         wm = wave >> 1; wn = wave & 1;
     }
@@ -321,7 +326,8 @@ struct Work {
                     }
                     if (vec) {
                         const uint32_t off = col0 + p * 64 < t.cols ? here + (uint32_t)(p * 64 * kEsz) : kOutside;
-                        __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, kStreaming);
+                        if (streaming) __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, kStreaming);
+                        else __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, 0);
                     } else {
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) {
@@ -657,11 +663,11 @@ __device__ __forceinline__ void run_paired(const Grouped &g, Tiles &&tiles) {
 
 template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(kThreads, 1) void k_grouped_gemm_wide(const Grouped g, int tiles_n) {
-    run_wide<FA, FB, OUT>(g, RowTiles<OUT, kWide>(g, tiles_n));
+    run_wide<FA, FB, OUT>(g, RowTiles<OUT>(g, 8, tiles_n));
 }
 template <int FA, int FB, int OUT>
-__global__ __launch_bounds__(kThreads, 2) void k_grouped_gemm_paired(const Grouped g, int tiles_n) {
-    run_paired<FA, FB, OUT>(g, RowTiles<OUT, kPaired>(g, tiles_n));
+__global__ __launch_bounds__(kThreads, 2) void k_grouped_gemm_paired(const Grouped g, int log2_tm, int tiles_n) {
+    run_paired<FA, FB, OUT>(g, RowTiles<OUT>(g, log2_tm, tiles_n));
 }
 template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
@@ -687,7 +693,7 @@ static int64_t most_row_tiles(int64_t cap, int64_t E, int64_t tm) {
 }
 // Tiles are numbered in 31 bits, positions up to a round of blocks past the last.
 bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) {
-    return most_row_tiles(cap, E, kPaired) <= (INT_MAX - (1 << 16)) / ((N + kTn) / kTn);
+    return most_row_tiles(cap, E, 32) <= (INT_MAX - (1 << 16)) / ((N + kTn) / kTn);
 }
 bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K) {
     const int64_t per = ((N + kPaired) / kPaired) * ((K + kTn) / kTn) + kXcds;   // at most 2^48
@@ -702,22 +708,41 @@ static bool wide_preferred(const Grouped &g, int tiles_n) {
     return g.cap / g.E >= 192 && (int64_t)g.cap / kWide * tiles_n >= 2 * kCUs;
 }
 
-hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
+// Paired tiles are at most 128 rows high, lower where fewer than one such tile for each CU would
+// come of even routing: more blocks then share the contraction's steps, which take about a
+// microsecond each (4 experts, 2664 rows, [240, 3392]: 49 us at 128 rows, 33 at 32).
+static int paired_log2(const Grouped &g, int tiles_n) {
+    int l = 7;
+    while (l > 5 && ((int64_t)g.cap >> l) * tiles_n < kCUs) --l;
+    return l;
+}
+
+// Outputs that no cache holds leave L2 first (nontemporal stores): 64 experts' weight gradient [2048,
+// 4096] of 512 rows each, 1.07 GB, 542 us without and 405 with; 270 MB of short rows that do not
+// fill their cache lines (64 x [608, 3472], 16 rows each) 60 and 97, 4 MB 19 and 22.
+static bool streams(int64_t elements, int out_dtype) {
+    return elements * (out_dtype == FP8DS_OUT_BF16 ? 2 : 4) >= (INT64_C(512) << 20);
+}
+
+hipError_t launch_grouped_gemm(Grouped g, int fa, int fb, int out_dtype, hipStream_t st) {
     const int tiles_n = (g.N + kTn - 1) / kTn;
     const bool wide = wide_preferred(g, tiles_n);
+    const int l = paired_log2(g, tiles_n);
+    g.streaming = streams((int64_t)g.cap * g.N, out_dtype);
     const unsigned grid = wide ? blocks_for(most_row_tiles(g.cap, g.E, kWide) * tiles_n, kCUs)
-                               : blocks_for(most_row_tiles(g.cap, g.E, kPaired) * tiles_n, 2 * kCUs);
-#define FP8DS_GG(FA_, FB_, O_)                                                          \
-    do {                                                                                \
-        if (wide) k_grouped_gemm_wide<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n); \
-        else k_grouped_gemm_paired<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n);    \
+                               : blocks_for(most_row_tiles(g.cap, g.E, 1 << l) * tiles_n, 2 * kCUs);
+#define FP8DS_GG(FA_, FB_, O_)                                                                 \
+    do {                                                                                       \
+        if (wide) k_grouped_gemm_wide<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n);       \
+        else k_grouped_gemm_paired<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, l, tiles_n);       \
     } while (0)
     FP8DS_GROUPED_SWITCH(FP8DS_GG)
 #undef FP8DS_GG
     return hipGetLastError();
 }
 
-hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
+hipError_t launch_grouped_wgrad(Grouped g, int fa, int fb, int out_dtype, hipStream_t st) {
+    g.streaming = streams((int64_t)g.E * g.N * g.K, out_dtype);
     const int tiles_m = (g.N + kPaired - 1) / kPaired, tiles_n = (g.K + kTn - 1) / kTn;
     const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n, 2 * kCUs);
 #define FP8DS_GW(FA_, FB_, O_) k_grouped_wgrad<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n)

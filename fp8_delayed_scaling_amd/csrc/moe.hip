@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_plan(const int32_t *__rest
                                                            int32_t *__restrict__ slot) {
     __shared__ int32_t base[kMoeMaxExperts];
     __shared__ int32_t wcnt[kPlanWaves][kMoeMaxExperts];
-    __shared__ int32_t wsum[kPlanWaves + 1];
+    __shared__ int32_t wsum[kPlanWaves + 1], ahead[kMoeMaxExperts];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, nb = gridDim.x;
     const int64_t i0 = (int64_t)blockIdx.x * rounds * kPlanThreads + t;
 
@@ -87,12 +87,25 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_plan(const int32_t *__rest
         }
         __syncthreads();
         total = base[t];
-    } else if (t < E) {
-        for (int b = 0; b < nb; ++b) {
-            const int32_t h = hist[(int64_t)b * E + t];
-            total += h;
-            before += b < (int)blockIdx.x ? h : 0;
+    } else {
+        // all threads read the histograms, 1024 / (E rounded up to a power of two) blocks' at a time
+        base[t] = ahead[t] = 0;
+        __syncthreads();
+        const int log2 = E > 1 ? 32 - __builtin_clz(E - 1) : 0, e = t & ((1 << log2) - 1);
+        int32_t all = 0, mine = 0;
+        if (e < E) {
+#pragma unroll 4
+            for (int b = t >> log2; b < nb; b += kPlanThreads >> log2) {
+                const int32_t h = hist[(int64_t)b * E + e];
+                all += h;
+                mine += b < (int)blockIdx.x ? h : 0;
+            }
         }
+        if (all != 0) atomicAdd(&base[e], all);
+        if (mine != 0) atomicAdd(&ahead[e], mine);
+        __syncthreads();
+        total = base[t];
+        before = ahead[t];
     }
     // first row of expert t: exclusive sum of the padded counts
     const int32_t padded = (total + align - 1) / align * align;
