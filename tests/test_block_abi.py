@@ -197,3 +197,31 @@ def test_grouped_binding_checks():
             torch.zeros(E, N, K, **bf))
     _raises("dW", F.fp8_grouped_wgrad, torch.zeros(N, cap, **u8), 0, s, torch.zeros(K, cap, **u8), 0, s, off,
             torch.zeros(E, K, N, **bf))
+
+
+def test_host_tensors_are_refused():
+    """Tensors that pass every check but are not on the GPU: refused, also by prepare()."""
+    M, H, E, T, k = 4, 32, 3, 6, 2
+    t = lambda *s: torch.zeros(s, **bf)  # noqa: E731
+    norm = (t(M, H), t(H), None, None, t(M, H), 1.0, t(M, H), None, t(H), None, None, t(M, H))
+    cap = F.fp8_moe_capacity(T, k, E)
+    plan = (torch.zeros(T, k, **i32), E, 16, torch.zeros(E + 1, **i32), torch.zeros(cap, **i32), torch.zeros(T, k, **i32))
+    s = torch.ones(1, **f32)
+    for fn, args in ((F.fp8_norm_residual_fwd, norm), (F.fp8_moe_plan, plan),
+                     (F.fp8_moe_combine, (t(cap, H), torch.zeros(T, k, **i32), None, t(T, H))),
+                     (F.fp8_moe_sort_cast, (t(T, H), torch.zeros(cap, **i32), k, None, s, 0, torch.zeros(cap, H, **u8)))):
+        with pytest.raises((ValueError, RuntimeError, AssertionError)):      # the stream may be asked for first
+            fn(*args)
+        with pytest.raises(ValueError, match="on the GPU"):
+            fn(*args, stream=0)
+        with pytest.raises(ValueError, match="on the GPU"):
+            F.prepare(fn, *args, stream=0)
+
+
+def test_grouped_leading_dimensions():
+    gemm = _call("fp8_grouped_gemm", dict(A=A16, fa=0, sa=A16, lda=64, B=A16, fb=1, sb=A16, ldb=64, stride=64 * 32, off=A16,
+                                          E=4, D=A16, ldd=1 << 23, dt=0, cap=128, N=32, K=64, st=None))
+    assert gemm() == -2
+    wg = _call("fp8_grouped_wgrad", dict(A=A16, fa=1, sa=A16, lda=128, B=A16, fb=0, sb=A16, ldb=128, off=A16, E=1, D=A16, dt=1,
+                                         cap=128, N=16, K=1 << 23, st=None))
+    assert wg() == -2
