@@ -114,6 +114,23 @@ def fp8ds_version() -> int:
     return int(lib().fp8ds_version())
 
 
+_calls = None
+
+
+def _native():
+    """The module of csrc/call.cpp, which takes the block operators' calls when every argument is as it should be."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _call
+        except ImportError as e:
+            raise RuntimeError("the module of csrc/call.cpp is not built: run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _calls = _call
+    return _calls
+
+
 # ----------------------------------------------------------------------------- marshalling
 
 def _ptr(t) -> Optional[int]:
@@ -487,6 +504,10 @@ def fp8_norm_residual_fwd(block_out, w_post, b_post, gate, resid, alpha, x, post
     ``h`` and / or FP8 codes ``h8`` (see include/fp8ds.h for what may be None).
 
     ``post_stats`` / ``pre_stats``: float32, rows values (RMS) or 2 * rows (layer: 1 / deviation, then mean)."""
+    if _tls.rec is None and (_calls or _native()).norm_fwd(
+            block_out, w_post, b_post, gate, resid, alpha, x, post_stats, w_pre, b_pre, pre_stats, h, h8, scale, fmt,
+            scale_inv_out, amax_slot, kind, eps, stream):
+        return
     ref, name = (resid, "resid") if block_out is None else (block_out, "block_out")
     _want(ref, _BF16, name, required=True)
     shape = ref.shape
@@ -511,6 +532,10 @@ def fp8_norm_residual_bwd(dh, dx, block_out, w_post, b_post, gate, alpha, x, pos
                           d_resid, dw_post, db_post, dgate, dw_pre, db_pre, workspace, kind=NORM_RMS, stream=None):
     """Gradients of fp8_norm_residual_fwd: ``dh`` of h, ``dx`` of x (either may be None), from the x and the
     statistics that the forward wrote.  ``workspace``: ``fp8_norm_residual_workspace_bytes(rows, width, gates)``."""
+    if _tls.rec is None and (_calls or _native()).norm_bwd(
+            dh, dx, block_out, w_post, b_post, gate, alpha, x, post_stats, w_pre, pre_stats, d_block, d_resid, dw_post,
+            db_post, dgate, dw_pre, db_pre, workspace, kind, stream):
+        return
     ref = dh if dh is not None else dx
     _want(ref, _BF16, "dh" if dh is not None else "dx", required=True)
     shape = ref.shape
@@ -544,6 +569,8 @@ def fp8_moe_workspace_bytes(T: int, top: int, E: int) -> int:
 def fp8_moe_plan(experts, E: int, align: int, offsets, src, slot, workspace=None, stream=None):
     """Sort the choices ``experts`` [T, top] (int32; outside [0, E): dropped) by expert: ``offsets`` [E + 1],
     ``src`` [capacity], ``slot`` [T, top] (see include/fp8ds.h)."""
+    if _tls.rec is None and (_calls or _native()).moe_plan(experts, E, align, offsets, src, slot, workspace, stream):
+        return
     _want(experts, _I32, "experts", required=True)
     if experts.dim() != 2:
         raise ValueError("experts must be [T, top]")
@@ -572,6 +599,9 @@ def _sort_args(x, dtypes, src, top, weights, out, out_dtypes, out_t):
 def fp8_moe_sort_cast(x, src, top: int, weights, scale, fmt, out, out_t=None, scale_inv_out=None, amax_slot=None,
                       stream=None):
     """Rows of bfloat16 ``x`` in expert order, times ``weights`` (or None), as FP8 codes and their transpose."""
+    if _tls.rec is None and (_calls or _native()).moe_sort_cast(
+            x, src, top, weights, scale, fmt, out, out_t, scale_inv_out, amax_slot, stream):
+        return
     T, H, cap, p_x, p_src, p_w, p_out, p_out_t = _sort_args(x, _BF16, src, top, weights, out, _U8, out_t)
     _invoke("fp8_moe_sort_cast", p_x, T, p_src, cap, int(top), p_w, _some(scale, _F32, 1, "scale"), int(fmt), p_out, p_out_t,
             _some(scale_inv_out, _F32, 1, "scale_inv_out"), _some(amax_slot, _F32, 1, "amax_slot"), H, _stream(stream))
@@ -579,6 +609,8 @@ def fp8_moe_sort_cast(x, src, top: int, weights, scale, fmt, out, out_t=None, sc
 
 def fp8_moe_sort_codes(x8, src, top: int, out, out_t=None, stream=None):
     """Rows of FP8 codes in expert order, and their transpose (codes copied; padding rows are zero)."""
+    if _tls.rec is None and (_calls or _native()).moe_sort_codes(x8, src, top, out, out_t, stream):
+        return
     T, H, cap, p_x, p_src, _, p_out, p_out_t = _sort_args(x8, _U8, src, top, None, out, _U8, out_t)
     _invoke("fp8_moe_sort_codes", p_x, T, p_src, cap, int(top), p_out, p_out_t, H, _stream(stream))
 
@@ -600,6 +632,8 @@ def _back_args(ys, slot):
 
 def fp8_moe_combine(ys, slot, weights, y, stream=None):
     """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights None: 1)."""
+    if _tls.rec is None and (_calls or _native()).moe_combine(ys, slot, weights, y, stream):
+        return
     cap, H, T, k, p_ys, p_slot = _back_args(ys, slot)
     _invoke("fp8_moe_combine", p_ys, cap, p_slot, _arg(weights, _F32, (T, k), "weights"), T, k, _arg(y, _BF16, (T, H), "y", True),
             H, _stream(stream))
@@ -607,6 +641,8 @@ def fp8_moe_combine(ys, slot, weights, y, stream=None):
 
 def fp8_moe_weight_grad(dy, ys, slot, dweights, stream=None):
     """dweights[t, j] = <dy[t], ys[slot[t, j]]>, 0 for a dropped choice."""
+    if _tls.rec is None and (_calls or _native()).moe_weight_grad(dy, ys, slot, dweights, stream):
+        return
     cap, H, T, k, p_ys, p_slot = _back_args(ys, slot)
     _invoke("fp8_moe_weight_grad", _arg(dy, _BF16, (T, H), "dy", True), p_ys, cap, p_slot, T, k,
             _arg(dweights, _F32, (T, k), "dweights", True), H, _stream(stream))
@@ -621,6 +657,9 @@ def _rows_dense(**kw):
 def fp8_grouped_gemm(A, fa, a_scale_inv, B, fb, b_scale_inv, offsets, D, stream=None):
     """D[r] = A[r] B[e]^T * a_scale_inv * b_scale_inv for the rows r in [offsets[e], offsets[e + 1]):
     A [cap, K] and B [E, N, K] FP8 codes (B may be a strided view), D [cap, N] bfloat16 or float32."""
+    if _tls.rec is None and (_calls or _native()).grouped_gemm(
+            A, fa, a_scale_inv, B, fb, b_scale_inv, offsets, D, stream):
+        return
     _want(A, _U8, "A", contiguous=False, required=True)
     _want(B, _U8, "B", contiguous=False, required=True)
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
@@ -640,6 +679,9 @@ def fp8_grouped_gemm(A, fa, a_scale_inv, B, fb, b_scale_inv, offsets, D, stream=
 def fp8_grouped_wgrad(At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, stream=None):
     """dW[e] = At[:, rows of e] Bt[:, rows of e]^T * a_scale_inv * b_scale_inv: At [N, cap] and Bt [K, cap] FP8
     codes (the transposes of the sorted rows), dW [E, N, K] bfloat16 or float32."""
+    if _tls.rec is None and (_calls or _native()).grouped_wgrad(
+            At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, stream):
+        return
     _want(At, _U8, "At", contiguous=False, required=True)
     _want(Bt, _U8, "Bt", contiguous=False, required=True)
     if At.dim() != 2 or Bt.dim() != 2 or At.shape[1] != Bt.shape[1]:

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -13,6 +14,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["cast.hip", "transpose.hip", "scale_update.hip", "gemm.hip", "api.cpp", "noalloc.hip",
            "norm.hip", "moe.hip", "grouped.hip", "api_block.cpp"]
+CALL = os.path.join(HERE, "_call.so")      # the Python module of call.cpp, next to the library it calls
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # No fast-math and no denormal flushing (the casts must round float32 subnormals exactly);
@@ -34,6 +36,22 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_call(out: str) -> None:
+    """The block operators' calls from Python (host code only): against this PyTorch's headers, linked with the
+    library in this folder."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include", INCLUDE]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(a for i in inc for a in ("-isystem", i)), os.path.join(CSRC, "call.cpp"), "-o", out,
+           "-L", HERE, "-lfp8ds", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for call.cpp:\n{r.stderr}")
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source (always, so a stale library is never reused) and link the library."""
     with ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as ex:
@@ -44,6 +62,8 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_call(CALL + ".tmp")
+    os.replace(CALL + ".tmp", CALL)
     if verbose:
         print("built", LIB)
     return LIB
