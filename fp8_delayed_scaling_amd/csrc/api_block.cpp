@@ -242,7 +242,7 @@ int fp8_grouped_gemm(const uint8_t *A, int fa, const float *a_scale_inv, int64_t
     if (offsets == nullptr || D == nullptr || a_scale_inv == nullptr || b_scale_inv == nullptr) return FP8DS_ERR_NULL;
     if (K > 0 && (A == nullptr || B == nullptr)) return FP8DS_ERR_NULL;
     const fp8ds::Grouped g{A, B, a_scale_inv, b_scale_inv, offsets, D, lda, ldb, stride_b, ldd, 0, (int)cap, (int)E,
-                           (int)N, (int)K, false};
+                           (int)N, (int)K};
     return hip_status(fp8ds::launch_grouped_gemm(g, fa, fb, out_dtype, stream));
 }
 
@@ -258,7 +258,7 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
     if (offsets == nullptr || dW == nullptr || a_scale_inv == nullptr || b_scale_inv == nullptr) return FP8DS_ERR_NULL;
     if (cap > 0 && (At == nullptr || Bt == nullptr)) return FP8DS_ERR_NULL;
     const fp8ds::Grouped g{At, Bt, a_scale_inv, b_scale_inv, offsets, dW, lda, ldb, 0, K, N * K, (int)cap, (int)E,
-                           (int)N, (int)K, false};
+                           (int)N, (int)K};
     return hip_status(fp8ds::launch_grouped_wgrad(g, fa, fb, out_dtype, stream));
 }
 

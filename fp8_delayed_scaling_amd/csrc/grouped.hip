@@ -247,15 +247,14 @@ template <int OUT> __device__ __forceinline__ int col_of(int q, int m) {
 }
 
 // What both kernels share: the loads, the fragments and the output.
-template <int FA, int FB, int OUT>
+template <int FA, int FB, int OUT, bool STREAM>
 struct Work {
     int64_t ldd;
     float sa, sb;
     int lda, ldb, wave, wm, wn;
-    bool streaming;
 
     explicit __device__ __forceinline__ Work(const Grouped &gr)
-        : ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb), streaming(gr.streaming) {
+        : ldd(gr.ldd), sa(*gr.a_sinv), sb(*gr.b_sinv), lda((int)gr.lda), ldb((int)gr.ldb) {
         wave = uniform((int)threadIdx.x >> 6);
         wm = wave >> 1; wn = wave & 1;
     }
@@ -326,8 +325,7 @@ struct Work {
                     }
                     if (vec) {
                         const uint32_t off = col0 + p * 64 < t.cols ? here + (uint32_t)(p * 64 * kEsz) : kOutside;
-                        if (streaming) __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, kStreaming);
-                        else __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(w, rs, (int)off, 0, STREAM ? kStreaming : 0);
                     } else {
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) {
@@ -350,9 +348,9 @@ struct Work {
 // were read into registers during step j - 1; it reads the fragments of B_{j+1}, loads B_{j+3} into
 // B_j's slot, before its last block waits for A_{j+1} and B_{j+2}, and in that block loads A_{j+2}
 // into A_j's slot.  A is read by several tiles at a time and comes from L2, B from HBM.
-template <int FA, int FB, int OUT>
-struct Wide : Work<FA, FB, OUT> {
-    using W = Work<FA, FB, OUT>;
+template <int FA, int FB, int OUT, bool STREAM>
+struct Wide : Work<FA, FB, OUT, STREAM> {
+    using W = Work<FA, FB, OUT, STREAM>;
     using Loads = typename W::Loads;
     using W::loads_of;
     using W::fresh_lane;
@@ -510,9 +508,9 @@ struct Wide : Work<FA, FB, OUT> {
 // loads A_{j+1} and B_{j+2} into the slots so freed while its MFMAs run; the other block's MFMAs
 // fill the time of the reads and waits, and its loads that of the output.  A is read by several
 // tiles at a time and comes from L2; B, from HBM, has two steps to arrive.
-template <int FA, int FB, int OUT>
-struct Paired : Work<FA, FB, OUT> {
-    using W = Work<FA, FB, OUT>;
+template <int FA, int FB, int OUT, bool STREAM>
+struct Paired : Work<FA, FB, OUT, STREAM> {
+    using W = Work<FA, FB, OUT, STREAM>;
     using Loads = typename W::Loads;
     using W::loads_of;
     using W::fresh_lane;
@@ -618,7 +616,7 @@ struct Paired : Work<FA, FB, OUT> {
 
 };
 
-template <int FA, int FB, int OUT, class Tiles>
+template <int FA, int FB, int OUT, bool STREAM, class Tiles>
 __device__ __forceinline__ void run_wide(const Grouped &g, Tiles &&tiles) {
     __shared__ __align__(16) uint8_t sa0[256 * kStep];
     __shared__ __align__(16) uint8_t sa1[256 * kStep];
@@ -627,7 +625,7 @@ __device__ __forceinline__ void run_wide(const Grouped &g, Tiles &&tiles) {
     __shared__ __align__(16) uint8_t sb2[256 * kStep];
     Tile t, next;
     if (!tiles(t)) return;
-    const Wide<FA, FB, OUT> w(g, sa0, sa1, sb0, sb1, sb2);
+    const Wide<FA, FB, OUT, STREAM> w(g, sa0, sa1, sb0, sb1, sb2);
     w.first_loads(t);
     int stores = 0;
     for (bool more = true; more; t = next) {
@@ -641,14 +639,14 @@ __device__ __forceinline__ void run_wide(const Grouped &g, Tiles &&tiles) {
     }
 }
 
-template <int FA, int FB, int OUT, class Tiles>
+template <int FA, int FB, int OUT, bool STREAM, class Tiles>
 __device__ __forceinline__ void run_paired(const Grouped &g, Tiles &&tiles) {
     __shared__ __align__(16) uint8_t sa0[128 * kStep];
     __shared__ __align__(16) uint8_t sb0[256 * kStep];
     __shared__ __align__(16) uint8_t sb1[256 * kStep];
     Tile t, next;
     if (!tiles(t)) return;
-    const Paired<FA, FB, OUT> w(g, sa0, sb0, sb1);
+    const Paired<FA, FB, OUT, STREAM> w(g, sa0, sb0, sb1);
     w.first_loads(t);
     for (bool more = true; more; t = next) {
         const int nb = (t.rows + 31) / 32;
@@ -663,15 +661,15 @@ __device__ __forceinline__ void run_paired(const Grouped &g, Tiles &&tiles) {
 
 template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(kThreads, 1) void k_grouped_gemm_wide(const Grouped g, int tiles_n) {
-    run_wide<FA, FB, OUT>(g, RowTiles<OUT>(g, 8, tiles_n));
+    run_wide<FA, FB, OUT, true>(g, RowTiles<OUT>(g, 8, tiles_n));
 }
 template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(kThreads, 2) void k_grouped_gemm_paired(const Grouped g, int log2_tm, int tiles_n) {
-    run_paired<FA, FB, OUT>(g, RowTiles<OUT>(g, log2_tm, tiles_n));
+    run_paired<FA, FB, OUT, true>(g, RowTiles<OUT>(g, log2_tm, tiles_n));
 }
-template <int FA, int FB, int OUT>
+template <int FA, int FB, int OUT, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(const Grouped g, int tiles_m, int tiles_n) {
-    run_paired<FA, FB, OUT>(g, ExpertTiles<OUT>(g, tiles_m, tiles_n));
+    run_paired<FA, FB, OUT, STREAM>(g, ExpertTiles<OUT>(g, tiles_m, tiles_n));
 }
 
 #define FP8DS_GROUPED_SWITCH(CALL)                                                                         \
@@ -717,18 +715,18 @@ static int paired_log2(const Grouped &g, int tiles_n) {
     return l;
 }
 
-// Outputs that no cache holds leave L2 first (nontemporal stores): 64 experts' weight gradient [2048,
-// 4096] of 512 rows each, 1.07 GB, 542 us without and 405 with; 270 MB of short rows that do not
-// fill their cache lines (64 x [608, 3472], 16 rows each) 60 and 97, 4 MB 19 and 22.
-static bool streams(int64_t elements, int out_dtype) {
-    return elements * (out_dtype == FP8DS_OUT_BF16 ? 2 : 4) >= (INT64_C(512) << 20);
+// Weight gradients that no cache holds leave L2 first (nontemporal stores): 64 experts' [2048, 4096]
+// of 512 rows each, 1.07 GB, 542 us without and 405 with; 270 MB of short rows that do not fill
+// their cache lines (64 x [608, 3472], 16 rows each) 60 and 97, 4 MB 19 and 22.  The forward's
+// output always does (input gradient of 6002 rows, [2560, 1424]: 60 us without, 54 with).
+static bool wgrad_streams(const Grouped &g, int out_dtype) {
+    return (int64_t)g.E * g.N * g.K * (out_dtype == FP8DS_OUT_BF16 ? 2 : 4) >= (INT64_C(512) << 20);
 }
 
-hipError_t launch_grouped_gemm(Grouped g, int fa, int fb, int out_dtype, hipStream_t st) {
+hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
     const int tiles_n = (g.N + kTn - 1) / kTn;
     const bool wide = wide_preferred(g, tiles_n);
     const int l = paired_log2(g, tiles_n);
-    g.streaming = streams((int64_t)g.cap * g.N, out_dtype);
     const unsigned grid = wide ? blocks_for(most_row_tiles(g.cap, g.E, kWide) * tiles_n, kCUs)
                                : blocks_for(most_row_tiles(g.cap, g.E, 1 << l) * tiles_n, 2 * kCUs);
 #define FP8DS_GG(FA_, FB_, O_)                                                                 \
@@ -741,11 +739,15 @@ hipError_t launch_grouped_gemm(Grouped g, int fa, int fb, int out_dtype, hipStre
     return hipGetLastError();
 }
 
-hipError_t launch_grouped_wgrad(Grouped g, int fa, int fb, int out_dtype, hipStream_t st) {
-    g.streaming = streams((int64_t)g.E * g.N * g.K, out_dtype);
+hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
+    const bool stream = wgrad_streams(g, out_dtype);
     const int tiles_m = (g.N + kPaired - 1) / kPaired, tiles_n = (g.K + kTn - 1) / kTn;
     const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n, 2 * kCUs);
-#define FP8DS_GW(FA_, FB_, O_) k_grouped_wgrad<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n)
+#define FP8DS_GW(FA_, FB_, O_)                                                                            \
+    do {                                                                                                  \
+        if (stream) k_grouped_wgrad<FA_, FB_, O_, true><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n);   \
+        else k_grouped_wgrad<FA_, FB_, O_, false><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n);         \
+    } while (0)
     FP8DS_GROUPED_SWITCH(FP8DS_GW)
 #undef FP8DS_GW
     return hipGetLastError();

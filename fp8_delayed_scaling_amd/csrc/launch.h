@@ -108,13 +108,12 @@ struct Grouped {
     void *D;
     int64_t lda, ldb, stride_b, ldd, stride_d;
     int cap, E, N, K;
-    bool streaming;          // set by the launcher: nontemporal output
 };
 constexpr int64_t kGroupedMaxLd = INT64_C(1) << 23;
 // whether a launch can number the call's tiles
 bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N);
 bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K);
-hipError_t launch_grouped_gemm(Grouped g, int fa, int fb, int out_dtype, hipStream_t st);
-hipError_t launch_grouped_wgrad(Grouped g, int fa, int fb, int out_dtype, hipStream_t st);
+hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st);
+hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st);
 
 }  // namespace fp8ds
