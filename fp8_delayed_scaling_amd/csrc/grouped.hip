@@ -172,8 +172,10 @@ __device__ __forceinline__ int offset_at(const Grouped &g, int e) {
 }
 
 // The weight gradient's tiles.  Every XCD takes an eighth of each expert's tiles, whatever the
-// routing: the ranges of B that an XCD reads stay in its L2, A is read by all of them.  Which
-// eighth moves with the expert, so that remainders spread.  Where two to four experts' eighths fill
+// routing, so that it reads few of the operands' rows and keeps them in its L2: half of the row
+// tiles by a quarter of the columns where the row tiles are even (547 us with all row tiles by an
+// eighth, 535 this way), else all by an eighth.  Which eighth moves with the expert, so that
+// remainders spread.  Where two to four experts' eighths fill
 // an XCD's blocks, those form as many groups, and each expert goes to the group that has the least
 // work so far (a tile costs its K steps and about three for its output); else the tiles are taken
 // in order, shifted by some blocks in every round.
@@ -223,7 +225,8 @@ struct ExpertTiles {
             }
             ++next;
         }
-        const int tn = divide(in, tiles_m), tm = in - tn * tiles_m;
+        const int stripe = tiles_m % 2 == 0 ? tiles_m / 2 : tiles_m, s = divide(in, stripe * tiles_n), q = in - s * stripe * tiles_n;
+        const int tn = divide(q, stripe), tm = s * stripe + q - tn * stripe;
         const int lo = offset_at(g, e), len = max(0, offset_at(g, e + 1) - lo);
         constexpr int kEsz = OUT == 0 ? 2 : 4;
         t = Tile{g.A + (int64_t)tm * h * g.lda + lo, g.B + (int64_t)tn * kTn * g.ldb + lo,
