@@ -39,6 +39,7 @@ constexpr int kStep = 128;                   // K bytes per step
 constexpr int kThreads = 256;
 constexpr int kCUs = 256;
 constexpr int kXcds = 8;                     // blocks are dealt round-robin to the XCDs
+constexpr int kLog2Run = 3;                  // tiles that follow each other on one XCD, in the forward
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every tile's extent (below 2^31 bytes)
 constexpr int kStreaming = 2;                // nontemporal
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
@@ -93,22 +94,22 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 // The forward's tiles, an expert's ceil(rows / tile height) * tiles_n with its row tiles running fastest.
 // Among 64 experts, tall tiles come first (in every expert all tiles but the last have one height).
-// The tiles are taken in rounds, runs of kRun dealt to the XCDs forwards and backwards in turn, a
-// run to blocks of one XCD: they share B's rows, which come from HBM once, and A's.  Every block so
+// The tiles are taken in rounds, runs of 8 (single ones, where an XCD has fewer blocks) dealt to the
+// XCDs forwards and backwards in turn, a run to blocks of one XCD: they share B's rows, which come
+// from HBM once, and A's.  Every block so
 // takes a like mixture of heights, and half of the blocks take theirs from the last round to the
 // first: tall tiles, bound by the products, run beside low ones, bound by B's bytes.  (Unevenly
 // routed forward of 64 experts, half of which have under 1 % of the rows: in the experts' order
 // 330 us, tall tiles first 286, this way 275; evenly routed 230.)
 template <int OUT>
 struct RowTiles {
-    static constexpr int kRun = 8;
     const Grouped &g;
-    int log2_tm, tiles_n, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
+    int log2_tm, tiles_n, log2_run, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
     __device__ __forceinline__ RowTiles(const Grouped &g_, int log2_tm_, int tiles_n_)
-        : g(g_), log2_tm(log2_tm_), tiles_n(tiles_n_), total(0), round(0), e0(0), before(0) {
+        : g(g_), log2_tm(log2_tm_), tiles_n(tiles_n_), log2_run(gridDim.x >= kXcds << kLog2Run ? kLog2Run : 0), total(0), round(0), e0(0), before(0) {
         int lo, hi;
         for (int e = 0; e < g.E; e += 64) total += count(e, lo, hi);
-        deals = (total + kRun * kXcds - 1) / (kRun * kXcds);
+        deals = (total + (kXcds << log2_run) - 1) / (kXcds << log2_run);
     }
     __device__ __forceinline__ int tiles_of(int n) const { return (n + (1 << log2_tm) - 1) >> log2_tm; }
     // tiles of the experts e .. e + 63, and the rows of the lane's among them
@@ -124,13 +125,13 @@ struct RowTiles {
     // the block's next tile; false when there is none
     __device__ __forceinline__ bool operator()(Tile &t) {
         const int slots = gridDim.x / kXcds, slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
-        const int rounds = divide(deals * kRun + slots - 1, slots);
+        const int rounds = divide((deals << log2_run) + slots - 1, slots);
         int tile;
         for (;; ++round) {
             if (round >= rounds) return false;
-            const int r = (slot / kRun) & 1 ? rounds - 1 - round : round;
-            const int l = r * slots + (r & 1 ? slots - 1 - slot : slot), deal = l / kRun;
-            tile = (deal * kXcds + (deal & 1 ? kXcds - 1 - xcd : xcd)) * kRun + l % kRun;
+            const int r = (slot >> log2_run) & 1 ? rounds - 1 - round : round;
+            const int l = r * slots + (r & 1 ? slots - 1 - slot : slot), deal = l >> log2_run;
+            tile = ((deal * kXcds + (deal & 1 ? kXcds - 1 - xcd : xcd)) << log2_run) + (l & ((1 << log2_run) - 1));
             if (tile < total) break;
         }
         ++round;
@@ -703,21 +704,25 @@ bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K) {
     const int64_t per = ((N + kPaired) / kPaired) * ((K + kTn) / kTn) + kXcds;   // at most 2^48
     return E <= (INT_MAX - (1 << 16)) / per;
 }
-// One or two blocks per CU, fewer for fewer tiles, a multiple of the XCDs.
-static unsigned blocks_for(int64_t tiles, int64_t most) {
-    return (unsigned)((tiles < most ? tiles + kXcds - 1 : most) / kXcds * kXcds);
+// One or two blocks per CU, fewer for fewer tiles: a multiple of `unit`, so that no XCD has more tiles
+// than blocks where others have fewer (unit: the XCDs, times a run where runs are dealt).
+static unsigned blocks_for(int64_t tiles, int64_t most, int64_t unit) {
+    return (unsigned)(tiles < most ? (tiles + unit - 1) / unit * unit : most);
+}
+static unsigned forward_blocks(int64_t tiles, int64_t most) {
+    return blocks_for(tiles, most, tiles >= kXcds << kLog2Run ? kXcds << kLog2Run : kXcds);
 }
 // Wide tiles from 192 rows for each expert on and two rounds of them on all CUs.
 static bool wide_preferred(const Grouped &g, int tiles_n) {
     return g.cap / g.E >= 192 && (int64_t)g.cap / kWide * tiles_n >= 2 * kCUs;
 }
 
-// Paired tiles are at most 128 rows high, lower where fewer than one such tile for each CU would
-// come of even routing: more blocks then share the contraction's steps, which take about a
-// microsecond each (4 experts, 2664 rows, [240, 3392]: 49 us at 128 rows, 33 at 32).
+// Paired tiles are at most 128 rows high, lower where even routing would give fewer than one for
+// every other CU: more blocks then share the rows (7872 rows over 6 experts, [400, 3056]: 35 us with
+// tiles of 32 rows, 24 of 64; 2704 over 4, [240, 3392]: 18.5 and 20.6).
 static int paired_log2(const Grouped &g, int tiles_n) {
     int l = 7;
-    while (l > 5 && ((int64_t)g.cap >> l) * tiles_n < kCUs) --l;
+    while (l > 5 && ((int64_t)g.cap >> l) * tiles_n < kCUs / 2) --l;
     return l;
 }
 
@@ -733,8 +738,8 @@ hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, 
     const int tiles_n = (g.N + kTn - 1) / kTn;
     const bool wide = wide_preferred(g, tiles_n);
     const int l = paired_log2(g, tiles_n);
-    const unsigned grid = wide ? blocks_for(most_row_tiles(g.cap, g.E, kWide) * tiles_n, kCUs)
-                               : blocks_for(most_row_tiles(g.cap, g.E, 1 << l) * tiles_n, 2 * kCUs);
+    const unsigned grid = wide ? forward_blocks(most_row_tiles(g.cap, g.E, kWide) * tiles_n, kCUs)
+                               : forward_blocks(most_row_tiles(g.cap, g.E, 1 << l) * tiles_n, 2 * kCUs);
 #define FP8DS_GG(FA_, FB_, O_)                                                                 \
     do {                                                                                       \
         if (wide) k_grouped_gemm_wide<FA_, FB_, O_><<<grid, kThreads, 0, st>>>(g, tiles_n);       \
@@ -748,7 +753,9 @@ hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, 
 hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st) {
     const bool stream = wgrad_streams(g, out_dtype);
     const int tiles_m = (g.N + kPaired - 1) / kPaired, tiles_n = (g.K + kTn - 1) / kTn;
-    const unsigned grid = blocks_for((int64_t)g.E * tiles_m * tiles_n, 2 * kCUs);
+    // an XCD's places: an eighth of each expert's tiles, rounded up
+    const int64_t places = (int64_t)g.E * (((int64_t)tiles_m * tiles_n + kXcds - 1) / kXcds);
+    const unsigned grid = blocks_for(places * kXcds, 2 * kCUs, kXcds);
 #define FP8DS_GW(FA_, FB_, O_)                                                                            \
     do {                                                                                                  \
         if (stream) k_grouped_wgrad<FA_, FB_, O_, true><<<grid, kThreads, 0, st>>>(g, tiles_m, tiles_n);   \
