@@ -17,7 +17,7 @@
 //           contractions, small problems and few rows per expert
 // Measured: 64 experts, [2048, 4096], 32768 rows: evenly routed forward 230 us (2.4 PFLOP/s; a dense
 // product of that size 212), unevenly 264-282 (2.0, bound by the products and by the 537 MB of
-// weights in turn), weight gradient 517-535 (1.07 GB of output), 64 rows 54 us (341 MB, 6.3 TB/s).
+// weights in turn), weight gradient 495-535 (1.07 GB of output), 64 rows 54 us (341 MB, 6.3 TB/s).
 // An expert's rows are shared evenly among its tiles, in steps of 32 (16 for each row of waves); a
 // tile runs only the 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the
 // tile's extent: rows past it, and the 16-byte pieces of the last K step past K (their offset is
