@@ -354,7 +354,9 @@ struct Work {
 // multiplies A_j, its fragments read one 16-row block ahead of the MFMAs, by B_j, whose fragments
 // were read into registers during step j - 1; it reads the fragments of B_{j+1}, loads B_{j+3} into
 // B_j's slot, before its last block waits for A_{j+1} and B_{j+2}, and in that block loads A_{j+2}
-// into A_j's slot.  A is read by several tiles at a time and comes from L2, B from HBM.
+// into A_j's slot.  So A_j, B_j and B_{j+1} have arrived in every wave's part before step j begins:
+// for step 0 by the wait at the tile's start.  A is read by several tiles at a time and comes from
+// L2, B from HBM.
 template <int FA, int FB, int OUT, bool STREAM>
 struct Wide : Work<FA, FB, OUT, STREAM> {
     using W = Work<FA, FB, OUT, STREAM>;
@@ -382,23 +384,32 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
     __device__ __forceinline__ uint8_t *slot_a(int p) const { return pick(p & 1, sa1, sa0); }
     __device__ __forceinline__ uint8_t *slot_b(int p) const { return pick(p % 3 == 0, sb0, pick(p % 3 == 1, sb1, sb2)); }
 
-    // A tile's first loads, all five slots: A_0 and B_0, then A_1, B_1 and B_2.
+    // A tile's first loads, all five slots, in the order of their waits: A_0, B_0 and B_1, which
+    // step 0 reads, then A_1 and B_2, which it waits for itself (kLater loads).
+    static constexpr int kLater = 16;
     __device__ __forceinline__ void first_loads(const Tile &t) const {
         const int p = phase(steps(t));
         const Loads ld = loads_of(fresh_lane());
         const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        auto load_a = [&](int j) {
             const uint32_t out = outside(t, j, ld.k);
-            uint8_t *const a = slot_a(p + j), *const b = slot_b(p + j);
-            if (j < 2) {
+            uint8_t *const a = slot_a(p + j);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | out) + i * 32 * lda, j);
-            }
+            for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | out) + i * 32 * lda, j);
+        };
+        auto load_b = [&](int j) {
+            const uint32_t out = outside(t, j, ld.k);
+            uint8_t *const b = slot_b(p + j);
 #pragma unroll
             for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out) + row_b(i) * ldb, j);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        };
+        load_a(0);
+        load_b(0);
+        load_b(1);
+        __builtin_amdgcn_sched_barrier(0);
+        load_a(1);
+        load_b(2);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // Waits for all loads but the last N before `stores` (at least that many) output stores: those
@@ -461,6 +472,8 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
                 interleave(8);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            // In flight: B_{j+3}, loaded above.  In step 0 its eight loads follow the stores of the tile
+            // before, which follow A_1 and B_2.
             if (j == 0) wait_before_stores<8>(stores);
             else FP8DS_WAIT_VM(8);
             FP8DS_WAIT_LGKM();
@@ -476,7 +489,7 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
             __builtin_amdgcn_sched_barrier(0);
         };
         const int p = phase(nk);
-        wait_before_stores<24>(stores);                      // A_0 and B_0
+        wait_before_stores<kLater>(stores);                  // A_0, B_0 and B_1; in flight: A_1, B_2, the stores
         FP8DS_BARRIER();
         {
             const uint8_t *b = slot_b(p), *a = slot_a(p);
