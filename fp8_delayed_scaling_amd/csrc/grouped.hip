@@ -20,8 +20,9 @@
 // weights in turn), weight gradient 495-535 (1.07 GB of output), 64 rows 54 us (341 MB, 6.3 TB/s).
 // An expert's rows are shared evenly among its tiles, in steps of 32 (16 for each row of waves); a
 // tile runs only the 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the
-// tile's extent: rows past it, and the 16-byte pieces of the last K step past K (their offset is
-// moved out of the bound), arrive as zeros without touching memory.
+// tile's extent: rows past it, and the 16-byte pieces past K (their offset is moved out of the bound),
+// arrive as zeros without touching memory.  The bound is compared with the lane's offset after the
+// scalar offset is taken off it, so the scalar offset stays inside the tile's K bytes too.
 #include <climits>
 #include <type_traits>
 
@@ -288,10 +289,13 @@ struct Work {
         const uint64_t u = (uint64_t)(uint32_t)uniform((int)a) | (uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32;
         return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, uniform((int)bytes), kBufDesc3);
     }
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t *slot, int i, uint32_t off, int j) const {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint8_t *slot, int i, uint32_t off, int k0) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(slot + (i * 4 + wave) * 1024), 16, off,
-                                                 (uint32_t)uniform(j * kStep), 0, 0);
+                                                 (uint32_t)k0, 0, 0);
     }
+    // K byte of step j's first piece: the loads' scalar offset, the last step's for one past it (all its
+    // pieces are outside)
+    static __device__ __forceinline__ int first_byte(int nk, int j) { return uniform(min(j, nk - 1) * kStep); }
     static __device__ __forceinline__ uint32_t outside(const Tile &t, int j, int piece) {
         return j * kStep + piece < t.K ? 0u : kOutside;
     }
@@ -306,7 +310,7 @@ struct Work {
 
     // row of B, after the lane's in the first load, that load i takes: slot rows 32 i .. are fragments 2 i and 2 i + 1
     static __device__ __forceinline__ constexpr int row_b(int i) { return (i >> 2) * 128 + (OUT == 0 ? 2 * (i & 3) : 64 * ((i >> 1) & 1) + 2 * (i & 1)); }
-    static __device__ __forceinline__ int steps(const Tile &t) { return max(1, (t.K + kStep - 1) / kStep); }   // K = 0: one of zeros
+    static __device__ __forceinline__ int steps(const Tile &t) { return max(1, (uniform(t.K) + kStep - 1) / kStep); }   // K = 0: one of zeros
     // lane l holds row 32 i + 16 wm + 4 (l / 16) + u, column col_of(q, l % 16), in element u of acc[i][q]
     template <int NB>
     __device__ __forceinline__ void store(const Tile &t, const f32x4 (&acc)[NB][8]) const {
@@ -366,6 +370,7 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
     using W::bounded;
     using W::load;
     using W::outside;
+    using W::first_byte;
     using W::frag;
     using W::row_b;
     using W::steps;
@@ -388,20 +393,22 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
     // step 0 reads, then A_1 and B_2, which it waits for itself (kLater loads).
     static constexpr int kLater = 16;
     __device__ __forceinline__ void first_loads(const Tile &t) const {
-        const int p = phase(steps(t));
+        const int nk = steps(t), p = phase(nk);
         const Loads ld = loads_of(fresh_lane());
         const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
         auto load_a = [&](int j) {
             const uint32_t out = outside(t, j, ld.k);
             uint8_t *const a = slot_a(p + j);
+            const int k0 = first_byte(nk, j);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | out) + i * 32 * lda, j);
+            for (int i = 0; i < 8; ++i) load(rs_a, a, i, (ld.va | out) + i * 32 * lda, k0);
         };
         auto load_b = [&](int j) {
             const uint32_t out = outside(t, j, ld.k);
             uint8_t *const b = slot_b(p + j);
+            const int k0 = first_byte(nk, j);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out) + row_b(i) * ldb, j);
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out) + row_b(i) * ldb, k0);
         };
         load_a(0);
         load_b(0);
@@ -459,6 +466,7 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
                         i32x8 (&fbn)[8]) {
             constexpr int P = decltype(pc)::value;
             const uint32_t out_b = outside(t, j + 3, ld.k);
+            const int k_b = first_byte(nk, j + 3);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
@@ -466,7 +474,7 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
 #pragma unroll
                 for (int q = 8 * i / kBlocks; q < 8 * (i + 1) / kBlocks; ++q) {
                     fbn[q] = frag_b(b_nxt, q);
-                    load(rs_b, b_free, q, (ld.vb | out_b) + row_b(q) * ldb, j + 3);
+                    load(rs_b, b_free, q, (ld.vb | out_b) + row_b(q) * ldb, k_b);
                 }
                 mfma(i, fa[(P * NB + i) & 1], fbc);
                 interleave(8);
@@ -482,8 +490,9 @@ struct Wide : Work<FA, FB, OUT, STREAM> {
             const i32x8 last = fa[(P * NB + NB - 1) & 1];
             fa[(P * NB + NB) & 1] = frag_a(a_nxt, 0);
             const uint32_t out_a = outside(t, j + 2, ld.k);
+            const int k_a = first_byte(nk, j + 2);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) load(rs_a, a_cur, n, (ld.va | out_a) + n * 32 * lda, j + 2);
+            for (int n = 0; n < NB; ++n) load(rs_a, a_cur, n, (ld.va | out_a) + n * 32 * lda, k_a);
             mfma(NB - 1, last, fbc);
             interleave(8);
             __builtin_amdgcn_sched_barrier(0);
@@ -537,6 +546,7 @@ struct Paired : Work<FA, FB, OUT, STREAM> {
     using W::bounded;
     using W::load;
     using W::outside;
+    using W::first_byte;
     using W::frag;
     using W::row_b;
     using W::steps;
@@ -555,10 +565,11 @@ struct Paired : Work<FA, FB, OUT, STREAM> {
 
     // A tile's first loads: B_0 and A_0, then B_1.
     __device__ __forceinline__ void first_loads(const Tile &t) const {
-        const int p = steps(t) & 1;
+        const int nk = steps(t), p = nk & 1;
         const Loads ld = loads_of(fresh_lane());
         const auto rs_a = bounded(t.A, (int64_t)t.rows * lda), rs_b = bounded(t.B, (int64_t)t.cols * ldb);
         const uint32_t out0 = outside(t, 0, ld.k), out1 = outside(t, 1, ld.k);
+        const int k1 = first_byte(nk, 1);
         uint8_t *b0 = slot_b(p), *b1 = slot_b(p + 1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) load(rs_b, b0, i, (ld.vb | out0) + row_b(i) * ldb, 0);
@@ -566,7 +577,7 @@ struct Paired : Work<FA, FB, OUT, STREAM> {
         for (int i = 0; i < 4; ++i) load(rs_a, sa0, i, (ld.va | out0) + i * 32 * lda, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(rs_b, b1, i, (ld.vb | out1) + row_b(i) * ldb, 1);
+        for (int i = 0; i < 8; ++i) load(rs_b, b1, i, (ld.vb | out1) + row_b(i) * ldb, k1);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -601,11 +612,12 @@ struct Paired : Work<FA, FB, OUT, STREAM> {
             FP8DS_BARRIER();
             __builtin_amdgcn_sched_barrier(0);
             const uint32_t out_a = outside(t, j + 1, ld.k), out_b = outside(t, j + 2, ld.k);
+            const int k_a = first_byte(nk, j + 1), k_b = first_byte(nk, j + 2);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) load(rs_a, sa0, i, (ld.va | out_a) + i * 32 * lda, j + 1);
+            for (int i = 0; i < NB; ++i) load(rs_a, sa0, i, (ld.va | out_a) + i * 32 * lda, k_a);
             __builtin_amdgcn_sched_barrier(0x7cf);           // loads into LDS stay in this order
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out_b) + row_b(i) * ldb, j + 2);
+            for (int i = 0; i < 8; ++i) load(rs_b, b, i, (ld.vb | out_b) + row_b(i) * ldb, k_b);
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int i = 0; i < NB; ++i)

@@ -1,0 +1,28 @@
+"""The experts' FP8 products with operands so small that a K step reaches past all of them."""
+import pytest
+import torch
+
+import fp8_delayed_scaling_amd as F
+from helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+F32 = dict(device=DEV, dtype=torch.float32)
+U8 = dict(device=DEV, dtype=torch.uint8)
+I32 = dict(device=DEV, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("N", [1, 3, 8, 16])
+@pytest.mark.parametrize("K", [16, 32, 144, 272])
+def test_operands_smaller_than_a_step(N, K):
+    """16 rows by N: a step's K bytes are more than the operand's extent.  Codes of 1.0."""
+    print(f"grouped small N={N} K={K}", flush=True)
+    s = torch.ones(1, **F32)
+    A, B = torch.full((16, K), 0x38, **U8), torch.full((1, N, K), 0x38, **U8)
+    D = torch.full((16, N), 7.0, **F32)
+    F.fp8_grouped_gemm(A, 0, s, B, 0, s, torch.tensor([0, 16], **I32), D)
+    assert (D == K).all()
+    dW = torch.full((1, N, 16), 7.0, **F32)
+    Bt = torch.full((16, K), 0x38, **U8)
+    F.fp8_grouped_wgrad(B[0], 0, s, Bt, 0, s, torch.tensor([0, K], **I32), dW)
+    assert (dW == K).all()
