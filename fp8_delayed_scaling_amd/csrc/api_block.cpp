@@ -241,6 +241,8 @@ int fp8_grouped_gemm(const uint8_t *A, int fa, const float *a_scale_inv, int64_t
     if (cap == 0 || N == 0 || E == 0) return FP8DS_OK;
     if (offsets == nullptr || D == nullptr || a_scale_inv == nullptr || b_scale_inv == nullptr) return FP8DS_ERR_NULL;
     if (K > 0 && (A == nullptr || B == nullptr)) return FP8DS_ERR_NULL;
+    // without a contraction the strides are unchecked and stand for nothing: none reaches an offset
+    if (K == 0) lda = ldb = stride_b = 0;
     const fp8ds::Grouped g{A, B, a_scale_inv, b_scale_inv, offsets, D, lda, ldb, stride_b, ldd, 0, (int)cap, (int)E,
                            (int)N, (int)K};
     return hip_status(fp8ds::launch_grouped_gemm(g, fa, fb, out_dtype, stream));
@@ -257,6 +259,7 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
     if (N == 0 || K == 0 || E == 0) return FP8DS_OK;
     if (offsets == nullptr || dW == nullptr || a_scale_inv == nullptr || b_scale_inv == nullptr) return FP8DS_ERR_NULL;
     if (cap > 0 && (At == nullptr || Bt == nullptr)) return FP8DS_ERR_NULL;
+    if (cap == 0) lda = ldb = 0;                       // as above
     const fp8ds::Grouped g{At, Bt, a_scale_inv, b_scale_inv, offsets, dW, lda, ldb, 0, K, N * K, (int)cap, (int)E,
                            (int)N, (int)K};
     return hip_status(fp8ds::launch_grouped_wgrad(g, fa, fb, out_dtype, stream));

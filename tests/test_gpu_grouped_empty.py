@@ -1,4 +1,5 @@
-"""The experts' FP8 products with operands so small that a K step reaches past all of them."""
+"""The experts' FP8 products without a contraction, whatever the operands' strides, and with operands so
+small that a K step reaches past all of them."""
 import pytest
 import torch
 
@@ -10,6 +11,22 @@ pytestmark = pytest.mark.gpu
 F32 = dict(device=DEV, dtype=torch.float32)
 U8 = dict(device=DEV, dtype=torch.uint8)
 I32 = dict(device=DEV, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("ld", [1, 1 << 24, 1 << 26, (1 << 28) + 16])
+@pytest.mark.parametrize("cap,E,N", [(64, 2, 48), (1024, 3, 600)])
+def test_empty_contraction_of_any_stride(ld, cap, E, N):
+    print(f"grouped empty ld={ld} cap={cap}", flush=True)
+    s = torch.ones(1, **F32)
+    none = torch.empty(0, **U8)
+    off = torch.tensor([0, *[16 * (e + 1) for e in range(E - 1)], cap], **I32)
+    for dtype in (torch.bfloat16, torch.float32):
+        D = torch.full((cap, N), 7.0, device=DEV, dtype=dtype)
+        F.fp8_grouped_gemm(none.as_strided((cap, 0), (ld, 1)), 0, s, none.as_strided((E, N, 0), (ld, ld, 1)), 0, s, off, D)
+        assert (D == 0).all()
+        dW = torch.full((E, N, 80), 7.0, device=DEV, dtype=dtype)
+        F.fp8_grouped_wgrad(none.as_strided((N, 0), (ld, 1)), 0, s, none.as_strided((80, 0), (ld, 1)), 0, s, off * 0, dW)
+        assert (dW == 0).all()
 
 
 @pytest.mark.parametrize("N", [1, 3, 8, 16])
