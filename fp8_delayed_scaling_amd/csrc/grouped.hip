@@ -6,8 +6,8 @@
 // offsets[e] .. offsets[e + 1] are expert e's rows, read on the device: the host never learns
 // them.  Both operands are K-contiguous and accumulate in float32; the one product order per output
 // is fixed, so results do not depend on the routing of other experts.  Offsets are held to [0, cap]
-// and to multiples of 16 as they are read, so no content of the buffer makes an access out of
-// bounds.
+// and to multiples of 16 as they are read, and the number of tiles to what offsets in order can give, so
+// no content of the buffer makes an access out of bounds or a search without end.
 //
 // Two kernels, both of four waves (2 x 2, each up to 128 x 128 made of v_mfma_f32_16x16x128_f8f6f4
 // tiles) that take one tile after the other, the first loads of a tile in flight while the tile
@@ -75,6 +75,13 @@ __host__ __device__ inline int tile_rows(int n, int tm) {
     return tiles > 0 ? (blocks + tiles - 1) / tiles * 32 : 0;
 }
 
+// The largest number of row tiles of at most tm rows that offsets in order can give: every expert with
+// rows adds at most one partial tile.
+__host__ __device__ inline int64_t most_row_tiles(int64_t cap, int64_t E, int64_t tm) {
+    const int64_t used = (cap + 15) / 16;
+    return cap / tm + (E < used ? E : used);
+}
+
 // A tile's operands and output, uniform over the block.
 struct Tile {
     const uint8_t *A, *B;
@@ -108,21 +115,27 @@ struct RowTiles {
     int log2_tm, tiles_n, log2_run, total, deals, round, e0, before;      // before: tiles before those of the experts e0 .. e0 + 63
     __device__ __forceinline__ RowTiles(const Grouped &g_, int log2_tm_, int tiles_n_)
         : g(g_), log2_tm(log2_tm_), tiles_n(tiles_n_), log2_run(gridDim.x >= kXcds << kLog2Run ? kLog2Run : 0), total(0), round(0), e0(0), before(0) {
+        // Offsets that fall may count rows for several experts, without end: past what offsets in order
+        // can give, nothing is computed.  So every number of tiles below fits in 31 bits.
+        const uint32_t most = (uint32_t)most_row_tiles(g.cap, g.E, 1 << log2_tm);
+        uint32_t all = 0;
         int lo, hi;
-        for (int e = 0; e < g.E; e += 64) total += count(e, lo, hi);
+        for (int e = 0; e < g.E; e += 64) all = min(all + row_tiles(e, lo, hi), most + 1);
+        total = uniform(all <= most ? (int)all * tiles_n : 0);
         deals = (total + (kXcds << log2_run) - 1) / (kXcds << log2_run);
     }
     __device__ __forceinline__ int tiles_of(int n) const { return (n + (1 << log2_tm) - 1) >> log2_tm; }
-    // tiles of the experts e .. e + 63, and the rows of the lane's among them
-    __device__ __forceinline__ int count(int e, int &lo, int &hi) const {
+    // row tiles of the experts e .. e + 63 (below 2^31), and the rows of the lane's among them
+    __device__ __forceinline__ uint32_t row_tiles(int e, int &lo, int &hi) const {
         const int i = e + (threadIdx.x & 63);
         lo = hi = 0;
         if (i < g.E) {
             lo = min(max(g.offsets[i], 0), g.cap) & ~15;
             hi = max(lo, min(max(g.offsets[i + 1], 0), g.cap) & ~15);
         }
-        return uniform(__builtin_amdgcn_readlane(wave_scan(tiles_of(hi - lo)), 63)) * tiles_n;
+        return (uint32_t)uniform(__builtin_amdgcn_readlane(wave_scan(tiles_of(hi - lo)), 63));
     }
+    __device__ __forceinline__ int count(int e, int &lo, int &hi) const { return (int)row_tiles(e, lo, hi) * tiles_n; }
     // the block's next tile; false when there is none
     __device__ __forceinline__ bool operator()(Tile &t) {
         const int slots = gridDim.x / kXcds, slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
@@ -716,11 +729,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(const Grouped g, 
         default: CALL(kE5M2, kE5M2, 1); break;                                                             \
     }
 
-// The largest number of row tiles: every expert with rows adds at most one partial tile.
-static int64_t most_row_tiles(int64_t cap, int64_t E, int64_t tm) {
-    const int64_t used = (cap + 15) / 16;
-    return cap / tm + (E < used ? E : used);
-}
 // Tiles are numbered in 31 bits, positions up to a round of blocks past the last.
 bool grouped_gemm_fits(int64_t cap, int64_t E, int64_t N) {
     return most_row_tiles(cap, E, 32) <= (INT_MAX - (1 << 16)) / ((N + kTn) / kTn);

@@ -429,9 +429,11 @@ int fp8_moe_weight_grad(const uint16_t *dy, const uint16_t *ys, int64_t cap, con
  * stack [E, N, K], or the cast's transpose [N, E * K] of a stack [E * K, N]: ldb = E * K, stride_b
  * = K), one scale for the whole stack.  D: [cap, N] bfloat16 or float32, row stride ldd; rows
  * outside every expert's are not written.  offsets: [E + 1] int32 on the device, multiples of 16
- * (held to [0, cap] and rounded down to multiples of 16 as they are read).  K % 16 == 0; lda, ldb
- * % 16 == 0, >= K; lda, ldb and ldd below 2^23; stride_b % 16 == 0; A, B 16-byte aligned.  With the output
- * gradient as A and the weights' transpose as B this is the input gradient.
+ * (held to [0, cap] and rounded down to multiples of 16 as they are read; where they fall, an expert
+ * whose end is not past its start has no rows, rows that several experts then cover hold one of their
+ * products, and D is not written at all if the experts would have more tiles than cap rows can give).
+ * K % 16 == 0; lda, ldb % 16 == 0, >= K; lda, ldb and ldd below 2^23; stride_b % 16 == 0; A, B 16-byte
+ * aligned.  With the output gradient as A and the weights' transpose as B this is the input gradient.
  *
  * fp8_grouped_wgrad -- the experts' weight gradients: dW[e][n, k] = (sum over e's rows r of
  * At[n, r] * Bt[k, r]) * (*a_scale_inv) * (*b_scale_inv), zeros for an expert without rows.
