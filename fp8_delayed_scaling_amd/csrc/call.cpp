@@ -97,10 +97,14 @@ struct Args {
     hipStream_t stream(int i) {
         if (!ok) return nullptr;
         if (a[i] == Py_None) return c10::hip::getCurrentHIPStream().stream();
-        if (PyLong_Check(a[i])) return reinterpret_cast<hipStream_t>(PyLong_AsVoidPtr(a[i]));
-        PyObject *handle = PyObject_GetAttrString(a[i], "cuda_stream");
-        void *p = handle != nullptr ? PyLong_AsVoidPtr(handle) : nullptr;
-        Py_XDECREF(handle);
+        void *p = nullptr;
+        if (PyLong_Check(a[i])) {
+            p = PyLong_AsVoidPtr(a[i]);
+        } else {
+            PyObject *handle = PyObject_GetAttrString(a[i], "cuda_stream");
+            if (handle != nullptr) p = PyLong_AsVoidPtr(handle);
+            Py_XDECREF(handle);
+        }
         if (PyErr_Occurred()) {
             PyErr_Clear();
             ok = false;
@@ -121,7 +125,7 @@ struct Args {
 
 PyObject *done(bool ok) { return PyBool_FromLong(ok); }
 
-PyObject *norm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *norm_fwd(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 20);
     if (!a.ok) return done(false);
     const at::Tensor *ref = a.tensor(args[0] == Py_None ? 4 : 0, kBf16);
@@ -150,7 +154,7 @@ PyObject *norm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                               sinv, amax, kind, eps, M, H, st) == FP8DS_OK);
 }
 
-PyObject *norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *norm_bwd(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 21);
     if (!a.ok) return done(false);
     const at::Tensor *ref = a.tensor(args[0] != Py_None ? 0 : 1, kBf16);
@@ -179,7 +183,7 @@ PyObject *norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                               db_post, dgate, dw_pre, db_pre, ws, bytes, kind, M, H, st) == FP8DS_OK);
 }
 
-PyObject *moe_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *moe_plan(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 8);
     const at::Tensor *e = a.tensor(0, kI32), *s = a.ok ? a.tensor(4, kI32) : nullptr;
     if (!a.ok || e->dim() != 2) return done(false);
@@ -194,7 +198,7 @@ PyObject *moe_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return done(a.ok && fp8_moe_plan(experts, T, k, E, align, cap, offsets, src, slot, ws, bytes, st) == FP8DS_OK);
 }
 
-PyObject *moe_sort_cast(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *moe_sort_cast(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 11);
     const at::Tensor *t = a.tensor(0, kBf16), *s = a.ok ? a.tensor(1, kI32) : nullptr;
     if (!a.ok || t->dim() != 2) return done(false);
@@ -210,7 +214,7 @@ PyObject *moe_sort_cast(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return done(a.ok && fp8_moe_sort_cast(x, T, src, cap, top, w, scale, fmt, out, out_t, sinv, amax, H, st) == FP8DS_OK);
 }
 
-PyObject *moe_sort_codes(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *moe_sort_codes(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 6);
     const at::Tensor *t = a.tensor(0, kU8), *s = a.ok ? a.tensor(1, kI32) : nullptr;
     if (!a.ok || t->dim() != 2) return done(false);
@@ -222,7 +226,7 @@ PyObject *moe_sort_codes(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return done(a.ok && fp8_moe_sort_codes(x, T, src, cap, top, out, out_t, H, st) == FP8DS_OK);
 }
 
-PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *moe_combine(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 5);
     const at::Tensor *t = a.tensor(0, kBf16), *s = a.ok ? a.tensor(1, kI32) : nullptr;
     if (!a.ok || t->dim() != 2 || s->dim() != 2) return done(false);
@@ -235,7 +239,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return done(a.ok && fp8_moe_combine(ys, cap, slot, w, T, k, y, H, st) == FP8DS_OK);
 }
 
-PyObject *moe_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *moe_weight_grad(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 5);
     const at::Tensor *t = a.tensor(1, kBf16), *s = a.ok ? a.tensor(2, kI32) : nullptr;
     if (!a.ok || t->dim() != 2 || s->dim() != 2) return done(false);
@@ -257,7 +261,7 @@ const at::Tensor *output(Args &a, int i, int &dtype) {
 }
 bool rows_dense(const at::Tensor *t) { return t->numel() == 0 || t->stride(-1) == 1; }
 
-PyObject *grouped_gemm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *grouped_gemm(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 9);
     const at::Tensor *A = a.tensor(0, kU8), *B = a.ok ? a.tensor(3, kU8) : nullptr;
     int dtype = 0;
@@ -274,7 +278,7 @@ PyObject *grouped_gemm(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                          D->data_ptr(), D->stride(0), dtype, cap, N, K, st) == FP8DS_OK);
 }
 
-PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 9);
     const at::Tensor *A = a.tensor(0, kU8), *B = a.ok ? a.tensor(3, kU8) : nullptr;
     const at::Tensor *off = a.ok ? a.tensor(6, kI32) : nullptr;
@@ -292,7 +296,19 @@ PyObject *grouped_wgrad(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                           st) == FP8DS_OK);
 }
 
-#define FP8DS_CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+// PyTorch raises C++ exceptions for tensors without storage or strides, and where there is no GPU to
+// have a current stream.  None may leave a function that C calls: the binding's checks raise them again.
+template <PyObject *(*call)(PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *, PyObject *const *args, Py_ssize_t n) noexcept {
+    try {
+        return call(args, n);
+    } catch (...) {
+        PyErr_Clear();
+        return done(false);
+    }
+}
+
+#define FP8DS_CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP8DS_CALL(norm_fwd),      FP8DS_CALL(norm_bwd),    FP8DS_CALL(moe_plan),        FP8DS_CALL(moe_sort_cast),
                          FP8DS_CALL(moe_sort_codes), FP8DS_CALL(moe_combine), FP8DS_CALL(moe_weight_grad), FP8DS_CALL(grouped_gemm),
                          FP8DS_CALL(grouped_wgrad), {nullptr, nullptr, 0, nullptr}};
