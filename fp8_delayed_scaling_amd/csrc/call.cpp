@@ -2,9 +2,10 @@
 //
 // Each function here takes a binding's arguments as they are and, when every one is what the call
 // wants (dense tensors on the GPU of the right type and shape, None where that may be), calls the C
-// entry point and returns True.  Anything else, a refusal by the entry point included, returns
-// False: the binding then goes through its own checks, which name what is wrong.  A refused call
-// has launched nothing, so nothing runs twice.
+// entry point and returns True.  Arguments that do not fit, and those that the entry point refuses
+// before it launches anything, give False: the binding then goes through its own checks, which name
+// what is wrong.  A HIP error may come after a launch, so that call is not made again: it raises the
+// binding's error from here.
 //
 // What it saves: a four-row norm takes 27 arguments, which ctypes and the checks in Python took
 // 10.2 us for, the launch included; the kernel runs 4.3.
@@ -124,6 +125,13 @@ struct Args {
 };
 
 PyObject *done(bool ok) { return PyBool_FromLong(ok); }
+PyObject *done_with(int status) {
+    if (status != FP8DS_ERR_HIP) return done(status == FP8DS_OK);
+    PyObject *package = PyImport_ImportModule("fp8_delayed_scaling_amd");
+    PyObject *never = package != nullptr ? PyObject_CallMethod(package, "_check", "i", status) : nullptr;      // raises
+    Py_XDECREF(package);
+    return never;
+}
 
 PyObject *norm_fwd(PyObject *const *args, Py_ssize_t n) {
     Args a(args, n, 20);
@@ -150,8 +158,9 @@ PyObject *norm_fwd(PyObject *const *args, Py_ssize_t n) {
     auto *sinv = a.some<float>(15, kF32, 1), *amax = a.some<float>(16, kF32, 1);
     const float eps = a.real(18);
     const hipStream_t st = a.stream(19);
-    return done(a.ok && fp8_norm_residual_fwd(o, w_post, b_post, gate, G, resid, alpha, x, post, w_pre, b_pre, pre, h, h8, scale, fmt,
-                                              sinv, amax, kind, eps, M, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_norm_residual_fwd(o, w_post, b_post, gate, G, resid, alpha, x, post, w_pre, b_pre, pre, h, h8,
+                                           scale, fmt, sinv, amax, kind, eps, M, H, st));
 }
 
 PyObject *norm_bwd(PyObject *const *args, Py_ssize_t n) {
@@ -179,8 +188,9 @@ PyObject *norm_bwd(PyObject *const *args, Py_ssize_t n) {
     size_t bytes;
     void *ws = a.workspace(18, bytes);
     const hipStream_t st = a.stream(20);
-    return done(a.ok && fp8_norm_residual_bwd(dh, dx, o, w_post, b_post, gate, G, alpha, x, post, w_pre, pre, d_block, d_resid, dw_post,
-                                              db_post, dgate, dw_pre, db_pre, ws, bytes, kind, M, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_norm_residual_bwd(dh, dx, o, w_post, b_post, gate, G, alpha, x, post, w_pre, pre, d_block, d_resid,
+                                           dw_post, db_post, dgate, dw_pre, db_pre, ws, bytes, kind, M, H, st));
 }
 
 PyObject *moe_plan(PyObject *const *args, Py_ssize_t n) {
@@ -195,7 +205,8 @@ PyObject *moe_plan(PyObject *const *args, Py_ssize_t n) {
     size_t bytes;
     void *ws = a.workspace(6, bytes);
     const hipStream_t st = a.stream(7);
-    return done(a.ok && fp8_moe_plan(experts, T, k, E, align, cap, offsets, src, slot, ws, bytes, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_moe_plan(experts, T, k, E, align, cap, offsets, src, slot, ws, bytes, st));
 }
 
 PyObject *moe_sort_cast(PyObject *const *args, Py_ssize_t n) {
@@ -211,7 +222,8 @@ PyObject *moe_sort_cast(PyObject *const *args, Py_ssize_t n) {
     auto *out = a.dense<uint8_t>(6, kU8, {cap, H}, true), *out_t = a.dense<uint8_t>(7, kU8, {H, cap});
     auto *sinv = a.some<float>(8, kF32, 1), *amax = a.some<float>(9, kF32, 1);
     const hipStream_t st = a.stream(10);
-    return done(a.ok && fp8_moe_sort_cast(x, T, src, cap, top, w, scale, fmt, out, out_t, sinv, amax, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_moe_sort_cast(x, T, src, cap, top, w, scale, fmt, out, out_t, sinv, amax, H, st));
 }
 
 PyObject *moe_sort_codes(PyObject *const *args, Py_ssize_t n) {
@@ -223,7 +235,8 @@ PyObject *moe_sort_codes(PyObject *const *args, Py_ssize_t n) {
     const auto *src = a.some<int32_t>(1, kI32, cap);
     auto *out = a.dense<uint8_t>(3, kU8, {cap, H}, true), *out_t = a.dense<uint8_t>(4, kU8, {H, cap});
     const hipStream_t st = a.stream(5);
-    return done(a.ok && fp8_moe_sort_codes(x, T, src, cap, top, out, out_t, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_moe_sort_codes(x, T, src, cap, top, out, out_t, H, st));
 }
 
 PyObject *moe_combine(PyObject *const *args, Py_ssize_t n) {
@@ -236,7 +249,8 @@ PyObject *moe_combine(PyObject *const *args, Py_ssize_t n) {
     const auto *w = a.dense<float>(2, kF32, {T, k});
     auto *y = a.dense<uint16_t>(3, kBf16, {T, H}, true);
     const hipStream_t st = a.stream(4);
-    return done(a.ok && fp8_moe_combine(ys, cap, slot, w, T, k, y, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_moe_combine(ys, cap, slot, w, T, k, y, H, st));
 }
 
 PyObject *moe_weight_grad(PyObject *const *args, Py_ssize_t n) {
@@ -249,7 +263,8 @@ PyObject *moe_weight_grad(PyObject *const *args, Py_ssize_t n) {
     const auto *slot = a.dense<int32_t>(2, kI32, {T, k});
     auto *dw = a.dense<float>(3, kF32, {T, k}, true);
     const hipStream_t st = a.stream(4);
-    return done(a.ok && fp8_moe_weight_grad(dy, ys, cap, slot, T, k, dw, H, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    return done_with(fp8_moe_weight_grad(dy, ys, cap, slot, T, k, dw, H, st));
 }
 
 // Output of the experts' products: its type, with unit stride along the rows.
@@ -273,9 +288,11 @@ PyObject *grouped_gemm(PyObject *const *args, Py_ssize_t n) {
     const auto *sa = a.some<float>(2, kF32, 1), *sb = a.some<float>(5, kF32, 1);
     const auto *off = a.dense<int32_t>(6, kI32, {E + 1}, true);
     const hipStream_t st = a.stream(8);
-    return done(a.ok && fp8_grouped_gemm(static_cast<const uint8_t *>(A->data_ptr()), fa, sa, A->stride(0),
-                                         static_cast<const uint8_t *>(B->data_ptr()), fb, sb, B->stride(1), B->stride(0), off, E,
-                                         D->data_ptr(), D->stride(0), dtype, cap, N, K, st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    const auto *pa = static_cast<const uint8_t *>(A->data_ptr()), *pb = static_cast<const uint8_t *>(B->data_ptr());
+    void *pd = D->data_ptr();
+    return done_with(fp8_grouped_gemm(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(1), B->stride(0), off, E, pd, D->stride(0),
+                                      dtype, cap, N, K, st));
 }
 
 PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
@@ -290,10 +307,11 @@ PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
     const int fa = a.small(1), fb = a.small(4);
     const auto *sa = a.some<float>(2, kF32, 1), *sb = a.some<float>(5, kF32, 1);
     const hipStream_t st = a.stream(8);
-    return done(a.ok && fp8_grouped_wgrad(static_cast<const uint8_t *>(A->data_ptr()), fa, sa, A->stride(0),
-                                          static_cast<const uint8_t *>(B->data_ptr()), fb, sb, B->stride(0),
-                                          static_cast<const int32_t *>(off->data_ptr()), E, D->data_ptr(), dtype, cap, N, K,
-                                          st) == FP8DS_OK);
+    if (!a.ok) return done(false);
+    const auto *pa = static_cast<const uint8_t *>(A->data_ptr()), *pb = static_cast<const uint8_t *>(B->data_ptr());
+    const auto *po = static_cast<const int32_t *>(off->data_ptr());
+    void *pd = D->data_ptr();
+    return done_with(fp8_grouped_wgrad(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(0), po, E, pd, dtype, cap, N, K, st));
 }
 
 // PyTorch raises C++ exceptions for tensors without storage or strides, and where there is no GPU to

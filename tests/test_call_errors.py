@@ -1,6 +1,7 @@
 """The native module's calls on arguments that PyTorch itself refuses, on the CPU: an exception has to
-reach Python, not end the interpreter.  They run in a process of their own.  Fake tensors stand for
-GPU tensors: they say they are on the GPU and hold no memory."""
+reach Python, not end the interpreter, and a HIP error that an entry point reports has to reach it too,
+without a second call.  They run in a process of their own.  Fake tensors stand for GPU tensors: they
+say they are on the GPU and hold no memory."""
 import os
 import subprocess
 import sys
@@ -92,3 +93,39 @@ def test_streams_that_are_no_handle():
     assert len(out) == len(streams)
     for line in out:
         assert line.split()[1] in ("Fp8dsError", "AttributeError", "TypeError", "ValueError", "ArgumentError"), line
+
+
+ENTRIES = {name: ("fp8_norm_residual_" + name[5:] if name.startswith("norm") else "fp8_" + name) for name in CALLS}
+# Entry points that count their calls and report what they are told to; loaded for all, so that they take the library's place.
+STUB = "int status, calls;\n" + "".join(f"int {e}(void) {{ ++calls; return status; }}\n" for e in ENTRIES.values())
+
+
+def _stub(tmp_path):
+    (tmp_path / "stub.c").write_text(STUB)
+    out = str(tmp_path / "stub.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", out, str(tmp_path / "stub.c")], check=True)
+    return f"""
+import ctypes
+stub = ctypes.CDLL({out!r}, ctypes.RTLD_GLOBAL)
+status, calls = ctypes.c_int.in_dll(stub, "status"), ctypes.c_int.in_dll(stub, "calls")
+"""
+
+
+def test_a_hip_error_is_raised_and_the_call_is_not_made_again(tmp_path):
+    """An entry point that reports a HIP error may have launched: a second call would run it twice, and with
+    x in resid's buffer the first norm would be added twice."""
+    code = _stub(tmp_path) + TRY + "F._invoke = lambda *a: print('again', a[0], flush=True)\nstatus.value = -6\n"
+    code += "".join(f"attempt({name!r}, lambda: {call.format(s=0)})\n" for name, call in CALLS.items()) + "print(calls.value)\n"
+    out = _run(code)
+    assert out[-1] == str(len(CALLS)) and len(out) == len(CALLS) + 1, out
+    for line, name in zip(out, CALLS):
+        assert line.startswith(f"{name} Fp8dsError FP8DS_ERR_HIP"), line
+
+
+def test_a_refusal_is_left_to_the_bindings_checks(tmp_path):
+    code = _stub(tmp_path) + TRY + "F._invoke = lambda *a: print('again', a[0], flush=True)\n"
+    refusals = (-1, -2, -3, -4, -5, -7)
+    for value in (*refusals, 0):
+        code += f"status.value = {value}\nattempt('norm', lambda: {CALLS['norm_fwd'].format(s=0)})\n"
+    out = _run(code + "print(calls.value)\n")
+    assert out == ["again fp8_norm_residual_fwd", "norm returned"] * len(refusals) + ["norm returned", str(len(refusals) + 1)], out
