@@ -125,7 +125,13 @@ struct Args {
 };
 
 PyObject *done(bool ok) { return PyBool_FromLong(ok); }
-PyObject *done_with(int status) {
+// Makes the call with the interpreter's lock released, as ctypes does: a launch waits while the GPU's
+// queue is full.
+template <class Call> PyObject *done_with(Call call) {
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = call();
+    Py_END_ALLOW_THREADS
     if (status != FP8DS_ERR_HIP) return done(status == FP8DS_OK);
     PyObject *package = PyImport_ImportModule("fp8_delayed_scaling_amd");
     PyObject *never = package != nullptr ? PyObject_CallMethod(package, "_check", "i", status) : nullptr;      // raises
@@ -159,8 +165,10 @@ PyObject *norm_fwd(PyObject *const *args, Py_ssize_t n) {
     const float eps = a.real(18);
     const hipStream_t st = a.stream(19);
     if (!a.ok) return done(false);
-    return done_with(fp8_norm_residual_fwd(o, w_post, b_post, gate, G, resid, alpha, x, post, w_pre, b_pre, pre, h, h8,
-                                           scale, fmt, sinv, amax, kind, eps, M, H, st));
+    return done_with([&] {
+        return fp8_norm_residual_fwd(o, w_post, b_post, gate, G, resid, alpha, x, post, w_pre, b_pre, pre, h, h8, scale,
+                                     fmt, sinv, amax, kind, eps, M, H, st);
+    });
 }
 
 PyObject *norm_bwd(PyObject *const *args, Py_ssize_t n) {
@@ -189,8 +197,10 @@ PyObject *norm_bwd(PyObject *const *args, Py_ssize_t n) {
     void *ws = a.workspace(18, bytes);
     const hipStream_t st = a.stream(20);
     if (!a.ok) return done(false);
-    return done_with(fp8_norm_residual_bwd(dh, dx, o, w_post, b_post, gate, G, alpha, x, post, w_pre, pre, d_block, d_resid,
-                                           dw_post, db_post, dgate, dw_pre, db_pre, ws, bytes, kind, M, H, st));
+    return done_with([&] {
+        return fp8_norm_residual_bwd(dh, dx, o, w_post, b_post, gate, G, alpha, x, post, w_pre, pre, d_block, d_resid,
+                                     dw_post, db_post, dgate, dw_pre, db_pre, ws, bytes, kind, M, H, st);
+    });
 }
 
 PyObject *moe_plan(PyObject *const *args, Py_ssize_t n) {
@@ -206,7 +216,9 @@ PyObject *moe_plan(PyObject *const *args, Py_ssize_t n) {
     void *ws = a.workspace(6, bytes);
     const hipStream_t st = a.stream(7);
     if (!a.ok) return done(false);
-    return done_with(fp8_moe_plan(experts, T, k, E, align, cap, offsets, src, slot, ws, bytes, st));
+    return done_with([&] {
+        return fp8_moe_plan(experts, T, k, E, align, cap, offsets, src, slot, ws, bytes, st);
+    });
 }
 
 PyObject *moe_sort_cast(PyObject *const *args, Py_ssize_t n) {
@@ -223,7 +235,9 @@ PyObject *moe_sort_cast(PyObject *const *args, Py_ssize_t n) {
     auto *sinv = a.some<float>(8, kF32, 1), *amax = a.some<float>(9, kF32, 1);
     const hipStream_t st = a.stream(10);
     if (!a.ok) return done(false);
-    return done_with(fp8_moe_sort_cast(x, T, src, cap, top, w, scale, fmt, out, out_t, sinv, amax, H, st));
+    return done_with([&] {
+        return fp8_moe_sort_cast(x, T, src, cap, top, w, scale, fmt, out, out_t, sinv, amax, H, st);
+    });
 }
 
 PyObject *moe_sort_codes(PyObject *const *args, Py_ssize_t n) {
@@ -236,7 +250,9 @@ PyObject *moe_sort_codes(PyObject *const *args, Py_ssize_t n) {
     auto *out = a.dense<uint8_t>(3, kU8, {cap, H}, true), *out_t = a.dense<uint8_t>(4, kU8, {H, cap});
     const hipStream_t st = a.stream(5);
     if (!a.ok) return done(false);
-    return done_with(fp8_moe_sort_codes(x, T, src, cap, top, out, out_t, H, st));
+    return done_with([&] {
+        return fp8_moe_sort_codes(x, T, src, cap, top, out, out_t, H, st);
+    });
 }
 
 PyObject *moe_combine(PyObject *const *args, Py_ssize_t n) {
@@ -250,7 +266,9 @@ PyObject *moe_combine(PyObject *const *args, Py_ssize_t n) {
     auto *y = a.dense<uint16_t>(3, kBf16, {T, H}, true);
     const hipStream_t st = a.stream(4);
     if (!a.ok) return done(false);
-    return done_with(fp8_moe_combine(ys, cap, slot, w, T, k, y, H, st));
+    return done_with([&] {
+        return fp8_moe_combine(ys, cap, slot, w, T, k, y, H, st);
+    });
 }
 
 PyObject *moe_weight_grad(PyObject *const *args, Py_ssize_t n) {
@@ -264,7 +282,9 @@ PyObject *moe_weight_grad(PyObject *const *args, Py_ssize_t n) {
     auto *dw = a.dense<float>(3, kF32, {T, k}, true);
     const hipStream_t st = a.stream(4);
     if (!a.ok) return done(false);
-    return done_with(fp8_moe_weight_grad(dy, ys, cap, slot, T, k, dw, H, st));
+    return done_with([&] {
+        return fp8_moe_weight_grad(dy, ys, cap, slot, T, k, dw, H, st);
+    });
 }
 
 // Output of the experts' products: its type, with unit stride along the rows.
@@ -291,8 +311,10 @@ PyObject *grouped_gemm(PyObject *const *args, Py_ssize_t n) {
     if (!a.ok) return done(false);
     const auto *pa = static_cast<const uint8_t *>(A->data_ptr()), *pb = static_cast<const uint8_t *>(B->data_ptr());
     void *pd = D->data_ptr();
-    return done_with(fp8_grouped_gemm(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(1), B->stride(0), off, E, pd, D->stride(0),
-                                      dtype, cap, N, K, st));
+    return done_with([&] {
+        return fp8_grouped_gemm(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(1), B->stride(0), off, E, pd,
+                                D->stride(0), dtype, cap, N, K, st);
+    });
 }
 
 PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
@@ -311,7 +333,9 @@ PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
     const auto *pa = static_cast<const uint8_t *>(A->data_ptr()), *pb = static_cast<const uint8_t *>(B->data_ptr());
     const auto *po = static_cast<const int32_t *>(off->data_ptr());
     void *pd = D->data_ptr();
-    return done_with(fp8_grouped_wgrad(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(0), po, E, pd, dtype, cap, N, K, st));
+    return done_with([&] {
+        return fp8_grouped_wgrad(pa, fa, sa, A->stride(0), pb, fb, sb, B->stride(0), po, E, pd, dtype, cap, N, K, st);
+    });
 }
 
 // PyTorch raises C++ exceptions for tensors without storage or strides, and where there is no GPU to

@@ -129,3 +129,30 @@ def test_a_refusal_is_left_to_the_bindings_checks(tmp_path):
         code += f"status.value = {value}\nattempt('norm', lambda: {CALLS['norm_fwd'].format(s=0)})\n"
     out = _run(code + "print(calls.value)\n")
     assert out == ["again fp8_norm_residual_fwd", "norm returned"] * len(refusals) + ["norm returned", str(len(refusals) + 1)], out
+
+
+def test_other_threads_run_during_a_call(tmp_path):
+    """A launch may wait for the GPU: the entry point here waits, at most two seconds, for another thread."""
+    (tmp_path / "wait.c").write_text("""
+#include <unistd.h>
+volatile int flag, seen;
+int fp8_moe_combine(void) {
+    for (int i = 0; i < 2000 && !flag; ++i) usleep(1000);
+    seen = flag;
+    return 0;
+}
+""")
+    lib = str(tmp_path / "wait.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", lib, str(tmp_path / "wait.c")], check=True)
+    out = _run(f"""
+import ctypes, threading
+stub = ctypes.CDLL({lib!r}, ctypes.RTLD_GLOBAL)
+flag, seen = ctypes.c_int.in_dll(stub, "flag"), ctypes.c_int.in_dll(stub, "seen")
+other = threading.Timer(0.05, lambda: setattr(flag, "value", 1))
+other.start()
+with mode:
+    {CALLS["moe_combine"].format(s=0)}
+print(seen.value)
+other.join()
+""")
+    assert out == ["1"]
