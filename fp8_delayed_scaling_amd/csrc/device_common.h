@@ -122,6 +122,11 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
            (encode_exact<FMT>(d) << 24);
 }
 
+// The s_waitcnt operand that waits for all but the last n vector memory accesses and for nothing else:
+// the count's six bits lie in two places (0-3 and 14-15), the bits between them are other counters'.
+constexpr int waitcnt_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
+constexpr int vm_of_waitcnt(int w) { return (w & 0xF) | ((w >> 14) << 4); }
+
 // float32 -> bfloat16, round to nearest even, by the hardware conversion (gfx950 converts two
 // values per instruction).  A NaN stays a NaN; its payload is not specified.
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));

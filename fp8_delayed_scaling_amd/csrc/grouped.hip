@@ -47,7 +47,7 @@ constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds ch
 
 // vmcnt-only wait, and a workgroup barrier without a fence (a fenced one would wait for every load
 // in flight); the empty asm statements keep memory accesses on their side.
-#define FP8DS_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(0xF70 | ((n) & 0xF) | (((n) >> 4) << 14))
+#define FP8DS_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(waitcnt_vm(n))
 #define FP8DS_WAIT_LGKM() __builtin_amdgcn_s_waitcnt(0xC07F)
 #define FP8DS_WAIT_ALL() __builtin_amdgcn_s_waitcnt(0x0070)     // vmcnt(0) lgkmcnt(0)
 #define FP8DS_BARRIER()                          \

@@ -337,8 +337,10 @@ struct RowInput {
 template <int V>
 __device__ __forceinline__ void wait_inputs(int later) {
     auto wait = [](auto n) {
+        constexpr int kVm = waitcnt_vm(decltype(n)::value);
+        static_assert(vm_of_waitcnt(kVm) == decltype(n)::value);     // 18 for three inputs of six loads
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xF70 | decltype(n)::value);      // vmcnt(n), n < 16
+        __builtin_amdgcn_s_waitcnt(kVm);
         asm volatile("" ::: "memory");
     };
     if (later == 3) wait(std::integral_constant<int, 3 * V>{});
