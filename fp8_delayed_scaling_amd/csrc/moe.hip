@@ -214,10 +214,10 @@ __device__ __forceinline__ uint32_t amax4(uint32_t acc, float a, float b, float 
 
 // Row-major output only: TX threads per row, 16 columns each step.
 template <int WHAT>
-__global__ __launch_bounds__(256) void k_moe_rows(const MoeSort a, int tx_log2) {
+__global__ __launch_bounds__(256) void k_moe_rows(const MoeSort a, int tx_log2, int64_t first) {
     __shared__ uint32_t red[4];
     const int tx = threadIdx.x & ((1 << tx_log2) - 1), ty = threadIdx.x >> tx_log2;
-    const int64_t row = ((int64_t)blockIdx.x << (8 - tx_log2)) + ty;
+    const int64_t row = ((first + blockIdx.x) << (8 - tx_log2)) + ty;
     constexpr bool kCast = WHAT == kSortE4M3 || WHAT == kSortE5M2;
     constexpr int FMT = WHAT == kSortE5M2 ? kE5M2 : kE4M3;
     float s = 0.f;
@@ -282,13 +282,13 @@ __global__ __launch_bounds__(256) void k_moe_rows(const MoeSort a, int tx_log2) 
 // LDS (slot rb of transposed row c at rb ^ (c / 8): conflict-free writes, 16-byte reads), as the
 // cast + transpose kernel does; here the tile's rows come from the tokens that src names.
 template <int WHAT, int TS>
-__global__ __launch_bounds__((TS / 8) * (TS / 8)) void k_moe_sort_t(const MoeSort a, int tiles_c) {
+__global__ __launch_bounds__((TS / 8) * (TS / 8)) void k_moe_sort_t(const MoeSort a, int tiles_c, int first) {
     constexpr int NRB = TS / 8, NT = NRB * NRB, CH = TS / 16;
     constexpr int FMT = WHAT == kSortE5M2 ? kE5M2 : kE4M3;
     __shared__ __align__(16) uint8_t tT[TS * TS];
     __shared__ uint32_t red[NT / 64];
     const int t = threadIdx.x, rb = t / NRB, cb = t % NRB;
-    const int tile_r = blockIdx.x / tiles_c, tile_c = blockIdx.x - tile_r * tiles_c;
+    const int tile = first + (int)blockIdx.x, tile_r = (uint32_t)tile / (uint32_t)tiles_c, tile_c = tile - tile_r * tiles_c;
     const int64_t r0 = (int64_t)tile_r * TS, row = r0 + rb * 8;
     const int c0 = tile_c * TS, col = c0 + cb * 8;
     const int H = a.width;
@@ -392,9 +392,9 @@ __global__ __launch_bounds__((TS / 8) * (TS / 8)) void k_moe_sort_t(const MoeSor
 template <bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t *__restrict__ ys, const int32_t *__restrict__ slot,
                                                      const float *__restrict__ weights, uint16_t *__restrict__ y,
-                                                     int64_t T, int k, int H, int64_t cap, int tx_log2) {
+                                                     int64_t T, int k, int H, int64_t cap, int tx_log2, int64_t first) {
     const int tx = threadIdx.x & ((1 << tx_log2) - 1), ty = threadIdx.x >> tx_log2;
-    const int64_t tok = ((int64_t)blockIdx.x << (8 - tx_log2)) + ty;
+    const int64_t tok = ((first + blockIdx.x) << (8 - tx_log2)) + ty;
     if (tok >= T) return;
     for (int c = tx; c < (H >> 3); c += 1 << tx_log2) {
         float acc[8];
@@ -434,9 +434,9 @@ __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t *__restrict_
 // Weights' gradient: one wave per choice.
 __global__ __launch_bounds__(256) void k_moe_weight_grad(const uint16_t *__restrict__ dy, const uint16_t *__restrict__ ys,
                                                          const int32_t *__restrict__ slot, float *__restrict__ dweights,
-                                                         int64_t n, int k, int H, int64_t cap) {
+                                                         int64_t n, int k, int H, int64_t cap, int64_t first) {
     const int lane = threadIdx.x & 63;
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t i = (first + blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (i >= n) return;
     const int32_t p = slot[i];
     float acc = 0.f;
@@ -465,6 +465,18 @@ int row_threads_log2(int64_t pieces) {
     return l;
 }
 constexpr int64_t kSortBigTiles = 256;    // 256 x 256 tiles from one per CU on, else 64 x 64
+
+// A launch numbers its threads in 32 bits, and one of more runs what is left modulo 2^32 without an
+// error: larger grids go in pieces, each told its first block.
+constexpr int64_t kMostThreads = INT64_C(1) << 31;
+template <class Launch> hipError_t in_pieces(int64_t blocks, int threads, Launch launch) {
+    const int64_t most = kMostThreads / threads;
+    for (int64_t first = 0; first < blocks; first += most) {
+        launch(dim3((unsigned)(blocks - first < most ? blocks - first : most)), first);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 }  // namespace
 
 hipError_t launch_moe_sort(const MoeSort &a, int what, hipStream_t st) {
@@ -472,47 +484,48 @@ hipError_t launch_moe_sort(const MoeSort &a, int what, hipStream_t st) {
         const int64_t big = ((a.cap + 255) / 256) * (((int64_t)a.width + 255) / 256);
         const int ts = big >= kSortBigTiles ? 256 : 64;
         const int tiles_c = (a.width + ts - 1) / ts;
-        const dim3 grid((unsigned)((a.cap + ts - 1) / ts * tiles_c));
+        return in_pieces((a.cap + ts - 1) / ts * tiles_c, ts == 256 ? 1024 : 64, [&](dim3 grid, int64_t first) {
 #define FP8DS_SORT_T(W_)                                                                                   \
     do {                                                                                                   \
-        if (ts == 256) k_moe_sort_t<W_, 256><<<grid, 1024, 0, st>>>(a, tiles_c);                           \
-        else k_moe_sort_t<W_, 64><<<grid, 64, 0, st>>>(a, tiles_c);                                        \
+        if (ts == 256) k_moe_sort_t<W_, 256><<<grid, 1024, 0, st>>>(a, tiles_c, (int)first);               \
+        else k_moe_sort_t<W_, 64><<<grid, 64, 0, st>>>(a, tiles_c, (int)first);                            \
     } while (0)
-        switch (what) {
-            case kSortCodes: FP8DS_SORT_T(kSortCodes); break;
-            case kSortE4M3: FP8DS_SORT_T(kSortE4M3); break;
-            default: FP8DS_SORT_T(kSortE5M2); break;
-        }
+            switch (what) {
+                case kSortCodes: FP8DS_SORT_T(kSortCodes); break;
+                case kSortE4M3: FP8DS_SORT_T(kSortE4M3); break;
+                default: FP8DS_SORT_T(kSortE5M2); break;
+            }
 #undef FP8DS_SORT_T
-        return hipGetLastError();
+        });
     }
     const int l = row_threads_log2(a.width >> 4);
-    const dim3 grid((unsigned)((a.cap + (256 >> l) - 1) / (256 >> l)));
-    switch (what) {
-        case kSortCodes: k_moe_rows<kSortCodes><<<grid, 256, 0, st>>>(a, l); break;
-        case kSortE4M3: k_moe_rows<kSortE4M3><<<grid, 256, 0, st>>>(a, l); break;
-        case kSortE5M2: k_moe_rows<kSortE5M2><<<grid, 256, 0, st>>>(a, l); break;
-        default: k_moe_rows<kSortBf16><<<grid, 256, 0, st>>>(a, l); break;
-    }
-    return hipGetLastError();
+    return in_pieces((a.cap + (256 >> l) - 1) / (256 >> l), 256, [&](dim3 grid, int64_t first) {
+        switch (what) {
+            case kSortCodes: k_moe_rows<kSortCodes><<<grid, 256, 0, st>>>(a, l, first); break;
+            case kSortE4M3: k_moe_rows<kSortE4M3><<<grid, 256, 0, st>>>(a, l, first); break;
+            case kSortE5M2: k_moe_rows<kSortE5M2><<<grid, 256, 0, st>>>(a, l, first); break;
+            default: k_moe_rows<kSortBf16><<<grid, 256, 0, st>>>(a, l, first); break;
+        }
+    });
 }
 
 hipError_t launch_moe_combine(const uint16_t *ys, const int32_t *slot, const float *weights, uint16_t *y, int64_t T,
                               int64_t k, int64_t width, int64_t cap, hipStream_t st) {
     const int l = row_threads_log2(width >> 3);
-    const dim3 grid((unsigned)((T + (256 >> l) - 1) / (256 >> l)));
-    if (weights != nullptr)
-        k_moe_combine<true><<<grid, 256, 0, st>>>(ys, slot, weights, y, T, (int)k, (int)width, cap, l);
-    else
-        k_moe_combine<false><<<grid, 256, 0, st>>>(ys, slot, weights, y, T, (int)k, (int)width, cap, l);
-    return hipGetLastError();
+    return in_pieces((T + (256 >> l) - 1) / (256 >> l), 256, [&](dim3 grid, int64_t first) {
+        if (weights != nullptr)
+            k_moe_combine<true><<<grid, 256, 0, st>>>(ys, slot, weights, y, T, (int)k, (int)width, cap, l, first);
+        else
+            k_moe_combine<false><<<grid, 256, 0, st>>>(ys, slot, weights, y, T, (int)k, (int)width, cap, l, first);
+    });
 }
 
 hipError_t launch_moe_weight_grad(const uint16_t *dy, const uint16_t *ys, const int32_t *slot, float *dweights,
                                   int64_t T, int64_t k, int64_t width, int64_t cap, hipStream_t st) {
     const int64_t n = T * k;
-    k_moe_weight_grad<<<dim3((unsigned)((n + 3) / 4)), 256, 0, st>>>(dy, ys, slot, dweights, n, (int)k, (int)width, cap);
-    return hipGetLastError();
+    return in_pieces((n + 3) / 4, 256, [&](dim3 grid, int64_t first) {
+        k_moe_weight_grad<<<grid, 256, 0, st>>>(dy, ys, slot, dweights, n, (int)k, (int)width, cap, first);
+    });
 }
 
 }  // namespace fp8ds
