@@ -32,10 +32,14 @@ inline bool size_ok(int64_t rows, int64_t cols) {
     return rows <= (INT64_C(1) << 40) / cols;
 }
 
-// The cast kernels take one 256 x 256 tile per workgroup, numbered in 32 bits; a launch holds at
-// most two tensors.
-inline bool ct_tiles_ok(int64_t rows, int64_t cols) {
-    return ((rows + 255) / 256) * ((cols + 255) / 256) <= INT_MAX / 2;
+// A launch numbers its threads in 32 bits, and one of more runs what is left modulo 2^32 without an
+// error: sizes that would need it are refused.
+constexpr int64_t kMostThreads = (INT64_C(1) << 32) - 1;
+inline int64_t tiles256(int64_t rows, int64_t cols) { return ((rows + 255) / 256) * ((cols + 255) / 256); }
+
+// The cast kernels take one 256 x 256 tile per workgroup of 1024 threads; a launch holds one tensor or two.
+inline bool ct_tiles_ok(int64_t rows, int64_t cols, int tensors = 1) {
+    return tiles256(rows, cols) <= kMostThreads / 1024 / tensors;
 }
 
 int check_cast_common(const uint16_t *x, const float *scale, int fmt, const uint8_t *out, const float *sinv,
@@ -53,7 +57,8 @@ int check_gemm(const uint8_t *A, int fa, const float *a_sinv, int64_t lda, const
     if (!valid_fmt(fa) || !valid_fmt(fb) || out_dtype < 0 || out_dtype > kOutE5M2) return FP8DS_ERR_FORMAT;
     if (M < 0 || N < 0 || K < 0 || M > INT_MAX || N > INT_MAX || K > INT_MAX) return FP8DS_ERR_SHAPE;
     if (K % 16 != 0) return FP8DS_ERR_SHAPE;
-    if (((M + 255) / 256) * ((N + 255) / 256) > INT_MAX) return FP8DS_ERR_SHAPE;
+    if (tiles256(M, N) > kMostThreads / 256) return FP8DS_ERR_SHAPE;
+    if (K == 0 && M * N > kMostThreads) return FP8DS_ERR_SHAPE;        // a thread for each output
     if (M == 0 || N == 0) return FP8DS_OK;
     if (D == nullptr) return FP8DS_ERR_NULL;
     if (K > 0 && (A == nullptr || B == nullptr || a_sinv == nullptr || b_sinv == nullptr)) return FP8DS_ERR_NULL;
@@ -152,7 +157,7 @@ size_t fp8_dbias_workspace_bytes(int64_t rows, int64_t cols) {
 int fp8_dbias_cast_transpose(const uint16_t *dy, int64_t rows, int64_t cols, const float *scale, int fmt,
                              uint8_t *out, uint8_t *out_t, float *scale_inv_out, float *amax_slot, float *dbias,
                              void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    if (!size_ok(rows, cols) || !ct_tiles_ok(rows, cols)) return FP8DS_ERR_SHAPE;
+    if (!size_ok(rows, cols) || !ct_tiles_ok(rows > 0 ? rows : 1, cols)) return FP8DS_ERR_SHAPE;
     if (!valid_fmt(fmt)) return FP8DS_ERR_FORMAT;
     if (cols == 0) return FP8DS_OK;
     if (dbias == nullptr) return FP8DS_ERR_NULL;
@@ -211,7 +216,7 @@ int fp8_transpose(const uint8_t *in, int64_t rows, int64_t cols, uint8_t *out_t,
                   hipStream_t stream) {
     if (!size_ok(rows, cols)) return FP8DS_ERR_SHAPE;
     if (rows == 0 || cols == 0) return FP8DS_OK;
-    if (((rows + 255) / 256) * ((cols + 255) / 256) > INT_MAX) return FP8DS_ERR_SHAPE;
+    if (tiles256(rows, cols) > kMostThreads / 256) return FP8DS_ERR_SHAPE;
     if (in == nullptr || out_t == nullptr) return FP8DS_ERR_NULL;
     if (noop && !aligned4(noop)) return FP8DS_ERR_ALIGN;
     return hip_status(fp8ds::launch_fp8_transpose(in, rows, cols, out_t, noop, stream));
@@ -261,7 +266,7 @@ int fp8_linear_fwd(const uint16_t *x, const uint16_t *w, const uint16_t *bias, i
                    const float *w_scale, float *w_amax, uint8_t *w8, uint8_t *w8_t, float *w_scale_inv,
                    const float *w_noop, uint16_t *y, hipStream_t stream) {
     if (M < 0 || N < 0 || K < 0 || !size_ok(M, K) || !size_ok(N, K) || !size_ok(M, N)) return FP8DS_ERR_SHAPE;
-    if (!ct_tiles_ok(M, K) || !ct_tiles_ok(N, K)) return FP8DS_ERR_SHAPE;
+    if (!ct_tiles_ok(M, K, 2) || !ct_tiles_ok(N, K, 2)) return FP8DS_ERR_SHAPE;
     if (K % 16 != 0) return FP8DS_ERR_SHAPE;
     if (M == 0 || N == 0) return FP8DS_OK;
     if (y == nullptr || x_scale_inv == nullptr || w_scale_inv == nullptr) return FP8DS_ERR_NULL;

@@ -21,7 +21,8 @@
  *   - Device pointers must be 16-byte aligned unless a call's comment says otherwise.
  *   - Scales live on the device (float32 scalars), so no call reads them on the host.
  *   - Return value: FP8DS_OK (0) or a negative fp8ds_status.  Arguments are checked on the
- *     host before anything is launched; a rejected call launches nothing.  After launching,
+ *     host before anything is launched; a rejected call launches nothing.  A size that would
+ *     need 2^32 threads in one launch counts as a wrong shape.  After launching,
  *     a HIP launch error is reported as FP8DS_ERR_HIP (no synchronisation is done, so faults
  *     inside kernels surface at the caller's next synchronisation).
  *   - Numerical trouble (zero, subnormal, infinite or NaN amax) is not an error: the scale
