@@ -144,9 +144,11 @@ struct TeamSum {
     }
 };
 
-// Mean and 1 / standard deviation of the row in v (columns past the width hold zero).
+// Mean and 1 / standard deviation of the row in v, whose columns past the width hold zero; v becomes its
+// deviations from the mean, and those columns stay zero: an infinite (0 - mean) * rstd there would turn
+// the next norm's sums into NaN.
 template <int TPR, int V, bool VEC, bool LN>
-__device__ __forceinline__ void row_stats(const float (&v)[8 * V], int H, int t, float eps, TeamSum<TPR> &sum,
+__device__ __forceinline__ void row_stats(float (&v)[8 * V], int H, int t, float eps, TeamSum<TPR> &sum,
                                           float &rstd, float &mean) {
     const float inv = 1.0f / (float)H;
     mean = 0.f;
@@ -159,8 +161,8 @@ __device__ __forceinline__ void row_stats(const float (&v)[8 * V], int H, int t,
         mean = s * inv;
 #pragma unroll
         for (int i = 0; i < 8 * V; ++i) {
-            const float d = Row<TPR, V, VEC>::col(t, i) < H ? v[i] - mean : 0.f;
-            ss += d * d;
+            v[i] = Row<TPR, V, VEC>::col(t, i) < H ? v[i] - mean : 0.f;
+            ss += v[i] * v[i];
         }
     } else {
 #pragma unroll
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const NormFw
                 }
 #pragma unroll
                 for (int i = 0; i < 8 * V; ++i) {
-                    v[i] = (v[i] - mean) * rstd * R::get(wr, i);
+                    v[i] = v[i] * rstd * R::get(wr, i);
                     if constexpr (LN) if (a.b_post != nullptr) v[i] += R::get(br, i);
                 }
             }
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const NormFw
         }
 #pragma unroll
         for (int i = 0; i < 8 * V; ++i) {
-            v[i] = (v[i] - mean) * rstd * R::get(wr, i);
+            v[i] = v[i] * rstd * R::get(wr, i);
             if constexpr (LN) if (a.b_pre != nullptr) v[i] += R::get(br, i);
         }
         if (a.h != nullptr) {
@@ -308,6 +310,15 @@ __device__ __forceinline__ float scalar_at(const float *p, int64_t i) {
     return reinterpret_cast<const __attribute__((address_space(4))) float *>(reinterpret_cast<uint64_t>(p))[i];
 }
 __device__ __forceinline__ float bf16_of(const u32x4 &q, int i) { return (i & 1) ? bf16_hi(q[i >> 1]) : bf16_lo(q[i >> 1]); }
+
+// A column's mean: zero past the width, where the row was loaded as zero, so that its normalised value
+// is zero too ((0 - mean) * rstd may be infinite, and its product with a zero NaN).  The launcher gives
+// rows of two chunks a thread and more to teams that they fill at least half: no bound to compare there.
+template <int TPR, int V, bool VEC, bool LN>
+__device__ __forceinline__ float mean_of(float mean, int H, int t, int v, int i) {
+    if (!LN || 2 * (v + 1) <= V) return mean;
+    return Row<TPR, V, VEC>::col(t, 8 * v + (VEC ? 0 : i)) < H ? mean : 0.f;
+}
 
 // One of a row's inputs: chunk v of the thread in LDS or in registers.
 template <int TPR, int V, bool VEC>
@@ -411,6 +422,8 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(const NormBwd a) {
             // opaque in every row: the weights stay packed, two to a register
 #pragma unroll
             for (int j = 0; j < 4 * V; ++j) asm volatile("" : "+v"(wq[j]), "+v"(wp[j]), "+v"(gr[j]));
+            int tc = t;                       // opaque too: the columns' bounds are compared anew, not kept
+            if constexpr (LN) asm volatile("" : "+v"(tc));
             float d[8 * V];
             if (a.dh != nullptr) {
                 const float rstd = scalar_at(a.pre_stats, row), mean = LN ? scalar_at(a.pre_stats, a.rows + row) : 0.f;
@@ -422,7 +435,7 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(const NormBwd a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int k = 8 * v + i;
-                        const float dy = bf16_of(dq, i), hat = (bf16_of(xq, i) - mean) * rstd;
+                        const float dy = bf16_of(dq, i), hat = (bf16_of(xq, i) - mean_of<TPR, V, VEC, LN>(mean, H, tc, v, i)) * rstd;
                         d[k] = dy * R::get(wq, k);          // zero past the width
                         p1[k] += dy * hat;
                         if constexpr (LN) { p0[k] += dy; m0 += d[k]; }
@@ -437,7 +450,7 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(const NormBwd a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int k = 8 * v + i;
-                        const float hat = (bf16_of(xq, i) - mean) * rstd;
+                        const float hat = (bf16_of(xq, i) - mean_of<TPR, V, VEC, LN>(mean, H, tc, v, i)) * rstd;
                         d[k] = rstd * (d[k] - m0 - hat * m1);
                     }
                 }
@@ -477,7 +490,7 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(const NormBwd a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int k = 8 * v + i;
-                        const float hat = (bf16_of(q, i) - mean) * rstd;
+                        const float hat = (bf16_of(q, i) - mean_of<TPR, V, VEC, LN>(mean, H, tc, v, i)) * rstd;
                         s1[k] += d[k] * hat;
                         if constexpr (LN) s0[k] += d[k];
                         d[k] = d[k] * R::get(gr, k) * R::get(wp, k);      // zero past the width
@@ -493,7 +506,7 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(const NormBwd a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int k = 8 * v + i;
-                        const float hat = (bf16_of(q, i) - mean) * rstd;
+                        const float hat = (bf16_of(q, i) - mean_of<TPR, V, VEC, LN>(mean, H, tc, v, i)) * rstd;
                         d[k] = rstd * (d[k] - m0 - hat * m1);
                     }
                 }
