@@ -7,8 +7,9 @@
 // what is wrong.  A HIP error may come after a launch, so that call is not made again: it raises the
 // binding's error from here.
 //
-// What it saves: a four-row norm takes 27 arguments, which ctypes and the checks in Python took
-// 10.2 us for, the launch included; the kernel runs 4.3.
+// What it saves: a four-row norm takes 20 arguments, which ctypes and the checks in Python took 10.2 us
+// for, the launch included; here the whole call takes 4.0 us on the host, 0.4 of them for the arguments,
+// and the kernel runs 4.2.
 #include <hip/hip_runtime_api.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>

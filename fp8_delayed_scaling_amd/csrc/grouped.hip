@@ -15,9 +15,9 @@
 //   Wide    up to 256 rows of A by 256 rows of B, one block on each CU: the fewest bytes per product
 //   Paired  up to 128 rows by 256, two blocks on each CU, which fill each other's waits: for short
 //           contractions, small problems and few rows per expert
-// Measured: 64 experts, [2048, 4096], 32768 rows: evenly routed forward 230 us (2.4 PFLOP/s; a dense
-// product of that size 212), unevenly 264-282 (2.0, bound by the products and by the 537 MB of
-// weights in turn), weight gradient 495-535 (1.07 GB of output), 64 rows 54 us (341 MB, 6.3 TB/s).
+// Measured: 64 experts, [2048, 4096], 32768 rows: evenly routed forward 239 us (2.3 PFLOP/s; a dense
+// product of that size 197), unevenly 262-268 (2.1, bound by the products and by the 537 MB of
+// weights in turn), weight gradient 496-504 (1.07 GB of output), 64 rows 54-57 us (341 MB, 6.2 TB/s).
 // An expert's rows are shared evenly among its tiles, in steps of 32 (16 for each row of waves); a
 // tile runs only the 16-row blocks it has.  All loads are buffer loads into LDS whose bound is the
 // tile's extent: rows past it, and the 16-byte pieces past K (their offset is moved out of the bound),
@@ -104,11 +104,10 @@ __device__ __forceinline__ int wave_scan(int v) {
 // Among 64 experts, tall tiles come first (in every expert all tiles but the last have one height).
 // The tiles are taken in rounds, runs of 8 (single ones, where an XCD has fewer blocks) dealt to the
 // XCDs forwards and backwards in turn, a run to blocks of one XCD: they share B's rows, which come
-// from HBM once, and A's.  Every block so
-// takes a like mixture of heights, and half of the blocks take theirs from the last round to the
-// first: tall tiles, bound by the products, run beside low ones, bound by B's bytes.  (Unevenly
-// routed forward of 64 experts, half of which have under 1 % of the rows: in the experts' order
-// 330 us, tall tiles first 286, this way 275; evenly routed 230.)
+// from HBM once, and A's.  Every block so takes a like mixture of heights, and half of the blocks take
+// theirs from the last round to the first: tall tiles, bound by the products, run beside low ones, bound
+// by B's bytes.  (Unevenly routed forward of 64 experts, half of which have under 1 % of the rows, when
+// this was chosen: in the experts' order 330 us, tall tiles first 286, this way 275.)
 template <int OUT>
 struct RowTiles {
     const Grouped &g;
@@ -611,7 +610,7 @@ struct Paired : Work<FA, FB, OUT, STREAM> {
         auto step = [&](int j, uint8_t *b) {
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("" ::: "memory");
-            FP8DS_WAIT_VM(8);                                // all but B_{j+1}
+            FP8DS_WAIT_VM(8);                                // in flight: B_{j+1}, or stores of the tile before
             FP8DS_BARRIER();
             __builtin_amdgcn_sched_barrier(0);
             i32x8 fa[NB], fb[8];

@@ -16,8 +16,9 @@
 // operand) from the same pass.  8192 tokens x 4 choices, width 4096: codes sorted with their
 // transpose 58 us for 302 MB (5.2 TB/s, what a plain copy reaches), combine 61 us for 336 MB; 5000 x
 // 6, width 2048: weighted FP8 gradients with their transpose 40 us, the weights' gradient 28 us; the
-// plan of 32768 choices 4.7 + 4.9 us, of 32 choices 3.7, launches and latency.  Indices are checked in the kernels: a src or slot out of range
-// counts as -1, so no content of the index buffers makes an access out of bounds.
+// plan of 32768 choices 4.7 + 4.9 us, of 32 choices 3.7, launches and latency.  Indices are checked in
+// the kernels: a src or slot out of range counts as -1, so no content of the index buffers makes an
+// access out of bounds.
 #include "../../include/fp8ds.h"
 #include "device_common.h"
 #include "launch.h"

@@ -176,8 +176,9 @@ __device__ __forceinline__ void row_stats(float (&v)[8 * V], int H, int t, float
 
 // ------------------------------------------------------------------------------------------
 // Forward: a team per row, rows taken in a grid-stride loop.  Bound by HBM: [8192, 4096] RMS with
-// bfloat16 and FP8 output 65.5 us for 302 MB (4.6 TB/s; a plain copy 5.2), [2051, 1001] layer norm
-// 9.4 us (20.5 with one column at a time), four rows of 4096 4.2 us, two row sums' latency.
+// bfloat16 and FP8 output 65.6 us for 302 MB (4.6 TB/s; a plain copy 5.1), [2051, 1001] layer norm
+// 9.3 us (20.5 with one column at a time; its teams of one wave are two on a SIMD, which hide little of
+// two dependent sums a norm), four rows of 4096 4.2 us, two row sums' latency.
 // ------------------------------------------------------------------------------------------
 template <int TPR, int V, bool VEC, bool LN, int FMT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const NormFwd a) {
@@ -302,7 +303,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const NormFw
 // the next row's as soon as this row's are used, so that a block per CU keeps HBM busy across the
 // two sums that every row waits for.  Other widths are loaded into registers.  ([2048, 12288]
 // layer norm: the kernel and k_norm_cols took 303 + 33 us with five column sums, spilled registers
-// and no loads ahead; they take 88 + 19 us.)
+// and no loads ahead; they take 85 + 19 us.)  The waits count loads only: the stores issued between
+// them make each wait stricter than the load it is for.
+//
+// Forms that spill registers, with bytes of scratch a thread (VEC / other widths): layer norms past
+// 8192 columns (0 / 484) and past 12288 (236 / 420), RMS norms there (0 / 68, 0 / 400); with MULTI layer
+// norms past 4096 (12 / 160), 8192 (448 / 1244) and 12288 (440 / 652), RMS norms past 8192 (0 / 124) and
+// 12288 (160 / 588).
 // ------------------------------------------------------------------------------------------
 namespace {
 // Uniform statistics by scalar loads: nothing waits behind the row loads and stores in flight.
@@ -685,7 +692,8 @@ hipError_t launch_norm_bwd(NormBwd a, int layer, int64_t n_gates, void *ws, hipS
         else k_norm_bwd<TPR, V, false, LN, false><<<grid, TPR, 0, st>>>(a);                                \
     } while (0)
     // the widest rows: teams whose column sums stay in registers (layer norms keep twice as many:
-    // [2048, 12288] 110 us with 256 threads, 128 with 768; rms norms 91 and 84)
+    // [2048, 12288] 110 us with 256 threads, 128 with 768; rms norms 91 and 84).  Two chunks a thread and
+    // more only for widths past half of the team's columns, which the kernel builds on.
     if (a.rows == 0) {}
     else if (a.width <= 512) { if (layer) FP8DS_NB(true, 64, 1); else FP8DS_NB(false, 64, 1); }
     else if (a.width <= 1024) { if (layer) FP8DS_NB(true, 128, 1); else FP8DS_NB(false, 128, 1); }
