@@ -28,6 +28,8 @@ __all__ = [
     "NORM_RMS", "NORM_LAYER", "fp8_norm_residual_fwd", "fp8_norm_residual_workspace_bytes", "fp8_norm_residual_bwd",
     "fp8_moe_capacity", "fp8_moe_workspace_bytes", "fp8_moe_plan", "fp8_moe_sort_cast", "fp8_moe_sort_codes",
     "fp8_moe_sort_bf16", "fp8_moe_combine", "fp8_moe_weight_grad", "fp8_grouped_gemm", "fp8_grouped_wgrad",
+    "fp8_attention_workspace_bytes", "fp8_attention_fwd", "fp8_attention_bwd_workspace_bytes", "fp8_attention_bwd",
+    "fp8_moe_route_workspace_bytes", "fp8_moe_route", "fp8_moe_route_bwd",
 ]
 
 E4M3 = 0
@@ -56,6 +58,13 @@ I32 = ctypes.c_int32
 F32 = ctypes.c_float
 INT = ctypes.c_int
 SZ = ctypes.c_size_t
+
+
+
+class _Heads(ctypes.Structure):
+    """fp8ds_heads: tokens of heads, strides in elements."""
+    _fields_ = [("data", P), ("token_stride", I64), ("head_stride", I64)]
+
 
 _SIGS = {
     "fp8ds_status_string": ([INT], ctypes.c_char_p),
@@ -86,6 +95,13 @@ _SIGS = {
     "fp8_moe_weight_grad": ([P, P, I64, P, I64, I64, P, I64, P], INT),
     "fp8_grouped_gemm": ([P, INT, P, I64, P, INT, P, I64, I64, P, I64, P, I64, INT, I64, I64, I64, P], INT),
     "fp8_grouped_wgrad": ([P, INT, P, I64, P, INT, P, I64, P, I64, P, INT, I64, I64, I64, P], INT),
+    "fp8_attention_workspace_bytes": ([I64] * 6, SZ),
+    "fp8_attention_fwd": ([_Heads] * 4 + [P, P, P, INT, P, P, P, P] + [I64] * 6 + [F32, INT, I64, P, SZ, P], INT),
+    "fp8_attention_bwd_workspace_bytes": ([I64] * 6, SZ),
+    "fp8_attention_bwd": ([_Heads] * 5 + [P] + [_Heads] * 3 + [P, P] + [I64] * 6 + [F32, INT, I64, P, SZ, P], INT),
+    "fp8_moe_route_workspace_bytes": ([I64, I64], SZ),
+    "fp8_moe_route": ([P, INT, I64, I64, I64, I64, INT, P, P, P, P, P, P, P, SZ, P], INT),
+    "fp8_moe_route_bwd": ([P, INT, I64, I64, I64, I64, INT, P, P, P, P, P, P, P, I64, P], INT),
 }
 
 
@@ -696,3 +712,131 @@ def fp8_grouped_wgrad(At, fa, a_scale_inv, Bt, fb, b_scale_inv, offsets, dW, str
     _invoke("fp8_grouped_wgrad", _ptr(At), int(fa), _some(a_scale_inv, _F32, 1, "a_scale_inv"), At.stride(0), _ptr(Bt), int(fb),
             _some(b_scale_inv, _F32, 1, "b_scale_inv"), Bt.stride(0), _ptr(offsets), E, p_dw, _out_dtype(dW), cap, N, K,
             _stream(stream))
+
+
+def fp8_attention_workspace_bytes(Tq: int, Tk: int, batch: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().fp8_attention_workspace_bytes(int(Tq), int(Tk), int(batch), int(Hq), int(Hkv), int(D)))
+
+
+def fp8_attention_bwd_workspace_bytes(Tq: int, Tk: int, batch: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().fp8_attention_bwd_workspace_bytes(int(Tq), int(Tk), int(batch), int(Hq), int(Hkv), int(D)))
+
+
+def _heads(t, T, H, D, name, required=True):
+    """[T, H, D] bfloat16 with strides of its own, the elements of a head one behind the other."""
+    _want(t, _BF16, name, contiguous=False, shape=(T, H, D), required=required)
+    if t is None:
+        return _Heads(None, D, D)
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if not t.is_cuda:
+        return _HOST
+    return _Heads(t.data_ptr(), t.stride(0) if T > 1 else D, t.stride(1) if H > 1 else D)
+
+
+def _attention_sizes(q, k, offsets_q, offsets_k, batch):
+    """Tq, Hq, D, Tk, Hkv, the number of sequences and the offsets' pointers."""
+    _want(q, _BF16, "q", contiguous=False, required=True)
+    _want(k, _BF16, "k", contiguous=False, required=True)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head size]")
+    if (offsets_q is None) != (offsets_k is None):
+        raise ValueError("offsets_q and offsets_k go together")
+    if offsets_q is not None:
+        _want(offsets_q, _I32, "offsets_q")
+        if offsets_q.numel() < 1:
+            raise ValueError("offsets_q must hold at least one element")
+        batch = offsets_q.numel() - 1
+    row = (int(batch) + 1,)
+    return (*q.shape, k.shape[0], k.shape[1], int(batch), _arg(offsets_q, _I32, row, "offsets_q"),
+            _arg(offsets_k, _I32, row, "offsets_k"))
+
+
+def fp8_attention_fwd(q, k, v, out, lse=None, offsets_q=None, offsets_k=None, batch: int = 1, causal: bool = True,
+                      window: int = 0, softmax_scale=None, out8=None, scale=None, fmt=E4M3, scale_inv_out=None,
+                      amax_slot=None, workspace=None, stream=None):
+    """Attention of ``q`` [Tq, Hq, D] over ``k``, ``v`` [Tk, Hkv, D] (any token and head strides) into ``out`` (or
+    None), ``lse`` [Hq, Tq] and FP8 codes ``out8`` [Tq, Hq * D]; sequences by offsets, or ``batch`` equal ones;
+    ``softmax_scale`` None: D ** -0.5 (see include/fp8ds.h)."""
+    if _tls.rec is None and (_calls or _native()).attention_fwd(
+            q, k, v, out, lse, offsets_q, offsets_k, batch, causal, window, softmax_scale, out8, scale, fmt, scale_inv_out,
+            amax_slot, workspace, stream):
+        return
+    Tq, Hq, D, Tk, Hkv, B, p_oq, p_ok = _attention_sizes(q, k, offsets_q, offsets_k, batch)
+    ws_bytes = _workspace_bytes(workspace)
+    _invoke("fp8_attention_fwd", _heads(q, Tq, Hq, D, "q"), _heads(k, Tk, Hkv, D, "k"), _heads(v, Tk, Hkv, D, "v"),
+            _heads(out, Tq, Hq, D, "out", required=False), _arg(lse, _F32, (Hq, Tq), "lse"),
+            _arg(out8, _U8, (Tq, Hq * D), "out8"), _some(scale, _F32, 1, "scale"), int(fmt),
+            _some(scale_inv_out, _F32, 1, "scale_inv_out"), _some(amax_slot, _F32, 1, "amax_slot"), p_oq, p_ok, B, Tq, Tk,
+            Hq, Hkv, D, D ** -0.5 if softmax_scale is None else float(softmax_scale), int(bool(causal)), int(window),
+            _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def fp8_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, workspace, offsets_q=None, offsets_k=None, batch: int = 1,
+                      causal: bool = True, window: int = 0, softmax_scale=None, stream=None):
+    """Gradients of fp8_attention_fwd into ``dq``, ``dk``, ``dv`` (bfloat16, any token and head strides), from the
+    ``out`` and ``lse`` that it wrote (see include/fp8ds.h)."""
+    if _tls.rec is None and (_calls or _native()).attention_bwd(
+            dout, q, k, v, out, lse, dq, dk, dv, workspace, offsets_q, offsets_k, batch, causal, window, softmax_scale,
+            stream):
+        return
+    Tq, Hq, D, Tk, Hkv, B, p_oq, p_ok = _attention_sizes(q, k, offsets_q, offsets_k, batch)
+    ws_bytes = _workspace_bytes(workspace)
+    _invoke("fp8_attention_bwd", _heads(dout, Tq, Hq, D, "dout"), _heads(q, Tq, Hq, D, "q"), _heads(k, Tk, Hkv, D, "k"),
+            _heads(v, Tk, Hkv, D, "v"), _heads(out, Tq, Hq, D, "out"), _arg(lse, _F32, (Hq, Tq), "lse", True),
+            _heads(dq, Tq, Hq, D, "dq"), _heads(dk, Tk, Hkv, D, "dk"), _heads(dv, Tk, Hkv, D, "dv"), p_oq, p_ok, B, Tq, Tk,
+            Hq, Hkv, D, D ** -0.5 if softmax_scale is None else float(softmax_scale), int(bool(causal)), int(window),
+            _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def fp8_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().fp8_moe_route_workspace_bytes(int(T), int(E)))
+
+
+def _logits(t, name):
+    """[T, E] float32 or bfloat16 rows with unit stride: pointer, type, row stride."""
+    _want(t, (torch.float32, torch.bfloat16), name, contiguous=False, required=True)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, E]")
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.data_ptr() if t.is_cuda else _HOST, _out_dtype(t), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def fp8_moe_route(logits, experts, weights, lse, counts, prob_sum, loss, workspace=None, normalise: bool = True, stream=None):
+    """The choice of experts from the router's ``logits`` [T, E] (float32 or bfloat16, rows with unit stride):
+    ``experts`` [T, top] int32 as fp8_moe_plan reads them, ``weights`` [T, top], ``lse`` [T], ``counts`` [E + 1] int32,
+    ``prob_sum`` [E] and the balance ``loss`` [1] (see include/fp8ds.h)."""
+    if _tls.rec is None and (_calls or _native()).moe_route(logits, experts, weights, lse, counts, prob_sum, loss, workspace,
+                                                            normalise, stream):
+        return
+    p_l, dtype, ld = _logits(logits, "logits")
+    _want(experts, _I32, "experts", required=True)
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, top]")
+    (T, E), top = logits.shape, experts.shape[1]
+    ws_bytes = _workspace_bytes(workspace)
+    _invoke("fp8_moe_route", p_l, dtype, ld, T, E, top, int(bool(normalise)), _arg(experts, _I32, (T, top), "experts"),
+            _arg(weights, _F32, (T, top), "weights", True), _arg(lse, _F32, (T,), "lse", True),
+            _arg(counts, _I32, (E + 1,), "counts", True), _arg(prob_sum, _F32, (E,), "prob_sum", True),
+            _some(loss, _F32, 1, "loss"), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def fp8_moe_route_bwd(logits, experts, weights, lse, counts, dweights, dloss, dlogits, normalise: bool = True, stream=None):
+    """Gradient of fp8_moe_route: ``dlogits`` (as ``logits``) from ``dweights`` [T, top] and ``dloss`` [1], either of
+    which may be None; experts, weights, lse, counts: what the forward wrote."""
+    if _tls.rec is None and (_calls or _native()).moe_route_bwd(logits, experts, weights, lse, counts, dweights, dloss,
+                                                                dlogits, normalise, stream):
+        return
+    p_l, dtype, ld = _logits(logits, "logits")
+    p_d, dtype_d, ld_d = _logits(dlogits, "dlogits")
+    if dtype != dtype_d or logits.shape != dlogits.shape:
+        raise ValueError("dlogits must have the type and shape of logits")
+    _want(experts, _I32, "experts", required=True)
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, top]")
+    (T, E), top = logits.shape, experts.shape[1]
+    _invoke("fp8_moe_route_bwd", p_l, dtype, ld, T, E, top, int(bool(normalise)), _arg(experts, _I32, (T, top), "experts"),
+            _arg(weights, _F32, (T, top), "weights", True), _arg(lse, _F32, (T,), "lse", True),
+            _arg(counts, _I32, (E + 1,), "counts", True), _arg(dweights, _F32, (T, top), "dweights"),
+            _some(dloss, _F32, 1, "dloss"), p_d, ld_d, _stream(stream))

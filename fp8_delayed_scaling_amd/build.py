@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libfp8ds.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["cast.hip", "transpose.hip", "scale_update.hip", "gemm.hip", "api.cpp", "noalloc.hip",
-           "norm.hip", "moe.hip", "grouped.hip", "api_block.cpp"]
+           "norm.hip", "moe.hip", "grouped.hip", "router.hip", "attention.hip", "api_block.cpp", "api_attention.cpp"]
 CALL = os.path.join(HERE, "_call.so")      # the Python module of call.cpp, next to the library it calls
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,888 @@
+// attention.hip -- attention between the QKV layer and the projection, forward and backward, on gfx950.
+#include <climits>
+
+#include "../../include/fp8ds.h"
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8ds {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kRows = 128;                   // query rows (or keys) of a block, 32 to a wave
+constexpr int kFewRows = 32;                 // query rows of a block whose waves share the keys instead
+constexpr int kKeys = 64;                    // keys of a step
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor's bound
+constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_inff();
+
+#define FP8DS_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(waitcnt_vm(n))
+#define FP8DS_WAIT_LGKM() __builtin_amdgcn_s_waitcnt(0xC07F)
+#define FP8DS_WAIT_ALL() __builtin_amdgcn_s_waitcnt(0x0070)     // vmcnt(0) lgkmcnt(0)
+#define FP8DS_BARRIER()                          \
+    do {                                         \
+        asm volatile("" ::: "memory");           \
+        __builtin_amdgcn_s_barrier();            \
+        asm volatile("" ::: "memory");           \
+    } while (0)
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ---------------------------------------------------------------------------------- sequences
+struct Span {
+    int64_t begin;
+    int len;
+};
+// Sequence b's tokens, held to [0, T) whatever the offsets are.
+__device__ __forceinline__ Span span_of(const int32_t *off, int b, int T, int B) {
+    if (off == nullptr) {
+        const int len = T / B;
+        return Span{(int64_t)b * len, len};
+    }
+    const int lo = min(max(off[b], 0), T), hi = min(max(off[b + 1], lo), T);
+    return Span{lo, hi - lo};
+}
+
+// Tile t of the sequences' rows (`group` rows a token, `height` rows a tile): its sequence and its number in it,
+// the last tile of a sequence first.  False past the last.
+__device__ __forceinline__ bool find_tile(const int32_t *off, int T, int B, int group, int height, int t, int &b, int &tile) {
+    if (off == nullptr) {
+        const int n = (T / B * group + height - 1) / height;
+        b = t % B;
+        tile = n - 1 - t / B;
+        return tile >= 0;
+    }
+    const int lane = threadIdx.x & 63;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        const int i = b0 + lane;
+        int n = 0;
+        if (i < B) n = (int)(((int64_t)span_of(off, i, T, B).len * group + height - 1) / height);
+        int64_t upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
+        }
+        const uint64_t past = __ballot(before + upto > t);
+        if (past != 0) {
+            const int first = __ffsll((unsigned long long)past) - 1;
+            b = uniform(b0 + first);
+            const int64_t end = before + __shfl(upto, first, 64);
+            tile = uniform((int)(end - 1 - t));
+            return true;
+        }
+        before += __shfl(upto, 63, 64);
+    }
+    return false;
+}
+
+// ------------------------------------------------------------------------------------- tiles
+// A tile in LDS holds rows of PITCH bytes in 16-byte pieces; piece c of a row lies at c ^ swz(row), so that reading one
+// piece of many rows and reading 4 rows of the transposed form both reach all banks.
+template <int DB> struct Shape {                 // DB: head size in blocks of 32
+    static constexpr int pitch = DB <= 2 ? 128 : 256;
+    static constexpr int pieces = pitch / 16;
+    static constexpr int rows_a_load = 1024 / pitch;     // rows that one load of a wave fills
+    static constexpr int ks = 2 * DB;                    // steps of 16 along the head
+    static __device__ __forceinline__ int swz(int row) {
+        return pitch == 256 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+    }
+};
+
+// A lane's addresses in a tile.  row[ks]: row l % 32, elements 16 ks + 8 (l / 32) .. + 7, an operand whose contraction
+// runs along the head.  tr[d][s]: the transposed read of elements 32 d + l % 32 of the rows 8 s + 4 (l / 32) .. + 3, an
+// operand whose contraction runs over the rows.
+template <int DB> struct Reader {
+    uint32_t row[2 * DB], tr[DB][2];
+    __device__ __forceinline__ explicit Reader(int lane) {
+        using S = Shape<DB>;
+        const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int k = 0; k < S::ks; ++k) row[k] = r * S::pitch + ((2 * k + h) ^ S::swz(r)) * 16;
+        const int i = lane & 15;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int tr_row = 8 * s + 4 * h + (i >> 2), c = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+                tr[d][s] = tr_row * S::pitch + (c ^ S::swz(tr_row)) * 16 + (i & 1) * 8;
+            }
+    }
+};
+__device__ __forceinline__ bf16x8 read_row(const uint8_t *p) { return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p)); }
+__device__ __forceinline__ i16x4 read_tr4(const uint8_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)p);
+}
+// rows s .. of block d: 16 rows of the contraction, in the order in which the products leave them (rows 4 h .. + 3, then
+// 8 + 4 h .. + 3 for lane half h)
+template <int DB> __device__ __forceinline__ bf16x8 read_tr(const uint8_t *p, const Reader<DB> &rd, int d) {
+    const i16x4 a = read_tr4(p + rd.tr[d][0]), b = read_tr4(p + rd.tr[d][1]);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+// eight of the 16 values that a lane holds of a 32 x 32 product, as an operand of the next
+__device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int s) {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[8 * s + i];
+    return r;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = (uint64_t)(uint32_t)uniform((int)a) | (uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), (short)0, uniform((int)bytes), kBufDesc3);
+}
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t *to, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)to, 16, off, 0, 0, 0);
+}
+
+// Loads of ROWS consecutive rows (tokens) by WAVES waves, rows and pieces past the end as zeros.
+template <int DB, int ROWS, int WAVES> struct RowLoads {
+    using S = Shape<DB>;
+    static constexpr int n = ROWS / (S::rows_a_load * WAVES);                    // loads of a wave
+    static constexpr int variants = S::rows_a_load * WAVES >= 16 ? 1 : 16 / (S::rows_a_load * WAVES);
+    uint32_t off[variants];
+    uint32_t step;                                                               // bytes from variant to variant's next turn
+    int wave;
+    __device__ __forceinline__ RowLoads(int lane, int wave_, int D, int64_t ts) : wave(wave_) {
+#pragma unroll
+        for (int i = 0; i < variants; ++i) {
+            const int row = (i * WAVES + wave) * S::rows_a_load + lane / S::pieces, c = (lane % S::pieces) ^ S::swz(row);
+            off[i] = c * 8 < D ? (uint32_t)(row * (int)ts * 2 + c * 16) : kOutside;
+        }
+        step = (uint32_t)(variants * WAVES * S::rows_a_load * (int)ts * 2);
+    }
+    // `first`: the first row; `left`: rows there are (at least one)
+    __device__ __forceinline__ void operator()(const uint16_t *first, int64_t ts, int left, uint8_t *tile) const {
+        const auto rs = bounded(first, (uint32_t)min(left, ROWS) * (uint32_t)ts * 2u);
+#pragma unroll
+        for (int i = 0; i < n; ++i) load_lds(rs, tile + (i * WAVES + wave) * 1024, off[i % variants] + (i / variants) * step);
+    }
+};
+
+__device__ __forceinline__ float both_halves_max(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float both_halves_sum(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+// A lane's values 8 s .. 8 s + 7 of a product [32 x 32] whose columns are lanes, turned into 8 consecutive rows:
+// 16 s + 8 (l / 32) .. + 7.
+__device__ __forceinline__ void consecutive8(const f32x16 &v, int s, float (&o)[8]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[8 * s + u]), __float_as_uint(v[8 * s + 4 + u]), false, false);
+        o[u] = __uint_as_float(p[0]);
+        o[4 + u] = __uint_as_float(p[1]);
+    }
+}
+__device__ __forceinline__ u32x4 to_bf16(const float (&v)[8]) {
+    return u32x4{f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]), f32x2_to_bf16x2_rne(v[4], v[5]), f32x2_to_bf16x2_rne(v[6], v[7])};
+}
+
+// Eight values of one output row: bfloat16, codes, the largest magnitude.
+struct Emit {
+    float scale;
+    uint32_t amax = 0;
+    __device__ __forceinline__ explicit Emit(const Attention &a) : scale(a.out8 != nullptr ? *a.scale : 1.f) {}
+    __device__ __forceinline__ void operator()(const Attention &a, int64_t token, int head, int d, const float (&v)[8]) {
+        if (a.out.p != nullptr) *reinterpret_cast<u32x4 *>(a.out.p + token * a.out.ts + head * a.out.hs + d) = to_bf16(v);
+        if (a.out8 == nullptr) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = v[i] * scale;
+        u32x2 w;
+        if (a.fmt == kE4M3) w = u32x2{encode4<kE4M3>(y[0], y[1], y[2], y[3]), encode4<kE4M3>(y[4], y[5], y[6], y[7])};
+        else w = u32x2{encode4<kE5M2>(y[0], y[1], y[2], y[3]), encode4<kE5M2>(y[4], y[5], y[6], y[7])};
+        *reinterpret_cast<u32x2 *>(a.out8 + (token * a.Hq + head) * a.D + d) = w;
+    }
+    // every lane of the wave takes part
+    __device__ __forceinline__ void finish(const Attention &a) {
+        if (a.out8 == nullptr || a.amax == nullptr) return;
+        const uint32_t m = wave_max_u32(amax);
+        if ((threadIdx.x & 63) == 0) fold_amax_bits(a.amax, m);
+    }
+};
+__device__ __forceinline__ void write_inverse(const Attention &a) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.out8 != nullptr && a.sinv != nullptr) *a.sinv = 1.0f / *a.scale;
+}
+
+// Keys that query row `pos` of a sequence may see: [lo, hi).
+struct Seen {
+    int lo, hi;
+};
+__device__ __forceinline__ Seen seen(const Attention &a, int pos, int lq, int lk) {
+    if (!a.causal) return Seen{0, lk};
+    const int at = pos + (lk - lq);              // the row's own key
+    return Seen{a.window > 0 ? max(0, at - a.window + 1) : 0, min(lk, at + 1)};
+}
+
+// One step of the running softmax: NKB blocks of 32 keys.
+template <int DB, int NKB> struct Softmax {
+    f32x16 o[DB];
+    float m = -kInf, l = 0.f;                    // in units of log2; l: of this lane's keys only
+    __device__ __forceinline__ Softmax() {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    }
+    __device__ __forceinline__ void step(const uint8_t *sk, const uint8_t *sv, const Reader<DB> &rd, const bf16x8 (&qf)[2 * DB],
+                                         float s2, bool masked, int key0, Seen see, int lane) {
+        using S = Shape<DB>;
+        f32x16 s[NKB];
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < S::ks; ++k) s[kb] = mfma(read_row(sk + kb * 32 * S::pitch + rd.row[k]), qf[k], s[kb]);
+        }
+        if (masked) {
+            const int h4 = key0 + 4 * (lane >> 5);
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = h4 + kb * 32 + (i >> 2) * 8 + (i & 3);
+                    s[kb][i] = key >= see.lo && key < see.hi ? s[kb][i] : -kInf;
+                }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
+        mx = both_halves_max(mx) * s2;
+        if (__any(mx > m + 8.f)) {               // no lane past 2^8 of its reference: the sums are kept as they are
+            const float mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= al;
+        }
+        const float ref = m == -kInf ? 0.f : m;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], s2, -ref));
+                l += s[kb][i];
+            }
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const bf16x8 p = pack8(s[kb], x);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] = mfma(read_tr<DB>(sv + (kb * 32 + x * 16) * S::pitch, rd, d), p, o[d]);
+            }
+    }
+};
+
+// The lane's query row as an operand: elements 16 k + 8 (l / 32) .. + 7.
+template <int DB>
+__device__ __forceinline__ void load_query(bf16x8 (&f)[2 * DB], const uint16_t *row, bool there, int D, int half) {
+#pragma unroll
+    for (int k = 0; k < 2 * DB; ++k) {
+        const int d = k * 16 + half * 8;
+        u32x4 v = {0, 0, 0, 0};
+        if (there && d < D) v = *reinterpret_cast<const u32x4 *>(row + d);
+        f[k] = __builtin_bit_cast(bf16x8, v);
+    }
+}
+
+__device__ __forceinline__ float *part_sums(const Attention &a, int split) { return a.part + ((int64_t)split * a.Tq * a.Hq) * a.D; }
+__device__ __forceinline__ float *part_stats(const Attention &a, int split) {
+    return a.part + (int64_t)a.splits * a.Tq * a.Hq * a.D + (int64_t)split * a.Tq * a.Hq * 2;
+}
+
+}  // namespace
+
+// A block: 128 query rows of one key/value head, 32 to each wave; all waves read the same keys.
+template <int DB>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
+    using S = Shape<DB>;
+    constexpr int kTile = kKeys * S::pitch;
+    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // K, K, V, V
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    write_inverse(a);
+    const int kvh = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, split = rest % a.splits;
+    int b, tile;
+    if (!find_tile(a.offsets_q, a.Tq, a.B, a.G, kRows, rest / a.splits, b, tile)) return;
+    const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    const int rows = sq.len * a.G, r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
+    const int r0w = r0 + wave * 32, r = r0w + (lane & 31);
+    const int pos = r / a.G, head = kvh * a.G + r - pos * a.G;
+    const bool there = r < rows;
+    const int64_t token = sq.begin + pos;
+    bf16x8 qf[S::ks];
+    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
+
+    // keys of the block, of the wave, of the lane
+    int lo = seen(a, r0 / a.G, sq.len, sk.len).lo & ~(kKeys - 1), hi = seen(a, last / a.G, sq.len, sk.len).hi;
+    if (a.splits > 1) {
+        const int steps = (max(hi - lo, 0) + kKeys - 1) / kKeys, each = (steps + a.splits - 1) / a.splits;
+        lo += split * each * kKeys;
+        hi = min(hi, lo + each * kKeys);
+    }
+    const int wf = min(r0w, last) / a.G, wl = min(r0w + 31, last) / a.G;
+    const Seen first = seen(a, wf, sq.len, sk.len), end = seen(a, wl, sq.len, sk.len);
+    const Seen see = seen(a, pos, sq.len, sk.len);         // rows past the last compute what is never written
+
+    const RowLoads<DB, kKeys, kWaves> loads_k(lane, wave, a.D, a.k.ts), loads_v(lane, wave, a.D, a.v.ts);
+    const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
+    const Reader<DB> rd(lane);
+    const float s2 = a.softmax_scale * kLog2e;
+    Softmax<DB, 2> sm;
+    if (lo < hi) {
+        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, smem);
+        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, smem + 2 * kTile);
+    }
+    int turn = 0;
+    for (int j = lo; j < hi; j += kKeys, turn ^= 1) {
+        FP8DS_WAIT_ALL();
+        FP8DS_BARRIER();
+        const int next = j + kKeys;
+        if (next < hi) {
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, smem + (turn ^ 1) * kTile);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, smem + (2 + (turn ^ 1)) * kTile);
+        }
+        if (j < end.hi && next > first.lo) {
+            const bool masked = next > first.hi || j < end.lo;
+            sm.step(smem + turn * kTile, smem + (2 + turn) * kTile, rd, qf, s2, masked, j, see, lane);
+        }
+    }
+    const float l = both_halves_sum(sm.l);
+    if (a.splits > 1) {
+        if (!there) return;
+        const int64_t row = token * a.Hq + head;
+        if (lane < 32) {
+            float *st = part_stats(a, split) + row * 2;
+            st[0] = sm.m;
+            st[1] = l;
+        }
+        float *to = part_sums(a, split) + row * a.D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = d * 32 + i * 8 + (lane >> 5) * 4;
+                if (at < a.D) *reinterpret_cast<f32x4 *>(to + at) = f32x4{sm.o[d][4 * i], sm.o[d][4 * i + 1], sm.o[d][4 * i + 2], sm.o[d][4 * i + 3]};
+            }
+        return;
+    }
+    Emit emit(a);
+    const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;       // a NaN stays one
+    if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (sm.m + __builtin_amdgcn_logf(l)) * kLn2;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float v[8];
+            consecutive8(sm.o[d], s, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            const int at = d * 32 + s * 16 + (lane >> 5) * 8;
+            if (there && at < a.D) emit(a, token, head, at, v);
+        }
+    emit.finish(a);
+}
+
+// A block: up to 32 query rows of one key/value head; its waves share the keys.
+template <int DB>
+__global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a) {
+    using S = Shape<DB>;
+    constexpr int kTile = 32 * S::pitch, kPitch = 32 * DB + 4;       // floats of an output row in LDS
+    __shared__ __align__(1024) uint8_t smem[kWaves * 4 * kTile > kWaves * 32 * kPitch * 4 ? kWaves * 4 * kTile : kWaves * 32 * kPitch * 4];
+    __shared__ float stats[kWaves][32][2];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    write_inverse(a);
+    const int kvh = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, split = rest % a.splits;
+    int b, tile;
+    if (!find_tile(a.offsets_q, a.Tq, a.B, a.G, kFewRows, rest / a.splits, b, tile)) return;
+    const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    const int rows = sq.len * a.G, r0 = tile * kFewRows, last = min(r0 + kFewRows, rows) - 1;
+    const int r = r0 + (lane & 31), pos = r / a.G, head = kvh * a.G + r - pos * a.G;
+    const bool there = r < rows;
+    bf16x8 qf[S::ks];
+    load_query<DB>(qf, a.q.p + (sq.begin + pos) * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
+    const Seen first = seen(a, r0 / a.G, sq.len, sk.len), end = seen(a, last / a.G, sq.len, sk.len);
+    const Seen see = seen(a, pos, sq.len, sk.len);         // rows past the last compute what is never written
+    constexpr int kStep = kWaves * 32;
+    int lo = first.lo & ~31, hi = end.hi;
+    if (a.splits > 1) {
+        const int steps = (max(hi - lo, 0) + kStep - 1) / kStep, each = (steps + a.splits - 1) / a.splits;
+        lo += split * each * kStep;
+        hi = min(hi, lo + each * kStep);
+    }
+    const RowLoads<DB, 32, 1> loads_k(lane, 0, a.D, a.k.ts), loads_v(lane, 0, a.D, a.v.ts);
+    const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
+    const Reader<DB> rd(lane);
+    const float s2 = a.softmax_scale * kLog2e;
+    Softmax<DB, 1> sm;
+    uint8_t *mine = smem + wave * 4 * kTile;                         // K, V, K, V
+    int j = lo + wave * 32, turn = 0;
+    if (j < hi) {
+        loads_k(kp + (int64_t)j * a.k.ts, a.k.ts, sk.len - j, mine);
+        loads_v(vp + (int64_t)j * a.v.ts, a.v.ts, sk.len - j, mine + kTile);
+    }
+    for (; j < hi; j += kStep, turn ^= 1) {
+        const int next = j + kStep;
+        FP8DS_WAIT_LGKM();                                           // the reads of the tile that is overwritten next
+        if (next < hi) {
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, mine + (turn ^ 1) * 2 * kTile);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, mine + ((turn ^ 1) * 2 + 1) * kTile);
+            FP8DS_WAIT_VM(2 * decltype(loads_k)::n);
+        } else {
+            FP8DS_WAIT_VM(0);
+        }
+        asm volatile("" ::: "memory");
+        const bool masked = j + 32 > first.hi || j < end.lo;
+        sm.step(mine + turn * 2 * kTile, mine + (turn * 2 + 1) * kTile, rd, qf, s2, masked, j, see, lane);
+    }
+    // the four waves' sums, joined in order
+    const float l = both_halves_sum(sm.l);
+    if (lane < 32) {
+        stats[wave][lane][0] = sm.m;
+        stats[wave][lane][1] = l;
+    }
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4 *>(sums + (wave * 32 + (lane & 31)) * kPitch + d * 32 + i * 8 + (lane >> 5) * 4) =
+                f32x4{sm.o[d][4 * i], sm.o[d][4 * i + 1], sm.o[d][4 * i + 2], sm.o[d][4 * i + 3]};
+    __syncthreads();
+    Emit emit(a);
+    constexpr int kPer = 4 * DB;                                     // threads of a row, 8 elements each
+    for (int w = threadIdx.x; w < (last - r0 + 1) * kPer; w += kThreads) {
+        const int x = w / kPer, d = w % kPer * 8, rr = r0 + x, p = rr / a.G, hd = kvh * a.G + rr - p * a.G;
+        if (d >= a.D) continue;
+        float m = -kInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) m = fmaxf(m, stats[i][x][0]);
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const float wt = stats[i][x][0] == -kInf ? 0.f : __builtin_amdgcn_exp2f(stats[i][x][0] - m);
+            sum += stats[i][x][1] * wt;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] += sums[(i * 32 + x) * kPitch + d + u] * wt;
+        }
+        const int64_t token = sq.begin + p, row = token * a.Hq + hd;
+        if (a.splits > 1) {
+            float *to = part_sums(a, split) + row * a.D + d;
+            *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            if (d == 0) {
+                float *st = part_stats(a, split) + row * 2;
+                st[0] = m;
+                st[1] = sum;
+            }
+            continue;
+        }
+        const float inv = sum > 0.f ? 1.0f / sum : sum == 0.f ? 0.f : sum;
+        if (d == 0 && a.lse != nullptr) a.lse[(int64_t)hd * a.Tq + token] = sum == 0.f ? -kInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= inv;
+        emit(a, token, hd, d, v);
+    }
+    if (a.splits == 1) emit.finish(a);
+}
+
+// The splits' sums of each row, joined in order.  16 threads a row; rows of no sequence stay as they are.
+__global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int d = (threadIdx.x & 15) * 8;
+    const int64_t token = row / a.Hq;
+    const int head = (int)(row - token * a.Hq);
+    bool there = token < a.Tq;
+    if (there && a.offsets_q != nullptr) {
+        // the last sequence that begins at or before the token
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.offsets_q[mid] <= token) lo = mid;
+            else hi = mid;
+        }
+        there = a.offsets_q[lo] <= token && token < a.offsets_q[lo + 1];
+    }
+    Emit emit(a);
+    if (there) {
+        float m = -kInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < a.splits; ++i) m = fmaxf(m, part_stats(a, i)[row * 2]);
+        for (int i = 0; i < a.splits; ++i) {
+            const float *st = part_stats(a, i) + row * 2;
+            if (st[0] == -kInf) continue;
+            const float wt = __builtin_amdgcn_exp2f(st[0] - m);
+            sum += st[1] * wt;
+            if (d < a.D) {
+                const float *from = part_sums(a, i) + row * a.D + d;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] += from[u] * wt;
+            }
+        }
+        const float inv = sum > 0.f ? 1.0f / sum : sum == 0.f ? 0.f : sum;
+        if (d == 0 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = sum == 0.f ? -kInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= inv;
+        if (d < a.D) emit(a, token, head, d, v);
+    }
+    emit.finish(a);
+}
+
+// ---------------------------------------------------------------------------------- backward
+// Of every query row, in the order [key/value head, token, head of the group]: -lse / scale and -<dout, out>.
+__global__ __launch_bounds__(kThreads) void k_attn_delta(const Attention a) {
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int d = (threadIdx.x & 15) * 8;
+    const int64_t token = row / a.Hq;
+    if (token >= a.Tq) return;
+    const int head = (int)(row - token * a.Hq);
+    float sum = 0.f;
+    if (d < a.D) {
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(a.dout.p + token * a.dout.ts + head * a.dout.hs + d);
+        const u32x4 y = *reinterpret_cast<const u32x4 *>(a.out.p + token * a.out.ts + head * a.out.hs + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += bf16_lo(x[i]) * bf16_lo(y[i]) + bf16_hi(x[i]) * bf16_hi(y[i]);
+    }
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 16);
+    if (d == 0) {
+        const float lse = a.lse[(int64_t)head * a.Tq + token];
+        const int kvh = head / a.G;
+        const int64_t at = ((int64_t)kvh * a.Tq + token) * a.G + head - kvh * a.G;
+        a.part[at] = lse == -kInf ? -kInf : -lse / a.softmax_scale;
+        a.part[(int64_t)a.Tq * a.Hq + at] = -sum;
+    }
+}
+
+// Rows of the group's heads, `32` at a time from row r0, for 4 waves: token pos, head g of the group.
+template <int DB> struct GroupLoads {
+    using S = Shape<DB>;
+    static constexpr int n = 32 / (S::rows_a_load * kWaves);         // loads of a wave for one tile
+    int row[n];                                                      // of the tile
+    uint32_t piece;                                                  // byte in the row, kOutside past the head
+    int wave;
+    __device__ __forceinline__ GroupLoads(int lane, int wave_, int D) : wave(wave_) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) row[i] = (i * kWaves + wave) * S::rows_a_load + lane / S::pieces;
+        const int c = (lane % S::pieces) ^ S::swz(row[0]);           // loads are 16 or 32 rows apart: the same piece
+        piece = c * 8 < D ? c * 16 : kOutside;
+    }
+    // of the sequence's rows r0 ..; base: the sequence's first token at the group's first head
+    __device__ __forceinline__ void operator()(const uint16_t *base, int64_t ts, int64_t hs, int G, int r0, int rows, uint8_t *tile) const {
+        const int p0 = r0 / G;
+        const auto rs = bounded(base + (int64_t)p0 * ts, 0x7FFFFFFFu);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const int r = r0 + row[i], p = r / G, g = r - p * G;
+            const uint32_t off = piece + (uint32_t)((p - p0) * (int)ts + g * (int)hs) * 2u;
+            load_lds(rs, tile + (i * kWaves + wave) * 1024, r < rows && piece != kOutside ? off : kOutside);
+        }
+    }
+};
+
+// A block: 128 keys of one key/value head, 32 to each wave, over all query rows of its group that see them.
+template <int DB>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
+    using S = Shape<DB>;
+    constexpr int kTile = 32 * S::pitch;
+    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // Q, Q, dO, dO
+    __shared__ __align__(256) float stats[2][64];                    // the rows' -lse / scale, then -delta
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int kvh = blockIdx.x % a.Hkv;
+    int b, tile;
+    if (!find_tile(a.offsets_k, a.Tk, a.B, 1, kRows, blockIdx.x / a.Hkv, b, tile)) return;
+    const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    const int G = a.G, rows = sq.len * G, j0 = tile * kRows, past = sk.len - sq.len;
+    const int jw = j0 + wave * 32, key = jw + (lane & 31);
+    const bool there = key < sk.len;
+    const int64_t token = sk.begin + key;
+    bf16x8 kf[S::ks], vf[S::ks];
+    load_query<DB>(kf, a.k.p + token * a.k.ts + kvh * a.k.hs, there, a.D, lane >> 5);
+    load_query<DB>(vf, a.v.p + token * a.v.ts + kvh * a.v.hs, there, a.D, lane >> 5);
+
+    // query rows that see key j: [(j - past) G, (j - past + window) G)
+    auto from = [&](int j) { return a.causal ? (int)min(max((int64_t)(j - past) * G, (int64_t)0), (int64_t)rows) : 0; };
+    auto until = [&](int j) {
+        return a.causal && a.window > 0 ? (int)min(max(((int64_t)j - past + a.window) * G, (int64_t)0), (int64_t)rows) : rows;
+    };
+    const int lo = from(j0) & ~31, hi = until(min(j0 + kRows, sk.len) - 1);
+    const int w_first = from(jw), w_end = until(jw + 31);            // rows that any key of the wave sees
+    const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
+    const int mine_from = from(key), mine_until = until(key);
+
+    const GroupLoads<DB> loads(lane, wave, a.D);
+    const uint16_t *qp = a.q.p + sq.begin * a.q.ts + (int64_t)kvh * G * a.q.hs;
+    const uint16_t *dp = a.dout.p + sq.begin * a.dout.ts + (int64_t)kvh * G * a.dout.hs;
+    const int64_t all = (int64_t)a.Tq * a.Hq, row0 = ((int64_t)kvh * a.Tq + sq.begin) * G;
+    const auto rs_stats = bounded(a.part, (uint32_t)(all * 8));
+    auto load = [&](int r, int to) {
+        loads(qp, a.q.ts, a.q.hs, G, r, rows, smem + to * kTile);
+        loads(dp, a.dout.ts, a.dout.hs, G, r, rows, smem + (2 + to) * kTile);
+        if (wave == 0)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)stats[to], 4,
+                                                     (uint32_t)(row0 + r + (lane & 31) + (lane >> 5) * all) * 4u, 0, 0, 0);
+    };
+    const Reader<DB> rd(lane);
+    const float s2 = a.softmax_scale * kLog2e;
+    f32x16 dk[DB], dv[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
+    if (lo < hi) load(lo, 0);
+    int turn = 0;
+    for (int r = lo; r < hi; r += 32, turn ^= 1) {
+        FP8DS_WAIT_ALL();
+        FP8DS_BARRIER();
+        if (r + 32 < hi) load(r + 32, turn ^ 1);
+        if (r >= w_end || r + 32 <= w_first) continue;
+        const uint8_t *tq = smem + turn * kTile, *td = smem + (2 + turn) * kTile;
+        f32x16 s, p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(&stats[turn][8 * i + 4 * (lane >> 5)]);
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(&stats[turn][32 + 8 * i + 4 * (lane >> 5)]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s[4 * i + u] = x[u];
+                p[4 * i + u] = y[u];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row[k]), kf[k], s);
+#pragma unroll
+        for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row[k]), vf[k], p);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
+            p[i] *= s[i];
+        }
+        if (r < all_from || r + 32 > all_until || r + 32 > rows) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int at = r + (i >> 2) * 8 + 4 * (lane >> 5) + (i & 3);
+                const bool sees = at >= mine_from && at < mine_until;
+                s[i] = sees ? s[i] : 0.f;
+                p[i] = sees ? p[i] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const bf16x8 pf = pack8(s, x), sf = pack8(p, x);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                dv[d] = mfma(read_tr<DB>(td + x * 16 * S::pitch, rd, d), pf, dv[d]);
+                dk[d] = mfma(read_tr<DB>(tq + x * 16 * S::pitch, rd, d), sf, dk[d]);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float x[8], y[8];
+            consecutive8(dk[d], s, x);
+            consecutive8(dv[d], s, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= a.softmax_scale;
+            const int at = d * 32 + s * 16 + (lane >> 5) * 8;
+            if (there && at < a.D) {
+                *reinterpret_cast<u32x4 *>(a.dk.p + token * a.dk.ts + kvh * a.dk.hs + at) = to_bf16(x);
+                *reinterpret_cast<u32x4 *>(a.dv.p + token * a.dv.ts + kvh * a.dv.hs + at) = to_bf16(y);
+            }
+        }
+}
+
+// A block: 128 query rows, 32 to each wave, over the keys that they see.
+template <int DB>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
+    using S = Shape<DB>;
+    constexpr int kTile = kKeys * S::pitch;
+    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // K, K, V, V
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int kvh = blockIdx.x % a.Hkv;
+    int b, tile;
+    if (!find_tile(a.offsets_q, a.Tq, a.B, a.G, kRows, blockIdx.x / a.Hkv, b, tile)) return;
+    const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    const int rows = sq.len * a.G, r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
+    const int r0w = r0 + wave * 32, r = r0w + (lane & 31);
+    const int pos = r / a.G, head = kvh * a.G + r - pos * a.G;
+    const bool there = r < rows;
+    const int64_t token = sq.begin + pos;
+    bf16x8 qf[S::ks], df[S::ks];
+    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
+    load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, there, a.D, lane >> 5);
+    const float s2 = a.softmax_scale * kLog2e;
+    float low = -kInf, delta = 0.f;
+    if (there) {
+        const int64_t at = ((int64_t)kvh * a.Tq + sq.begin) * a.G + r;
+        low = a.part[at] * s2;
+        delta = a.part[(int64_t)a.Tq * a.Hq + at];
+    }
+    const int lo = seen(a, r0 / a.G, sq.len, sk.len).lo & ~(kKeys - 1), hi = seen(a, last / a.G, sq.len, sk.len).hi;
+    const Seen first = seen(a, min(r0w, last) / a.G, sq.len, sk.len), end = seen(a, min(r0w + 31, last) / a.G, sq.len, sk.len);
+    const Seen see = seen(a, pos, sq.len, sk.len);         // rows past the last compute what is never written
+    const RowLoads<DB, kKeys, kWaves> loads_k(lane, wave, a.D, a.k.ts), loads_v(lane, wave, a.D, a.v.ts);
+    const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
+    const Reader<DB> rd(lane);
+    f32x16 dq[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[d][i] = 0.f;
+    if (lo < hi) {
+        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, smem);
+        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, smem + 2 * kTile);
+    }
+    int turn = 0;
+    for (int j = lo; j < hi; j += kKeys, turn ^= 1) {
+        FP8DS_WAIT_ALL();
+        FP8DS_BARRIER();
+        const int next = j + kKeys;
+        if (next < hi) {
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, smem + (turn ^ 1) * kTile);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, smem + (2 + (turn ^ 1)) * kTile);
+        }
+        if (j >= end.hi || next <= first.lo) continue;
+        const bool masked = next > first.hi || j < end.lo;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const uint8_t *tk = smem + turn * kTile + kb * 32 * S::pitch, *tv = smem + (2 + turn) * kTile + kb * 32 * S::pitch;
+            f32x16 s, p;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = 0.f;
+                p[i] = delta;
+            }
+#pragma unroll
+            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tk + rd.row[k]), qf[k], s);
+#pragma unroll
+            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(tv + rd.row[k]), df[k], p);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, low));
+            if (masked) {
+                const int h4 = j + kb * 32 + 4 * (lane >> 5);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = h4 + (i >> 2) * 8 + (i & 3);
+                    p[i] = key >= see.lo && key < see.hi ? p[i] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const bf16x8 sf = pack8(p, x);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) dq[d] = mfma(read_tr<DB>(tk + x * 16 * S::pitch, rd, d), sf, dq[d]);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float x[8];
+            consecutive8(dq[d], s, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= a.softmax_scale;
+            const int at = d * 32 + s * 16 + (lane >> 5) * 8;
+            if (there && at < a.D) *reinterpret_cast<u32x4 *>(a.dq.p + token * a.dq.ts + head * a.dq.hs + at) = to_bf16(x);
+        }
+}
+
+// ---------------------------------------------------------------------------------- launches
+namespace {
+constexpr int kCUs = 256;
+constexpr int64_t kMostBlocks = (INT64_C(1) << 32) / kThreads - 1;
+
+int64_t most_tiles(int64_t T, int64_t B, int64_t group, int64_t height, bool ragged) {
+    return ragged ? T * group / height + B : B * ((T / B * group + height - 1) / height);
+}
+struct Plan {
+    bool few;
+    int64_t blocks, splits;
+};
+// Few query rows to a sequence: the waves share the keys.  Few blocks: the keys are split.
+Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ragged) {
+    Plan p;
+    p.few = Tq * G <= kFewRows * B;
+    const int64_t tiles = most_tiles(Tq, B, G, p.few ? kFewRows : kRows, ragged) * Hkv;
+    const int64_t want = p.few ? 2 * kCUs : 2 * kCUs, shortest = p.few ? 256 : 512;
+    int64_t s = tiles > 0 ? want / tiles : 1;
+    const int64_t most = Tk / B / shortest;
+    if (s > most) s = most;
+    p.splits = s < 1 ? 1 : s > 64 ? 64 : s;
+    p.blocks = tiles * p.splits;
+    return p;
+}
+}  // namespace
+
+bool attention_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, bool ragged) {
+    if (B == 0) return true;
+    return fwd_plan(Tq, Tk, B, Hkv, Hq / Hkv, ragged).blocks <= kMostBlocks && most_tiles(Tq, B, Hq / Hkv, kRows, ragged) * Hkv <= kMostBlocks &&
+           most_tiles(Tk, B, 1, kRows, ragged) * Hkv <= kMostBlocks;
+}
+
+size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+    if (B == 0 || Tq == 0) return 0;
+    int64_t s = 1;
+    for (bool ragged : {false, true}) {
+        if (!ragged && (Tq % B != 0 || Tk % B != 0)) continue;
+        const int64_t n = fwd_plan(Tq, Tk, B, Hkv, Hq / Hkv, ragged).splits;
+        if (n > s) s = n;
+    }
+    return s > 1 ? (size_t)(s * Tq * Hq * (D + 2) * 4) : 0;
+}
+size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq) { return (size_t)(Tq * Hq * 8); }
+
+#define FP8DS_BY_HEAD(KERNEL, BLOCKS)                                                                  \
+    do {                                                                                               \
+        const dim3 grid((unsigned)(BLOCKS));                                                           \
+        if (a.D <= 64) KERNEL<2><<<grid, kThreads, 0, st>>>(a);                                        \
+        else if (a.D <= 96) KERNEL<3><<<grid, kThreads, 0, st>>>(a);                                   \
+        else KERNEL<4><<<grid, kThreads, 0, st>>>(a);                                                  \
+    } while (0)
+
+hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st) {
+    const Plan p = fwd_plan(a.Tq, a.Tk, a.B, a.Hkv, a.G, a.offsets_q != nullptr);
+    a.splits = (int)p.splits;
+    a.part = static_cast<float *>(ws);
+    if (p.few) FP8DS_BY_HEAD(k_attn_fwd_few, p.blocks);
+    else FP8DS_BY_HEAD(k_attn_fwd, p.blocks);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || a.splits == 1) return e;
+    k_attn_join<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st) {
+    const bool ragged = a.offsets_q != nullptr;
+    a.part = static_cast<float *>(ws);
+    if (a.Tq > 0) k_attn_delta<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (a.Tk > 0) FP8DS_BY_HEAD(k_attn_dkv, most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv);
+    return hipGetLastError();
+}
+
+}  // namespace fp8ds

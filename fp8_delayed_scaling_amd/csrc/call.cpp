@@ -14,6 +14,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 
 #include "../../include/fp8ds.h"
@@ -86,6 +87,15 @@ struct Args {
         if (v != (int)v) ok = false;
         return (int)v;
     }
+    int truth(int i) {
+        if (!ok) return 0;
+        const int v = PyObject_IsTrue(a[i]);
+        if (v < 0) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return v > 0;
+    }
     float real(int i) {
         if (!ok) return 0.f;
         const double v = PyFloat_AsDouble(a[i]);
@@ -112,6 +122,23 @@ struct Args {
             ok = false;
         }
         return static_cast<hipStream_t>(p);
+    }
+    // [T, H, D] bfloat16 with strides of its own, the elements of a head one behind the other; or None
+    fp8ds_heads heads(int i, int64_t T, int64_t H, int64_t D, bool required = true) {
+        fp8ds_heads h{nullptr, D, D};
+        if (!ok) return h;
+        if (a[i] == Py_None) {
+            ok = !required;
+            return h;
+        }
+        const at::Tensor *t = tensor(i, kBf16);
+        if (t == nullptr) return h;
+        ok = t->sizes() == c10::IntArrayRef({T, H, D}) && (t->numel() == 0 || t->stride(2) == 1);
+        if (!ok) return h;
+        h.data = static_cast<uint16_t *>(t->data_ptr());
+        if (T > 1) h.token_stride = t->stride(0);      // of a single token or head a stride says nothing
+        if (H > 1) h.head_stride = t->stride(1);
+        return h;
     }
     // gate [G, H] with G dividing the rows, or None
     const uint16_t *gate(int i, int64_t rows, int64_t width, int64_t &n) {
@@ -339,6 +366,126 @@ PyObject *grouped_wgrad(PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// q [Tq, Hq, D] and k [Tk, Hkv, D] give an attention's sizes, the offsets (both or neither) its sequences.
+struct AttentionSizes {
+    int64_t Tq = 0, Hq = 0, D = 0, Tk = 0, Hkv = 0, B = 0;
+    const int32_t *off_q = nullptr, *off_k = nullptr;
+    AttentionSizes(Args &a, int q, int k, int offsets_q, int offsets_k, int batch) {
+        const at::Tensor *tq = a.tensor(q, kBf16), *tk = a.ok ? a.tensor(k, kBf16) : nullptr;
+        if (!a.ok || tq->dim() != 3 || tk->dim() != 3) {
+            a.ok = false;
+            return;
+        }
+        Tq = tq->size(0), Hq = tq->size(1), D = tq->size(2), Tk = tk->size(0), Hkv = tk->size(1);
+        if (a.a[offsets_q] == Py_None) {
+            B = a.integer(batch);
+            a.ok = a.ok && a.a[offsets_k] == Py_None;
+            return;
+        }
+        const at::Tensor *o = a.tensor(offsets_q, kI32);
+        if (o == nullptr) return;
+        B = o->numel() - 1;
+        off_q = a.dense<int32_t>(offsets_q, kI32, {B + 1}, true);
+        off_k = a.dense<int32_t>(offsets_k, kI32, {B + 1}, true);
+    }
+    float scale(Args &a, int i) const { return a.ok && a.a[i] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : a.real(i); }
+};
+
+PyObject *attention_fwd(PyObject *const *args, Py_ssize_t n) {
+    Args a(args, n, 18);
+    if (!a.ok) return done(false);
+    const AttentionSizes z(a, 0, 1, 5, 6, 7);
+    const fp8ds_heads q = a.heads(0, z.Tq, z.Hq, z.D), k = a.heads(1, z.Tk, z.Hkv, z.D), v = a.heads(2, z.Tk, z.Hkv, z.D);
+    const fp8ds_heads out = a.heads(3, z.Tq, z.Hq, z.D, false);
+    auto *lse = a.dense<float>(4, kF32, {z.Hq, z.Tq});
+    const int causal = a.truth(8);
+    const int64_t window = a.integer(9);
+    const float scale = z.scale(a, 10);
+    auto *out8 = a.dense<uint8_t>(11, kU8, {z.Tq, z.Hq * z.D});
+    const auto *s8 = a.some<float>(12, kF32, 1);
+    const int fmt = a.small(13);
+    auto *sinv = a.some<float>(14, kF32, 1), *amax = a.some<float>(15, kF32, 1);
+    size_t bytes;
+    void *ws = a.workspace(16, bytes);
+    const hipStream_t st = a.stream(17);
+    if (!a.ok) return done(false);
+    return done_with([&] {
+        return fp8_attention_fwd(q, k, v, out, lse, out8, s8, fmt, sinv, amax, z.off_q, z.off_k, z.B, z.Tq, z.Tk, z.Hq, z.Hkv,
+                                 z.D, scale, causal, window, ws, bytes, st);
+    });
+}
+
+PyObject *attention_bwd(PyObject *const *args, Py_ssize_t n) {
+    Args a(args, n, 17);
+    if (!a.ok) return done(false);
+    const AttentionSizes z(a, 1, 2, 10, 11, 12);
+    const fp8ds_heads dout = a.heads(0, z.Tq, z.Hq, z.D), q = a.heads(1, z.Tq, z.Hq, z.D), k = a.heads(2, z.Tk, z.Hkv, z.D);
+    const fp8ds_heads v = a.heads(3, z.Tk, z.Hkv, z.D), out = a.heads(4, z.Tq, z.Hq, z.D);
+    const auto *lse = a.dense<float>(5, kF32, {z.Hq, z.Tq}, true);
+    const fp8ds_heads dq = a.heads(6, z.Tq, z.Hq, z.D), dk = a.heads(7, z.Tk, z.Hkv, z.D), dv = a.heads(8, z.Tk, z.Hkv, z.D);
+    size_t bytes;
+    void *ws = a.workspace(9, bytes);
+    const int causal = a.truth(13);
+    const int64_t window = a.integer(14);
+    const float scale = z.scale(a, 15);
+    const hipStream_t st = a.stream(16);
+    if (!a.ok) return done(false);
+    return done_with([&] {
+        return fp8_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, z.off_q, z.off_k, z.B, z.Tq, z.Tk, z.Hq, z.Hkv, z.D, scale,
+                                 causal, window, ws, bytes, st);
+    });
+}
+
+// Rows of logits: float32 or bfloat16, [T, E], unit stride along a row.
+const at::Tensor *logits_of(Args &a, int i, int &dtype) {
+    const at::Tensor *t = output(a, i, dtype);
+    if (t == nullptr) return nullptr;
+    return t->dim() == 2 && (t->size(1) <= 1 || rows_dense(t)) ? t : a.fail();
+}
+int64_t row_stride(const at::Tensor *t) { return t->size(0) > 1 ? t->stride(0) : t->size(1); }
+
+PyObject *moe_route(PyObject *const *args, Py_ssize_t n) {
+    Args a(args, n, 10);
+    int dtype = 0;
+    const at::Tensor *l = logits_of(a, 0, dtype), *x = a.ok ? a.tensor(1, kI32) : nullptr;
+    if (!a.ok || x->dim() != 2) return done(false);
+    const int64_t T = l->size(0), E = l->size(1), top = x->size(1);
+    auto *experts = a.dense<int32_t>(1, kI32, {T, top}, true);
+    auto *weights = a.dense<float>(2, kF32, {T, top}, true), *lse = a.dense<float>(3, kF32, {T}, true);
+    auto *counts = a.dense<int32_t>(4, kI32, {E + 1}, true);
+    auto *prob_sum = a.dense<float>(5, kF32, {E}, true), *loss = a.some<float>(6, kF32, 1);
+    size_t bytes;
+    void *ws = a.workspace(7, bytes);
+    const int normalise = a.truth(8);
+    const hipStream_t st = a.stream(9);
+    if (!a.ok) return done(false);
+    const void *pl = l->data_ptr();
+    return done_with([&] {
+        return fp8_moe_route(pl, dtype, row_stride(l), T, E, top, normalise, experts, weights, lse, counts, prob_sum, loss, ws, bytes, st);
+    });
+}
+
+PyObject *moe_route_bwd(PyObject *const *args, Py_ssize_t n) {
+    Args a(args, n, 10);
+    int dtype = 0, dtype_d = 0;
+    const at::Tensor *l = logits_of(a, 0, dtype), *x = a.ok ? a.tensor(1, kI32) : nullptr, *d = logits_of(a, 7, dtype_d);
+    if (!a.ok || x->dim() != 2 || dtype != dtype_d || l->sizes() != d->sizes()) return done(false);
+    const int64_t T = l->size(0), E = l->size(1), top = x->size(1);
+    const auto *experts = a.dense<int32_t>(1, kI32, {T, top}, true);
+    const auto *weights = a.dense<float>(2, kF32, {T, top}, true), *lse = a.dense<float>(3, kF32, {T}, true);
+    const auto *counts = a.dense<int32_t>(4, kI32, {E + 1}, true);
+    const auto *dweights = a.dense<float>(5, kF32, {T, top}), *dloss = a.some<float>(6, kF32, 1);
+    const int normalise = a.truth(8);
+    const hipStream_t st = a.stream(9);
+    if (!a.ok) return done(false);
+    const void *pl = l->data_ptr();
+    void *pd = d->data_ptr();
+    return done_with([&] {
+        return fp8_moe_route_bwd(pl, dtype, row_stride(l), T, E, top, normalise, experts, weights, lse, counts, dweights, dloss, pd,
+                                 row_stride(d), st);
+    });
+}
+
 // PyTorch raises C++ exceptions for tensors without storage or strides, and where there is no GPU to
 // have a current stream.  None may leave a function that C calls: the binding's checks raise them again.
 template <PyObject *(*call)(PyObject *const *, Py_ssize_t)>
@@ -354,7 +501,8 @@ PyObject *guarded(PyObject *, PyObject *const *args, Py_ssize_t n) noexcept {
 #define FP8DS_CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP8DS_CALL(norm_fwd),      FP8DS_CALL(norm_bwd),    FP8DS_CALL(moe_plan),        FP8DS_CALL(moe_sort_cast),
                          FP8DS_CALL(moe_sort_codes), FP8DS_CALL(moe_combine), FP8DS_CALL(moe_weight_grad), FP8DS_CALL(grouped_gemm),
-                         FP8DS_CALL(grouped_wgrad), {nullptr, nullptr, 0, nullptr}};
+                         FP8DS_CALL(grouped_wgrad), FP8DS_CALL(attention_fwd), FP8DS_CALL(attention_bwd), FP8DS_CALL(moe_route),
+                         FP8DS_CALL(moe_route_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", "The block operators' calls.", -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

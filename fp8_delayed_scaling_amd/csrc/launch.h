@@ -116,4 +116,54 @@ bool grouped_wgrad_fits(int64_t E, int64_t N, int64_t K);
 hipError_t launch_grouped_gemm(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st);
 hipError_t launch_grouped_wgrad(const Grouped &g, int fa, int fb, int out_dtype, hipStream_t st);
 
+// Attention between the QKV layer and the projection (attention.hip).  A tensor of heads: elements of a
+// head follow each other, tokens and heads lie ts and hs elements apart.
+struct Heads {
+    uint16_t *p;
+    int64_t ts, hs;
+};
+struct Attention {
+    Heads q, k, v, out, dout, dq, dk, dv;
+    const int32_t *offsets_q, *offsets_k;    // both nullptr: B sequences of equal lengths
+    float *lse;
+    uint8_t *out8;
+    const float *scale;
+    float *sinv, *amax;
+    float softmax_scale;
+    int fmt, causal, window;                 // window 0: none
+    int B, Tq, Tk, Hq, Hkv, G, D;
+    // set by the launcher
+    int splits;
+    float *part;
+};
+constexpr int64_t kAttnMaxHead = 128;
+constexpr int64_t kAttnMaxStride = INT64_C(1) << 23;     // between tokens: 64 rows' offsets stay below 2^31
+constexpr int64_t kAttnMaxRows = INT64_C(1) << 28;       // tokens x heads
+bool attention_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, bool ragged);
+size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq);
+hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st);
+hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st);
+
+// The choice of experts from the router's logits (router.hip).
+struct Route {
+    const void *logits;
+    int64_t ld, T;
+    int E, top, bf16, normalise;
+    int32_t *experts;
+    float *weights, *lse;
+    int32_t *counts;
+    float *prob_sum, *loss;
+    // backward
+    const float *dweights, *dloss;
+    void *dlogits;
+    int64_t ld_d;
+    // set by the launcher: the blocks' parts
+    float *part_sum;
+    int32_t *part_cnt;
+};
+size_t moe_route_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_moe_route(Route a, void *ws, hipStream_t st);
+hipError_t launch_moe_route_bwd(const Route &a, hipStream_t st);
+
 }  // namespace fp8ds

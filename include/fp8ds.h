@@ -450,6 +450,94 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
                       const float *b_scale_inv, int64_t ldb, const int32_t *offsets, int64_t E, void *dW,
                       int out_dtype, int64_t cap, int64_t N, int64_t K, hipStream_t stream);
 
+/*
+ * fp8_attention_fwd -- attention between the QKV linear layer and the projection; the projection's
+ * input leaves as bfloat16, as FP8 codes, or both.  For query head h, its key/value head h / (Hq / Hkv)
+ * and a sequence of lq query tokens and lk keys:
+ *
+ *   s[i, j] = softmax_scale * <q[i], k[j]>       for the keys j that row i sees
+ *   lse[i]  = log(sum_j exp(s[i, j]))            o[i] = sum_j exp(s[i, j] - lse[i]) * v[j]
+ *   out = bfloat16(o);  out8 = saturating round-to-nearest-even code (fmt) of o * (*scale);
+ *   amax_slot, scale_inv_out as fp8_cast_amax, with the amax of o in float32 before the scale
+ *
+ * causal != 0: row i sees the keys j <= i + lk - lq (the sequence's last query token is at its last key);
+ * with window > 0 only the last `window` of those.  A row that sees no key gives zeros and lse = -inf.
+ *
+ * q, out: Tq tokens of Hq heads of D bfloat16 elements, k, v: Tk tokens of Hkv heads (Hq % Hkv == 0), each
+ * with strides of its own: slices of the QKV layer's output, head-major caches, heads that share one
+ * (head stride 0 for inputs).  lse: [Hq, Tq] float32 or NULL.  out8: [Tq, Hq * D] or NULL, out.data may be
+ * NULL with it.  offsets_q, offsets_k: [B + 1] int32 each on the device, sequence b's tokens are
+ * [offsets[b], offsets[b + 1]) (held to [0, T) as they are read); both NULL: B sequences of equal lengths.
+ * They must not fall: a falling pair is an empty sequence, and rows that several sequences then cover hold any
+ * of their results or none.  Rows of no sequence are neither read nor written.
+ *
+ * D % 8 == 0, 8 <= D <= 128; strides % 8 == 0; token strides >= D (one token: any) and below 2^23; data 16-byte
+ * aligned; T * heads <= 2^28; the heads that share a key/value head lie within 2^30 elements.
+ * softmax_scale > 0; window only with causal.  Scores, softmax and sums are float32; the probabilities are
+ * rounded to bfloat16 as operands of the matrix cores.  A NaN or an infinity in q, k or v may reach every row
+ * of its sequence, those that do not see it too.  workspace: fp8_attention_workspace_bytes (may be 0: NULL),
+ * 16-byte aligned, no initialisation; calls that overlap in time must not share it.
+ */
+typedef struct {
+    uint16_t *data;
+    int64_t token_stride, head_stride; /* in elements */
+} fp8ds_heads;
+
+size_t fp8_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads out, float *lse, uint8_t *out8,
+                      const float *scale, int fmt, float *scale_inv_out, float *amax_slot, const int32_t *offsets_q,
+                      const int32_t *offsets_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                      float softmax_scale, int causal, int64_t window, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/*
+ * fp8_attention_bwd -- gradients of fp8_attention_fwd; the probabilities are computed again from lse.
+ *
+ *   p = exp(s - lse);  ds = p * (<dout, v> - <dout, out>)
+ *   dq[i] = softmax_scale * sum_j ds[i, j] * k[j]
+ *   dk[j] = softmax_scale * sum_i ds[i, j] * q[i],  dv[j] = sum_i p[i, j] * dout[i]    (over the heads that share k, v)
+ *
+ * out, lse: what the forward wrote.  dq, dk, dv: bfloat16, strided as q, k, v may be (no two elements in one
+ * place), so that they can be slices of the QKV layer's output gradient; rows of no sequence are not written.
+ * The rest as fp8_attention_fwd.  p and ds are rounded to bfloat16 as operands; every sum is float32 in a
+ * fixed order: the same run to run.
+ */
+size_t fp8_attention_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+int fp8_attention_bwd(fp8ds_heads dout, fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads out, const float *lse,
+                      fp8ds_heads dq, fp8ds_heads dk, fp8ds_heads dv, const int32_t *offsets_q, const int32_t *offsets_k,
+                      int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float softmax_scale, int causal,
+                      int64_t window, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * fp8_moe_route -- the router's choice of experts, its weights, and the balance loss.
+ *
+ *   lse[t] = log(sum_e exp(logits[t, e]));  p[t, e] = exp(logits[t, e] - lse[t])
+ *   experts[t, j]: the expert with the j-th largest logit, ties to the lowest expert; never one whose logit is
+ *                  -inf or NaN: -1 where there are no others left
+ *   weights[t, j] = p of that expert, 0 for -1; normalise != 0: divided by the row's sum of them
+ *   counts[e]: choices of expert e;  counts[E]: rows with any probability (those whose logits are not all -inf)
+ *   prob_sum[e] = sum_t p[t, e]
+ *   *loss = E * sum_e (counts[e] / max(1, sum counts)) * prob_sum[e] / max(1, counts[E])
+ *
+ * A row of nothing but -inf (padding) chooses nothing, has lse = -inf and is in no sum.  A NaN or +inf in a row
+ * makes its lse, its share of prob_sum and the loss NaN.
+ * logits: [T, E] float32 or bfloat16 (dtype, an fp8ds_out_dtype), row stride ld >= E.  experts [T, top] int32, what
+ * fp8_moe_plan reads; weights [T, top], lse [T], prob_sum [E], loss [1] float32; counts [E + 1] int32.  1 <= E <= 1024,
+ * 1 <= top <= E.  Sums are float32 in a fixed order.  workspace: fp8_moe_route_workspace_bytes (0 for small T:
+ * NULL), 4-byte aligned, no initialisation; calls that overlap in time must not share it.
+ *
+ * fp8_moe_route_bwd -- dlogits (type of logits, row stride ld_d) from dweights [T, top] and *dloss, either may be NULL:
+ * counts are constants, weights and prob_sum are functions of the logits.  experts, weights, lse, counts: what the
+ * forward wrote; a choice outside [0, E) has no gradient; padding rows get zeros.
+ */
+size_t fp8_moe_route_workspace_bytes(int64_t T, int64_t E);
+int fp8_moe_route(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t top, int normalise, int32_t *experts,
+                  float *weights, float *lse, int32_t *counts, float *prob_sum, float *loss, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+int fp8_moe_route_bwd(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t top, int normalise,
+                      const int32_t *experts, const float *weights, const float *lse, const int32_t *counts,
+                      const float *dweights, const float *dloss, void *dlogits, int64_t ld_d, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
