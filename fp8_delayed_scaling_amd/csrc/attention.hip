@@ -17,6 +17,7 @@ constexpr int kThreads = 256, kWaves = 4;
 constexpr int kRows = 128;                   // query rows (or keys) of a block, 32 to a wave
 constexpr int kFewRows = 32;                 // query rows of a block whose waves share the keys instead
 constexpr int kKeys = 64;                    // keys of a step
+constexpr int kStepRows = 64;                // query rows of a step
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor's bound
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -51,11 +52,12 @@ __device__ __forceinline__ Span span_of(const int32_t *off, int b, int T, int B)
 
 // Tile t of the sequences' rows (`group` rows a token, `height` rows a tile): its sequence and its number in it,
 // the last tile of a sequence first.  False past the last.
-__device__ __forceinline__ bool find_tile(const int32_t *off, int T, int B, int group, int height, int t, int &b, int &tile) {
+__device__ __forceinline__ bool find_tile(const int32_t *off, int T, int B, int group, int height, int t, int &b, int &tile, bool pairs = false) {
     if (off == nullptr) {
         const int n = (T / B * group + height - 1) / height;
         b = t % B;
         tile = n - 1 - t / B;
+        if (pairs && 2 * tile < n) tile = (n - 1) / 2 - tile;     // the second half the other way round
         return tile >= 0;
     }
     const int lane = threadIdx.x & 63;
@@ -575,10 +577,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_delta(const Attention a) {
     }
 }
 
-// Rows of the group's heads, `32` at a time from row r0, for 4 waves: token pos, head g of the group.
+// Rows of the group's heads, 64 at a time from row r0, for 4 waves: token pos, head g of the group.
 template <int DB> struct GroupLoads {
     using S = Shape<DB>;
-    static constexpr int n = 32 / (S::rows_a_load * kWaves);         // loads of a wave for one tile
+    static constexpr int n = kStepRows / (S::rows_a_load * kWaves);  // loads of a wave for one tile
     int row[n];                                                      // of the tile
     uint32_t piece;                                                  // byte in the row, kOutside past the head
     int wave;
@@ -605,13 +607,13 @@ template <int DB> struct GroupLoads {
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = 32 * S::pitch;
+    constexpr int kTile = kStepRows * S::pitch;
     __shared__ __align__(1024) uint8_t smem[4 * kTile];              // Q, Q, dO, dO
-    __shared__ __align__(256) float stats[2][64];                    // the rows' -lse / scale, then -delta
+    __shared__ __align__(256) float stats[2][2 * kStepRows];         // the rows' -lse / scale, then -delta
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hkv;
     int b, tile;
-    if (!find_tile(a.offsets_k, a.Tk, a.B, 1, kRows, blockIdx.x / a.Hkv, b, tile)) return;
+    if (!find_tile(a.offsets_k, a.Tk, a.B, 1, kRows, blockIdx.x / a.Hkv, b, tile, gridDim.x <= 512)) return;
     const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
     const int G = a.G, rows = sq.len * G, j0 = tile * kRows, past = sk.len - sq.len;
     const int jw = j0 + wave * 32, key = jw + (lane & 31);
@@ -626,7 +628,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     auto until = [&](int j) {
         return a.causal && a.window > 0 ? (int)min(max(((int64_t)j - past + a.window) * G, (int64_t)0), (int64_t)rows) : rows;
     };
-    const int lo = from(j0) & ~31, hi = until(min(j0 + kRows, sk.len) - 1);
+    const int lo = from(j0) & ~(kStepRows - 1), hi = until(min(j0 + kRows, sk.len) - 1);
     const int w_first = from(jw), w_end = until(jw + 31);            // rows that any key of the wave sees
     const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
     const int mine_from = from(key), mine_until = until(key);
@@ -639,9 +641,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     auto load = [&](int r, int to) {
         loads(qp, a.q.ts, a.q.hs, G, r, rows, smem + to * kTile);
         loads(dp, a.dout.ts, a.dout.hs, G, r, rows, smem + (2 + to) * kTile);
-        if (wave == 0)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)stats[to], 4,
-                                                     (uint32_t)(row0 + r + (lane & 31) + (lane >> 5) * all) * 4u, 0, 0, 0);
+        if (wave < 2)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(stats[to] + wave * kStepRows), 4,
+                                                     (uint32_t)(row0 + r + lane + wave * all) * 4u, 0, 0, 0);
     };
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
@@ -652,48 +654,52 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
         for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
     if (lo < hi) load(lo, 0);
     int turn = 0;
-    for (int r = lo; r < hi; r += 32, turn ^= 1) {
+    for (int r0 = lo; r0 < hi; r0 += kStepRows, turn ^= 1) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
-        if (r + 32 < hi) load(r + 32, turn ^ 1);
-        if (r >= w_end || r + 32 <= w_first) continue;
-        const uint8_t *tq = smem + turn * kTile, *td = smem + (2 + turn) * kTile;
-        f32x16 s, p;
+        if (r0 + kStepRows < hi) load(r0 + kStepRows, turn ^ 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(&stats[turn][8 * i + 4 * (lane >> 5)]);
-            const f32x4 y = *reinterpret_cast<const f32x4 *>(&stats[turn][32 + 8 * i + 4 * (lane >> 5)]);
+        for (int part = 0; part < kStepRows / 32; ++part) {
+            const int r = r0 + part * 32;
+            if (r >= w_end || r + 32 <= w_first) continue;
+            const uint8_t *tq = smem + turn * kTile + part * 32 * S::pitch, *td = smem + (2 + turn) * kTile + part * 32 * S::pitch;
+            const float *st = &stats[turn][part * 32 + 4 * (lane >> 5)];
+            f32x16 s, p;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                s[4 * i + u] = x[u];
-                p[4 * i + u] = y[u];
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(st + 8 * i), y = *reinterpret_cast<const f32x4 *>(st + kStepRows + 8 * i);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    s[4 * i + u] = x[u];
+                    p[4 * i + u] = y[u];
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row[k]), kf[k], s);
+            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row[k]), kf[k], s);
 #pragma unroll
-        for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row[k]), vf[k], p);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
-            p[i] *= s[i];
-        }
-        if (r < all_from || r + 32 > all_until || r + 32 > rows) {
+            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row[k]), vf[k], p);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int at = r + (i >> 2) * 8 + 4 * (lane >> 5) + (i & 3);
-                const bool sees = at >= mine_from && at < mine_until;
-                s[i] = sees ? s[i] : 0.f;
-                p[i] = sees ? p[i] : 0.f;
+                s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
+                p[i] *= s[i];
             }
-        }
+            if (r < all_from || r + 32 > all_until || r + 32 > rows) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const bf16x8 pf = pack8(s, x), sf = pack8(p, x);
+                for (int i = 0; i < 16; ++i) {
+                    const int at = r + (i >> 2) * 8 + 4 * (lane >> 5) + (i & 3);
+                    const bool sees = at >= mine_from && at < mine_until;
+                    s[i] = sees ? s[i] : 0.f;
+                    p[i] = sees ? p[i] : 0.f;
+                }
+            }
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                dv[d] = mfma(read_tr<DB>(td + x * 16 * S::pitch, rd, d), pf, dv[d]);
-                dk[d] = mfma(read_tr<DB>(tq + x * 16 * S::pitch, rd, d), sf, dk[d]);
+            for (int x = 0; x < 2; ++x) {
+                const bf16x8 pf = pack8(s, x), sf = pack8(p, x);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    dv[d] = mfma(read_tr<DB>(td + x * 16 * S::pitch, rd, d), pf, dv[d]);
+                    dk[d] = mfma(read_tr<DB>(tq + x * 16 * S::pitch, rd, d), sf, dk[d]);
+                }
             }
         }
     }

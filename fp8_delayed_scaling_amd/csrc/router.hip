@@ -189,24 +189,48 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const Route a) {
     finish_loss(a, sums[0], cnt, red);
 }
 
-// The blocks' counts and sums, added in order.
-__global__ __launch_bounds__(kThreads) void k_moe_route_join(const Route a, int nb) {
-    __shared__ float sums[kMoeMaxExperts];
-    __shared__ int cnt[kMoeMaxExperts + 1];
+// The blocks' counts and sums: `groups` threads an expert take every groups-th block, the groups are added in order.
+__global__ __launch_bounds__(kThreads) void k_moe_route_join(const Route a, int nb, int log2_e) {
+    __shared__ float sums[kThreads];
+    __shared__ int cnt[kThreads + 1];
     __shared__ float red[2 * kWaves];
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) {
-        float s = 0.f;
-        int c = 0;
-        for (int b = 0; b < nb; ++b) {
-            if (e < a.E) s += a.part_sum[(int64_t)b * a.E + e];
+    const int t = threadIdx.x, e = t & ((1 << log2_e) - 1), groups = kThreads >> log2_e;
+    float s = 0.f;
+    int c = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int b = t >> log2_e; b < nb; b += groups) {
+            s += a.part_sum[(int64_t)b * a.E + e];
             c += a.part_cnt[(int64_t)b * (a.E + 1) + e];
         }
-        if (e < a.E) {
-            a.prob_sum[e] = s;
-            sums[e] = s;
+    }
+    sums[t] = s;
+    cnt[t] = c;
+    int live = 0;
+    if (t < 64) {
+        for (int b = t; b < nb; b += 64) live += a.part_cnt[(int64_t)b * (a.E + 1) + a.E];
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) live += __shfl_xor(live, o, 64);
+    }
+    __syncthreads();
+    if (t < a.E) {
+        s = 0.f;
+        c = 0;
+        for (int g = 0; g < groups; ++g) {
+            s += sums[(g << log2_e) + t];
+            c += cnt[(g << log2_e) + t];
         }
-        a.counts[e] = c;
-        cnt[e] = c;
+        a.prob_sum[t] = s;
+        a.counts[t] = c;
+    }
+    __syncthreads();
+    if (t < a.E) {
+        sums[t] = s;
+        cnt[t] = c;
+    }
+    if (t == 0) {
+        a.counts[a.E] = live;
+        cnt[a.E] = live;
     }
     __syncthreads();
     finish_loss(a, sums, cnt, red);
@@ -308,7 +332,9 @@ hipError_t launch_moe_route(Route a, void *ws, hipStream_t st) {
     a.part_cnt = static_cast<int32_t *>(ws) + nb * a.E;
     FP8DS_BY_EXPERTS(k_moe_route, nb, kThreads);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || nb == 1) return e;
-    k_moe_route_join<<<1, kThreads, 0, st>>>(a, (int)nb);
+    int log2_e = 0;
+    while ((1 << log2_e) < a.E) ++log2_e;
+    k_moe_route_join<<<1, kThreads, 0, st>>>(a, (int)nb, log2_e);
     return hipGetLastError();
 }
 

@@ -30,6 +30,8 @@ def buffers(T, E, top):
 def run(x, top, normalise=True, stream=None):
     b = buffers(x.shape[0], x.shape[1], top)
     ws = torch.full((max(4, F.fp8_moe_route_workspace_bytes(*x.shape)),), 0xFF, dtype=torch.uint8, device=DEV)
+    if stream is not None:
+        torch.cuda.synchronize()                       # the buffers' filling, on the current stream
     F.fp8_moe_route(x, *b.values(), ws, normalise, stream=stream)
     return b
 
@@ -160,9 +162,9 @@ def test_strided_rows():
 
 # ------------------------------------------------------------------------------------ gradient
 
-def backward(x, f, dweights, dloss, normalise, stream=None):
+def backward(x, f, dweights, dloss, normalise):
     d = torch.full_like(x, 7.0)
-    F.fp8_moe_route_bwd(x, f["experts"], f["weights"], f["lse"], f["counts"], dweights, dloss, d, normalise, stream=stream)
+    F.fp8_moe_route_bwd(x, f["experts"], f["weights"], f["lse"], f["counts"], dweights, dloss, d, normalise)
     return d
 
 
@@ -279,7 +281,13 @@ def test_repeats_captured_and_on_other_streams():
     other = run(x, 4, stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(want[n], other[n]) for n in want)
-    assert torch.equal(d, backward(x, want, dw, dl, True, stream=side.cuda_stream))
+    step()
+    torch.cuda.synchronize()
+    other = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    F.fp8_moe_route_bwd(x, want["experts"], want["weights"], want["lse"], want["counts"], dw, dl, other, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(d, other)
 
 
 def test_feeds_the_plan():
