@@ -128,6 +128,22 @@ template <int DB> __device__ __forceinline__ bf16x8 read_tr(const uint8_t *p, co
     const i16x4 a = read_tr4(p + rd.tr[d][0]), b = read_tr4(p + rd.tr[d][1]);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
+// The same addresses from three registers: the pieces' numbers enter by exclusive or.  16 of those a step cost less than
+// 13 registers where these are short.
+template <int DB> struct Walker {
+    uint32_t row0, tr0, tr1;
+    __device__ __forceinline__ explicit Walker(int lane) {
+        const Reader<DB> rd(lane);
+        row0 = rd.row[0], tr0 = rd.tr[0][0], tr1 = rd.tr[0][1];
+    }
+    // keeps the addresses from being computed ahead of the loop, into registers
+    __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(row0), "+v"(tr0), "+v"(tr1)); }
+    __device__ __forceinline__ uint32_t row(int k) const { return row0 ^ (k * 32); }
+    __device__ __forceinline__ bf16x8 tr(const uint8_t *p, int d) const {
+        const i16x4 a = read_tr4(p + (tr0 ^ (d * 64))), b = read_tr4(p + (tr1 ^ (d * 64)));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 // eight of the 16 values that a lane holds of a 32 x 32 product, as an operand of the next
 __device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int s) {
@@ -577,29 +593,48 @@ __global__ __launch_bounds__(kThreads) void k_attn_delta(const Attention a) {
     }
 }
 
-// Rows of the group's heads, 64 at a time from row r0, for 4 waves: token pos, head g of the group.
+// Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  The rows are
+// walked, not divided: a lane's row moves on by 64, its further loads lie 16 or 32 rows behind.
 template <int DB> struct GroupLoads {
     using S = Shape<DB>;
-    static constexpr int n = kStepRows / (S::rows_a_load * kWaves);  // loads of a wave for one tile
-    int row[n];                                                      // of the tile
+    static constexpr int rows_a_turn = S::rows_a_load * kWaves, n = kStepRows / rows_a_turn;       // loads of a wave for one tile
+    int r, p, g;                                                     // the lane's row of the next tile, token after p0, head
+    int p0, g0;                                                      // token and head of the tile's first row
     uint32_t piece;                                                  // byte in the row, kOutside past the head
     int wave;
-    __device__ __forceinline__ GroupLoads(int lane, int wave_, int D) : wave(wave_) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) row[i] = (i * kWaves + wave) * S::rows_a_load + lane / S::pieces;
-        const int c = (lane % S::pieces) ^ S::swz(row[0]);           // loads are 16 or 32 rows apart: the same piece
+    __device__ __forceinline__ GroupLoads(int lane, int wave_, int D, int G, int first) : wave(wave_) {
+        const int row = wave * S::rows_a_load + lane / S::pieces;
+        const int c = (lane % S::pieces) ^ S::swz(row);              // loads are 16 or 32 rows apart: the same piece
         piece = c * 8 < D ? c * 16 : kOutside;
+        r = first + row;
+        p0 = first / G, g0 = first - p0 * G;
+        p = r / G, g = r - p * G;
+        p -= p0;
     }
-    // of the sequence's rows r0 ..; base: the sequence's first token at the group's first head
-    __device__ __forceinline__ void operator()(const uint16_t *base, int64_t ts, int64_t hs, int G, int r0, int rows, uint8_t *tile) const {
-        const int p0 = r0 / G;
-        const auto rs = bounded(base + (int64_t)p0 * ts, 0x7FFFFFFFu);
+    // Q's and dO's rows; the bases: the sequence's first token at the group's first head
+    __device__ __forceinline__ void operator()(const uint16_t *q, int q_ts, int q_hs, const uint16_t *o, int o_ts, int o_hs, int G, int rows,
+                                               uint8_t *tq, uint8_t *to) {
+        const auto rq = bounded(q + (int64_t)p0 * q_ts, 0x7FFFFFFFu), ro = bounded(o + (int64_t)p0 * o_ts, 0x7FFFFFFFu);
+        const int dp = rows_a_turn / G, dg = rows_a_turn - dp * G;   // uniform
+        int x = p, y = g;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const int r = r0 + row[i], p = r / G, g = r - p * G;
-            const uint32_t off = piece + (uint32_t)((p - p0) * (int)ts + g * (int)hs) * 2u;
-            load_lds(rs, tile + (i * kWaves + wave) * 1024, r < rows && piece != kOutside ? off : kOutside);
+            const bool in = r + i * rows_a_turn < rows && piece != kOutside;
+            const uint32_t oq = piece + (uint32_t)(__mul24(x, q_ts) + y * q_hs) * 2u, oo = piece + (uint32_t)(__mul24(x, o_ts) + y * o_hs) * 2u;
+            load_lds(rq, tq + (i * kWaves + wave) * 1024, in ? oq : kOutside);
+            load_lds(ro, to + (i * kWaves + wave) * 1024, in ? oo : kOutside);
+            y += dg, x += dp;
+            if (y >= G) y -= G, ++x;
         }
+        r += kStepRows;
+        // the lane's row and the tile's first, 64 rows on
+        const int tp = kStepRows / G, tg = kStepRows - tp * G;
+        g += tg, p += tp;
+        if (g >= G) g -= G, ++p;
+        g0 += tg;
+        const int moved = tp + (g0 >= G);
+        if (g0 >= G) g0 -= G;
+        p0 += moved, p -= moved;
     }
 };
 
@@ -633,19 +668,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
     const int mine_from = from(key), mine_until = until(key);
 
-    const GroupLoads<DB> loads(lane, wave, a.D);
+    GroupLoads<DB> loads(lane, wave, a.D, G, lo);
     const uint16_t *qp = a.q.p + sq.begin * a.q.ts + (int64_t)kvh * G * a.q.hs;
     const uint16_t *dp = a.dout.p + sq.begin * a.dout.ts + (int64_t)kvh * G * a.dout.hs;
     const int64_t all = (int64_t)a.Tq * a.Hq, row0 = ((int64_t)kvh * a.Tq + sq.begin) * G;
     const auto rs_stats = bounded(a.part, (uint32_t)(all * 8));
     auto load = [&](int r, int to) {
-        loads(qp, a.q.ts, a.q.hs, G, r, rows, smem + to * kTile);
-        loads(dp, a.dout.ts, a.dout.hs, G, r, rows, smem + (2 + to) * kTile);
+        loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, smem + to * kTile, smem + (2 + to) * kTile);
         if (wave < 2)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(stats[to] + wave * kStepRows), 4,
                                                      (uint32_t)(row0 + r + lane + wave * all) * 4u, 0, 0, 0);
     };
-    const Reader<DB> rd(lane);
+    Walker<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
     f32x16 dk[DB], dv[DB];
 #pragma unroll
@@ -664,6 +698,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
             if (r >= w_end || r + 32 <= w_first) continue;
             const uint8_t *tq = smem + turn * kTile + part * 32 * S::pitch, *td = smem + (2 + turn) * kTile + part * 32 * S::pitch;
             const float *st = &stats[turn][part * 32 + 4 * (lane >> 5)];
+            rd.fresh();
             f32x16 s, p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -675,9 +710,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
                 }
             }
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row[k]), kf[k], s);
+            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row(k)), kf[k], s);
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row[k]), vf[k], p);
+            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row(k)), vf[k], p);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
@@ -697,8 +732,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
                 const bf16x8 pf = pack8(s, x), sf = pack8(p, x);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    dv[d] = mfma(read_tr<DB>(td + x * 16 * S::pitch, rd, d), pf, dv[d]);
-                    dk[d] = mfma(read_tr<DB>(tq + x * 16 * S::pitch, rd, d), sf, dk[d]);
+                    dv[d] = mfma(rd.tr(td + x * 16 * S::pitch, d), pf, dv[d]);
+                    dk[d] = mfma(rd.tr(tq + x * 16 * S::pitch, d), sf, dk[d]);
                 }
             }
         }
