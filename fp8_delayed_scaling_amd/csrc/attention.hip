@@ -338,7 +338,8 @@ template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     using S = Shape<DB>;
     constexpr int kTile = kKeys * S::pitch;
-    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // K, K, V, V
+    // two turns of K and V: arrays of their own, so that reading one does not wait for the loads into the other
+    __shared__ __align__(1024) uint8_t k0[kTile], k1[kTile], v0[kTile], v1[kTile];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     write_inverse(a);
     const int kvh = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, split = rest % a.splits;
@@ -370,22 +371,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     const float s2 = a.softmax_scale * kLog2e;
     Softmax<DB, 2> sm;
     if (lo < hi) {
-        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, smem);
-        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, smem + 2 * kTile);
+        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
+        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
     }
-    int turn = 0;
-    for (int j = lo; j < hi; j += kKeys, turn ^= 1) {
+    auto turn = [&](int j, const uint8_t *tk, const uint8_t *tv, uint8_t *next_k, uint8_t *next_v) __attribute__((always_inline)) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
         const int next = j + kKeys;
         if (next < hi) {
-            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, smem + (turn ^ 1) * kTile);
-            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, smem + (2 + (turn ^ 1)) * kTile);
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v);
         }
         if (j < end.hi && next > first.lo) {
             const bool masked = next > first.hi || j < end.lo;
-            sm.step(smem + turn * kTile, smem + (2 + turn) * kTile, rd, qf, s2, masked, j, see, lane);
+            sm.step(tk, tv, rd, qf, s2, masked, j, see, lane);
         }
+    };
+    for (int j = lo; j < hi; j += 2 * kKeys) {
+        turn(j, k0, v0, k1, v1);
+        if (j + kKeys >= hi) break;
+        turn(j + kKeys, k1, v1, k0, v0);
     }
     const float l = both_halves_sum(sm.l);
     if (a.splits > 1) {
@@ -428,7 +433,10 @@ template <int DB>
 __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a) {
     using S = Shape<DB>;
     constexpr int kTile = 32 * S::pitch, kPitch = 32 * DB + 4;       // floats of an output row in LDS
-    __shared__ __align__(1024) uint8_t smem[kWaves * 4 * kTile > kWaves * 32 * kPitch * 4 ? kWaves * 4 * kTile : kWaves * 32 * kPitch * 4];
+    // each wave's K and V, two turns; afterwards the waves' sums
+    constexpr int kPart = kWaves * kTile;
+    static_assert(kPart >= 32 * kPitch * 4, "an array holds one wave's sums");
+    __shared__ __align__(1024) uint8_t k0[kPart], k1[kPart], v0[kPart], v1[kPart];
     __shared__ float stats[kWaves][32][2];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     write_inverse(a);
@@ -455,25 +463,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
     Softmax<DB, 1> sm;
-    uint8_t *mine = smem + wave * 4 * kTile;                         // K, V, K, V
-    int j = lo + wave * 32, turn = 0;
+    const int mine = wave * kTile;
+    int j = lo + wave * 32;
     if (j < hi) {
-        loads_k(kp + (int64_t)j * a.k.ts, a.k.ts, sk.len - j, mine);
-        loads_v(vp + (int64_t)j * a.v.ts, a.v.ts, sk.len - j, mine + kTile);
+        loads_k(kp + (int64_t)j * a.k.ts, a.k.ts, sk.len - j, k0 + mine);
+        loads_v(vp + (int64_t)j * a.v.ts, a.v.ts, sk.len - j, v0 + mine);
     }
-    for (; j < hi; j += kStep, turn ^= 1) {
-        const int next = j + kStep;
+    auto turn = [&](int at, const uint8_t *tk, const uint8_t *tv, uint8_t *next_k, uint8_t *next_v) __attribute__((always_inline)) {
+        const int next = at + kStep;
         FP8DS_WAIT_LGKM();                                           // the reads of the tile that is overwritten next
+        asm volatile("" ::: "memory");
         if (next < hi) {
-            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, mine + (turn ^ 1) * 2 * kTile);
-            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, mine + ((turn ^ 1) * 2 + 1) * kTile);
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k + mine);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v + mine);
             FP8DS_WAIT_VM(2 * decltype(loads_k)::n);
         } else {
             FP8DS_WAIT_VM(0);
         }
         asm volatile("" ::: "memory");
-        const bool masked = j + 32 > first.hi || j < end.lo;
-        sm.step(mine + turn * 2 * kTile, mine + (turn * 2 + 1) * kTile, rd, qf, s2, masked, j, see, lane);
+        const bool masked = at + 32 > first.hi || at < end.lo;
+        sm.step(tk + mine, tv + mine, rd, qf, s2, masked, at, see, lane);
+    };
+    for (; j < hi; j += 2 * kStep) {
+        turn(j, k0, v0, k1, v1);
+        if (j + kStep >= hi) break;
+        turn(j + kStep, k1, v1, k0, v0);
     }
     // the four waves' sums, joined in order
     const float l = both_halves_sum(sm.l);
@@ -482,12 +496,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
         stats[wave][lane][1] = l;
     }
     __syncthreads();
-    float *sums = reinterpret_cast<float *>(smem);
+    const uint8_t *const sums[kWaves] = {k0, k1, v0, v1};
+    uint8_t *own = wave == 0 ? k0 : wave == 1 ? k1 : wave == 2 ? v0 : v1;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4 *>(sums + (wave * 32 + (lane & 31)) * kPitch + d * 32 + i * 8 + (lane >> 5) * 4) =
+            *reinterpret_cast<f32x4 *>(own + ((lane & 31) * kPitch + d * 32 + i * 8 + (lane >> 5) * 4) * 4) =
                 f32x4{sm.o[d][4 * i], sm.o[d][4 * i + 1], sm.o[d][4 * i + 2], sm.o[d][4 * i + 3]};
     __syncthreads();
     Emit emit(a);
@@ -503,7 +518,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
             const float wt = stats[i][x][0] == -kInf ? 0.f : __builtin_amdgcn_exp2f(stats[i][x][0] - m);
             sum += stats[i][x][1] * wt;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] += sums[(i * 32 + x) * kPitch + d + u] * wt;
+            for (int u = 0; u < 8; ++u) v[u] += reinterpret_cast<const float *>(sums[i])[x * kPitch + d + u] * wt;
         }
         const int64_t token = sq.begin + p, row = token * a.Hq + hd;
         if (a.splits > 1) {
@@ -643,8 +658,8 @@ template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
     constexpr int kTile = kStepRows * S::pitch;
-    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // Q, Q, dO, dO
-    __shared__ __align__(256) float stats[2][2 * kStepRows];         // the rows' -lse / scale, then -delta
+    __shared__ __align__(1024) uint8_t q0[kTile], q1[kTile], o0[kTile], o1[kTile];      // Q and dO, two turns
+    __shared__ __align__(256) float st0[2 * kStepRows], st1[2 * kStepRows];             // the rows' -lse / scale, then -delta
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hkv;
     int b, tile;
@@ -673,10 +688,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     const uint16_t *dp = a.dout.p + sq.begin * a.dout.ts + (int64_t)kvh * G * a.dout.hs;
     const int64_t all = (int64_t)a.Tq * a.Hq, row0 = ((int64_t)kvh * a.Tq + sq.begin) * G;
     const auto rs_stats = bounded(a.part, (uint32_t)(all * 8));
-    auto load = [&](int r, int to) {
-        loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, smem + to * kTile, smem + (2 + to) * kTile);
+    auto load = [&](int r, uint8_t *tq, uint8_t *to, float *ts) __attribute__((always_inline)) {
+        loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, tq, to);
         if (wave < 2)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(stats[to] + wave * kStepRows), 4,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(ts + wave * kStepRows), 4,
                                                      (uint32_t)(row0 + r + lane + wave * all) * 4u, 0, 0, 0);
     };
     Walker<DB> rd(lane);
@@ -686,18 +701,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
-    if (lo < hi) load(lo, 0);
-    int turn = 0;
-    for (int r0 = lo; r0 < hi; r0 += kStepRows, turn ^= 1) {
+    if (lo < hi) load(lo, q0, o0, st0);
+    auto turn = [&](int r0, const uint8_t *step_q, const uint8_t *step_o, const float *step_st, uint8_t *next_q, uint8_t *next_o,
+                    float *next_st) __attribute__((always_inline)) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
-        if (r0 + kStepRows < hi) load(r0 + kStepRows, turn ^ 1);
+        if (r0 + kStepRows < hi) load(r0 + kStepRows, next_q, next_o, next_st);
 #pragma unroll
         for (int part = 0; part < kStepRows / 32; ++part) {
             const int r = r0 + part * 32;
             if (r >= w_end || r + 32 <= w_first) continue;
-            const uint8_t *tq = smem + turn * kTile + part * 32 * S::pitch, *td = smem + (2 + turn) * kTile + part * 32 * S::pitch;
-            const float *st = &stats[turn][part * 32 + 4 * (lane >> 5)];
+            const uint8_t *tq = step_q + part * 32 * S::pitch, *td = step_o + part * 32 * S::pitch;
+            const float *st = step_st + part * 32 + 4 * (lane >> 5);
             rd.fresh();
             f32x16 s, p;
 #pragma unroll
@@ -737,6 +752,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
                 }
             }
         }
+    };
+    for (int r = lo; r < hi; r += 2 * kStepRows) {
+        turn(r, q0, o0, st0, q1, o1, st1);
+        if (r + kStepRows >= hi) break;
+        turn(r + kStepRows, q1, o1, st1, q0, o0, st0);
     }
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -760,7 +780,7 @@ template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;
     constexpr int kTile = kKeys * S::pitch;
-    __shared__ __align__(1024) uint8_t smem[4 * kTile];              // K, K, V, V
+    __shared__ __align__(1024) uint8_t k0[kTile], k1[kTile], v0[kTile], v1[kTile];      // as in the forward
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hkv;
     int b, tile;
@@ -793,23 +813,22 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[d][i] = 0.f;
     if (lo < hi) {
-        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, smem);
-        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, smem + 2 * kTile);
+        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
+        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
     }
-    int turn = 0;
-    for (int j = lo; j < hi; j += kKeys, turn ^= 1) {
+    auto turn = [&](int j, const uint8_t *tk, const uint8_t *tv, uint8_t *next_k, uint8_t *next_v) __attribute__((always_inline)) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
         const int next = j + kKeys;
         if (next < hi) {
-            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, smem + (turn ^ 1) * kTile);
-            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, smem + (2 + (turn ^ 1)) * kTile);
+            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k);
+            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v);
         }
-        if (j >= end.hi || next <= first.lo) continue;
+        if (j >= end.hi || next <= first.lo) return;
         const bool masked = next > first.hi || j < end.lo;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            const uint8_t *tk = smem + turn * kTile + kb * 32 * S::pitch, *tv = smem + (2 + turn) * kTile + kb * 32 * S::pitch;
+            const uint8_t *rk = tk + kb * 32 * S::pitch, *rv = tv + kb * 32 * S::pitch;
             f32x16 s, p;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -817,9 +836,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
                 p[i] = delta;
             }
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tk + rd.row[k]), qf[k], s);
+            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(rk + rd.row[k]), qf[k], s);
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(tv + rd.row[k]), df[k], p);
+            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(rv + rd.row[k]), df[k], p);
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, low));
             if (masked) {
@@ -834,9 +853,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
             for (int x = 0; x < 2; ++x) {
                 const bf16x8 sf = pack8(p, x);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) dq[d] = mfma(read_tr<DB>(tk + x * 16 * S::pitch, rd, d), sf, dq[d]);
+                for (int d = 0; d < DB; ++d) dq[d] = mfma(read_tr<DB>(rk + x * 16 * S::pitch, rd, d), sf, dq[d]);
             }
         }
+    };
+    for (int j = lo; j < hi; j += 2 * kKeys) {
+        turn(j, k0, v0, k1, v1);
+        if (j + kKeys >= hi) break;
+        turn(j + kKeys, k1, v1, k0, v0);
     }
 #pragma unroll
     for (int d = 0; d < DB; ++d)
