@@ -52,12 +52,11 @@ __device__ __forceinline__ Span span_of(const int32_t *off, int b, int T, int B)
 
 // Tile t of the sequences' rows (`group` rows a token, `height` rows a tile): its sequence and its number in it,
 // the last tile of a sequence first.  False past the last.
-__device__ __forceinline__ bool find_tile(const int32_t *off, int T, int B, int group, int height, int t, int &b, int &tile, bool pairs = false) {
+__device__ __forceinline__ bool find_tile(const int32_t *off, int T, int B, int group, int height, int t, int &b, int &tile) {
     if (off == nullptr) {
         const int n = (T / B * group + height - 1) / height;
         b = t % B;
         tile = n - 1 - t / B;
-        if (pairs && 2 * tile < n) tile = (n - 1) / 2 - tile;     // the second half the other way round
         return tile >= 0;
     }
     const int lane = threadIdx.x & 63;
@@ -609,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_delta(const Attention a) {
 }
 
 // Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  The rows are
-// walked, not divided: a lane's row moves on by 64, its further loads lie 16 or 32 rows behind.
+// walked, not divided: a lane's row moves on by 128 (two sets of waves), its further loads lie 16 or 32 rows behind.
 template <int DB> struct GroupLoads {
     using S = Shape<DB>;
     static constexpr int rows_a_turn = S::rows_a_load * kWaves, n = kStepRows / rows_a_turn;       // loads of a wave for one tile
@@ -641,9 +640,9 @@ template <int DB> struct GroupLoads {
             y += dg, x += dp;
             if (y >= G) y -= G, ++x;
         }
-        r += kStepRows;
-        // the lane's row and the tile's first, 64 rows on
-        const int tp = kStepRows / G, tg = kStepRows - tp * G;
+        r += 2 * kStepRows;
+        // the lane's row and the tile's first, 128 rows on
+        const int tp = 2 * kStepRows / G, tg = 2 * kStepRows - tp * G;
         g += tg, p += tp;
         if (g >= G) g -= G, ++p;
         g0 += tg;
@@ -653,18 +652,20 @@ template <int DB> struct GroupLoads {
     }
 };
 
-// A block: 128 keys of one key/value head, 32 to each wave, over all query rows of its group that see them.
+// A block: 128 keys of one key/value head over all query rows of its group that see them.  Two sets of four waves take
+// turns at the steps of 64 rows, 32 keys to each wave of a set; the second set's sums are added to the first's at the end.
 template <int DB>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
+__global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
     constexpr int kTile = kStepRows * S::pitch;
-    __shared__ __align__(1024) uint8_t q0[kTile], q1[kTile], o0[kTile], o1[kTile];      // Q and dO, two turns
-    __shared__ __align__(256) float st0[2 * kStepRows], st1[2 * kStepRows];             // the rows' -lse / scale, then -delta
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    __shared__ __align__(1024) uint8_t q0[2 * kTile], q1[2 * kTile], o0[2 * kTile], o1[2 * kTile];     // Q and dO of each set, two turns
+    __shared__ __align__(256) float st0[2][2 * kStepRows], st1[2][2 * kStepRows];    // the rows' -lse / scale, then -delta
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6 & 3), set = uniform(threadIdx.x >> 8);
     const int kvh = blockIdx.x % a.Hkv;
     int b, tile;
-    if (!find_tile(a.offsets_k, a.Tk, a.B, 1, kRows, blockIdx.x / a.Hkv, b, tile, gridDim.x <= 512)) return;
+    if (!find_tile(a.offsets_k, a.Tk, a.B, 1, kRows, blockIdx.x / a.Hkv, b, tile)) return;
     const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    if (a.causal) tile = (sk.len + kRows - 1) / kRows - 1 - tile;    // the keys that most rows see first
     const int G = a.G, rows = sq.len * G, j0 = tile * kRows, past = sk.len - sq.len;
     const int jw = j0 + wave * 32, key = jw + (lane & 31);
     const bool there = key < sk.len;
@@ -683,15 +684,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
     const int mine_from = from(key), mine_until = until(key);
 
-    GroupLoads<DB> loads(lane, wave, a.D, G, lo);
+    GroupLoads<DB> loads(lane, wave, a.D, G, lo + set * kStepRows);
     const uint16_t *qp = a.q.p + sq.begin * a.q.ts + (int64_t)kvh * G * a.q.hs;
     const uint16_t *dp = a.dout.p + sq.begin * a.dout.ts + (int64_t)kvh * G * a.dout.hs;
     const int64_t all = (int64_t)a.Tq * a.Hq, row0 = ((int64_t)kvh * a.Tq + sq.begin) * G;
     const auto rs_stats = bounded(a.part, (uint32_t)(all * 8));
-    auto load = [&](int r, uint8_t *tq, uint8_t *to, float *ts) __attribute__((always_inline)) {
-        loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, tq, to);
+    auto load = [&](int r, uint8_t *tq, uint8_t *to, float (*ts)[2 * kStepRows]) __attribute__((always_inline)) {
+        loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, tq + set * kTile, to + set * kTile);
         if (wave < 2)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(ts + wave * kStepRows), 4,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(ts[set] + wave * kStepRows), 4,
                                                      (uint32_t)(row0 + r + lane + wave * all) * 4u, 0, 0, 0);
     };
     Walker<DB> rd(lane);
@@ -701,33 +702,51 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
-    if (lo < hi) load(lo, q0, o0, st0);
-    auto turn = [&](int r0, const uint8_t *step_q, const uint8_t *step_o, const float *step_st, uint8_t *next_q, uint8_t *next_o,
-                    float *next_st) __attribute__((always_inline)) {
+    // r0: the first set's rows; the second's lie 64 behind
+    if (lo + set * kStepRows < hi) load(lo + set * kStepRows, q0, o0, st0);
+    auto turn = [&](int r0, const uint8_t *step_q, const uint8_t *step_o, const float (*step_st)[2 * kStepRows], uint8_t *next_q,
+                    uint8_t *next_o, float (*next_st)[2 * kStepRows]) __attribute__((always_inline)) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
-        if (r0 + kStepRows < hi) load(r0 + kStepRows, next_q, next_o, next_st);
+        r0 += set * kStepRows;
+        if (r0 + 2 * kStepRows < hi) load(r0 + 2 * kStepRows, next_q, next_o, next_st);
 #pragma unroll
         for (int part = 0; part < kStepRows / 32; ++part) {
             const int r = r0 + part * 32;
             if (r >= w_end || r + 32 <= w_first) continue;
-            const uint8_t *tq = step_q + part * 32 * S::pitch, *td = step_o + part * 32 * S::pitch;
-            const float *st = step_st + part * 32 + 4 * (lane >> 5);
+            const uint8_t *tq = step_q + set * kTile + part * 32 * S::pitch, *td = step_o + set * kTile + part * 32 * S::pitch;
+            const float *st = step_st[set] + part * 32 + 4 * (lane >> 5);
             rd.fresh();
+            __builtin_amdgcn_sched_barrier(0);
             f32x16 s, p;
+            auto start = [&](f32x16 &v, const float *from) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(st + 8 * i), y = *reinterpret_cast<const f32x4 *>(st + kStepRows + 8 * i);
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 x = *reinterpret_cast<const f32x4 *>(from + 8 * i);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    s[4 * i + u] = x[u];
-                    p[4 * i + u] = y[u];
+                    for (int u = 0; u < 4; ++u) v[4 * i + u] = x[u];
                 }
-            }
+            };
+            start(s, st);
 #pragma unroll
             for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row(k)), kf[k], s);
+            start(p, st + kStepRows);
 #pragma unroll
             for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row(k)), vf[k], p);
+            // four operands ahead of the products
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+            for (int k = 0; k < S::ks - 4; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < S::ks; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
@@ -742,22 +761,54 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dkv(const Attention a) {
                     p[i] = sees ? p[i] : 0.f;
                 }
             }
+            const bf16x8 pf[2] = {pack8(s, 0), pack8(s, 1)}, sf[2] = {pack8(p, 0), pack8(p, 1)};
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const bf16x8 pf = pack8(s, x), sf = pack8(p, x);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    dv[d] = mfma(rd.tr(td + x * 16 * S::pitch, d), pf, dv[d]);
-                    dk[d] = mfma(rd.tr(tq + x * 16 * S::pitch, d), sf, dk[d]);
+                    dv[d] = mfma(rd.tr(td + x * 16 * S::pitch, d), pf[x], dv[d]);
+                    dk[d] = mfma(rd.tr(tq + x * 16 * S::pitch, d), sf[x], dk[d]);
                 }
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+            for (int k = 0; k < 4 * DB - 4; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    for (int r = lo; r < hi; r += 2 * kStepRows) {
+    for (int r = lo; r < hi; r += 4 * kStepRows) {
         turn(r, q0, o0, st0, q1, o1, st1);
-        if (r + kStepRows >= hi) break;
-        turn(r + kStepRows, q1, o1, st1, q0, o0, st0);
+        if (r + 2 * kStepRows >= hi) break;
+        turn(r + 2 * kStepRows, q1, o1, st1, q0, o0, st0);
     }
+    // the second set's sums
+    FP8DS_WAIT_ALL();
+    __syncthreads();
+    static_assert(sizeof(q0) >= 2 * DB * 16 * 64 * 4, "an array holds a wave's sums");
+    float *mine = reinterpret_cast<float *>(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? o0 : o1) + lane;
+    if (set == 1) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                mine[(d * 16 + i) * 64] = dk[d][i];
+                mine[((DB + d) * 16 + i) * 64] = dv[d][i];
+            }
+    }
+    __syncthreads();
+    if (set == 1) return;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            dk[d][i] += mine[(d * 16 + i) * 64];
+            dv[d][i] += mine[((DB + d) * 16 + i) * 64];
+        }
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -878,7 +929,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
 // ---------------------------------------------------------------------------------- launches
 namespace {
 constexpr int kCUs = 256;
-constexpr int64_t kMostBlocks = (INT64_C(1) << 32) / kThreads - 1;
+constexpr int64_t kMostBlocks = (INT64_C(1) << 32) / (2 * kThreads) - 1;
 
 int64_t most_tiles(int64_t T, int64_t B, int64_t group, int64_t height, bool ragged) {
     return ragged ? T * group / height + B : B * ((T / B * group + height - 1) / height);
@@ -920,20 +971,20 @@ size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, 
 }
 size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq) { return (size_t)(Tq * Hq * 8); }
 
-#define FP8DS_BY_HEAD(KERNEL, BLOCKS)                                                                  \
+#define FP8DS_BY_HEAD(KERNEL, BLOCKS, THREADS)                                                                \
     do {                                                                                               \
         const dim3 grid((unsigned)(BLOCKS));                                                           \
-        if (a.D <= 64) KERNEL<2><<<grid, kThreads, 0, st>>>(a);                                        \
-        else if (a.D <= 96) KERNEL<3><<<grid, kThreads, 0, st>>>(a);                                   \
-        else KERNEL<4><<<grid, kThreads, 0, st>>>(a);                                                  \
+        if (a.D <= 64) KERNEL<2><<<grid, THREADS, 0, st>>>(a);                                        \
+        else if (a.D <= 96) KERNEL<3><<<grid, THREADS, 0, st>>>(a);                                   \
+        else KERNEL<4><<<grid, THREADS, 0, st>>>(a);                                                  \
     } while (0)
 
 hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st) {
     const Plan p = fwd_plan(a.Tq, a.Tk, a.B, a.Hkv, a.G, a.offsets_q != nullptr);
     a.splits = (int)p.splits;
     a.part = static_cast<float *>(ws);
-    if (p.few) FP8DS_BY_HEAD(k_attn_fwd_few, p.blocks);
-    else FP8DS_BY_HEAD(k_attn_fwd, p.blocks);
+    if (p.few) FP8DS_BY_HEAD(k_attn_fwd_few, p.blocks, kThreads);
+    else FP8DS_BY_HEAD(k_attn_fwd, p.blocks, kThreads);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || a.splits == 1) return e;
     k_attn_join<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
     return hipGetLastError();
@@ -944,9 +995,9 @@ hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st) {
     a.part = static_cast<float *>(ws);
     if (a.Tq > 0) k_attn_delta<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.Tk > 0) FP8DS_BY_HEAD(k_attn_dkv, most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv);
+    if (a.Tk > 0) FP8DS_BY_HEAD(k_attn_dkv, most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv, 2 * kThreads);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv);
+    if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv, kThreads);
     return hipGetLastError();
 }
 
