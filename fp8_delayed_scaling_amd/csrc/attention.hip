@@ -35,6 +35,12 @@ constexpr float kInf = __builtin_inff();
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// What follows from v is computed where it is used, not ahead of a loop that has no registers to keep it.
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // ---------------------------------------------------------------------------------- sequences
 struct Span {
     int64_t begin;
@@ -657,7 +663,7 @@ template <int DB> struct GroupLoads {
 template <int DB>
 __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = kStepRows * S::pitch;
+    constexpr int kTile = kStepRows * S::pitch, kAhead = DB == 4 ? 3 : 4;
     __shared__ __align__(1024) uint8_t q0[2 * kTile], q1[2 * kTile], o0[2 * kTile], o1[2 * kTile];     // Q and dO of each set, two turns
     __shared__ __align__(256) float st0[2][2 * kStepRows], st1[2][2 * kStepRows];    // the rows' -lse / scale, then -delta
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6 & 3), set = uniform(threadIdx.x >> 8);
@@ -668,11 +674,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     if (a.causal) tile = (sk.len + kRows - 1) / kRows - 1 - tile;    // the keys that most rows see first
     const int G = a.G, rows = sq.len * G, j0 = tile * kRows, past = sk.len - sq.len;
     const int jw = j0 + wave * 32, key = jw + (lane & 31);
-    const bool there = key < sk.len;
-    const int64_t token = sk.begin + key;
     bf16x8 kf[S::ks], vf[S::ks];
-    load_query<DB>(kf, a.k.p + token * a.k.ts + kvh * a.k.hs, there, a.D, lane >> 5);
-    load_query<DB>(vf, a.v.p + token * a.v.ts + kvh * a.v.hs, there, a.D, lane >> 5);
+    load_query<DB>(kf, a.k.p + (sk.begin + key) * a.k.ts + kvh * a.k.hs, key < sk.len, a.D, lane >> 5);
+    load_query<DB>(vf, a.v.p + (sk.begin + key) * a.v.ts + kvh * a.v.hs, key < sk.len, a.D, lane >> 5);
 
     // query rows that see key j: [(j - past) G, (j - past + window) G)
     auto from = [&](int j) { return a.causal ? (int)min(max((int64_t)(j - past) * G, (int64_t)0), (int64_t)rows) : 0; };
@@ -682,7 +686,6 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     const int lo = from(j0) & ~(kStepRows - 1), hi = until(min(j0 + kRows, sk.len) - 1);
     const int w_first = from(jw), w_end = until(jw + 31);            // rows that any key of the wave sees
     const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
-    const int mine_from = from(key), mine_until = until(key);
 
     GroupLoads<DB> loads(lane, wave, a.D, G, lo + set * kStepRows);
     const uint16_t *qp = a.q.p + sq.begin * a.q.ts + (int64_t)kvh * G * a.q.hs;
@@ -730,22 +733,23 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
             start(s, st);
 #pragma unroll
             for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row(k)), kf[k], s);
+            rd.fresh();
             start(p, st + kStepRows);
 #pragma unroll
             for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row(k)), vf[k], p);
-            // four operands ahead of the products
-            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+            // kAhead operands ahead of the products; the second sums' start comes in with the first four
+            __builtin_amdgcn_sched_group_barrier(0x100, 4 + kAhead, 0);
 #pragma unroll
-            for (int k = 0; k < S::ks - 4; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             }
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) {
+            for (int k = 0; k < 2 * S::ks - 4 - kAhead; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -753,6 +757,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
                 p[i] *= s[i];
             }
             if (r < all_from || r + 32 > all_until || r + 32 > rows) {
+                const int k = opaque(key), mine_from = from(k), mine_until = until(k);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int at = r + (i >> 2) * 8 + 4 * (lane >> 5) + (i & 3);
@@ -765,19 +770,20 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+                rd.fresh();
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     dv[d] = mfma(rd.tr(td + x * 16 * S::pitch, d), pf[x], dv[d]);
                     dk[d] = mfma(rd.tr(tq + x * 16 * S::pitch, d), sf[x], dk[d]);
                 }
             }
-            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
 #pragma unroll
-            for (int k = 0; k < 4 * DB - 4; ++k) {
+            for (int k = 0; k < 4 * DB - kAhead; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -802,6 +808,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     }
     __syncthreads();
     if (set == 1) return;
+    const int out = opaque(key);
+    const bool there = out < sk.len;
+    const int64_t token = sk.begin + out;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
