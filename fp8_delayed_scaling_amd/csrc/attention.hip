@@ -387,16 +387,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
             loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k);
             loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v);
         }
-        if (j < end.hi && next > first.lo) {
-            const bool masked = next > first.hi || j < end.lo;
-            sm.step(tk, tv, rd, qf, s2, masked, j, see, lane);
-        }
+        sm.step(tk, tv, rd, qf, s2, next > first.hi || j < end.lo, j, see, lane);
     };
-    for (int j = lo; j < hi; j += 2 * kKeys) {
+    // a branch around a step, or out of the loop between two, would have the sums copied at each
+    int j = lo;
+    for (; j + kKeys < hi; j += 2 * kKeys) {
         turn(j, k0, v0, k1, v1);
-        if (j + kKeys >= hi) break;
         turn(j + kKeys, k1, v1, k0, v0);
     }
+    if (j < hi) turn(j, k0, v0, k1, v1);
     const float l = both_halves_sum(sm.l);
     if (a.splits > 1) {
         if (!there) return;
@@ -489,11 +488,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
         const bool masked = at + 32 > first.hi || at < end.lo;
         sm.step(tk + mine, tv + mine, rd, qf, s2, masked, at, see, lane);
     };
-    for (; j < hi; j += 2 * kStep) {
+    for (; j + kStep < hi; j += 2 * kStep) {
         turn(j, k0, v0, k1, v1);
-        if (j + kStep >= hi) break;
         turn(j + kStep, k1, v1, k0, v0);
     }
+    if (j < hi) turn(j, k0, v0, k1, v1);
     // the four waves' sums, joined in order
     const float l = both_halves_sum(sm.l);
     if (lane < 32) {
@@ -588,31 +587,6 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
 }
 
 // ---------------------------------------------------------------------------------- backward
-// Of every query row, in the order [key/value head, token, head of the group]: -lse / scale and -<dout, out>.
-__global__ __launch_bounds__(kThreads) void k_attn_delta(const Attention a) {
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int d = (threadIdx.x & 15) * 8;
-    const int64_t token = row / a.Hq;
-    if (token >= a.Tq) return;
-    const int head = (int)(row - token * a.Hq);
-    float sum = 0.f;
-    if (d < a.D) {
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(a.dout.p + token * a.dout.ts + head * a.dout.hs + d);
-        const u32x4 y = *reinterpret_cast<const u32x4 *>(a.out.p + token * a.out.ts + head * a.out.hs + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum += bf16_lo(x[i]) * bf16_lo(y[i]) + bf16_hi(x[i]) * bf16_hi(y[i]);
-    }
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 16);
-    if (d == 0) {
-        const float lse = a.lse[(int64_t)head * a.Tq + token];
-        const int kvh = head / a.G;
-        const int64_t at = ((int64_t)kvh * a.Tq + token) * a.G + head - kvh * a.G;
-        a.part[at] = lse == -kInf ? -kInf : -lse / a.softmax_scale;
-        a.part[(int64_t)a.Tq * a.Hq + at] = -sum;
-    }
-}
-
 // Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  The rows are
 // walked, not divided: a lane's row moves on by 128 (two sets of waves), its further loads lie 16 or 32 rows behind.
 template <int DB> struct GroupLoads {
@@ -835,7 +809,8 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
         }
 }
 
-// A block: 128 query rows, 32 to each wave, over the keys that they see.
+// A block: 128 query rows, 32 to each wave, over the keys that they see.  It also leaves what the keys' gradients need of
+// each row in the workspace, in the order [key/value head, token, head of the group].
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;
@@ -855,11 +830,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
     load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, there, a.D, lane >> 5);
     const float s2 = a.softmax_scale * kLog2e;
+    // -lse / scale and -<dout, out> of the row, kept for the keys' gradients
     float low = -kInf, delta = 0.f;
+    {
+        bf16x8 of[S::ks];
+        load_query<DB>(of, a.out.p + token * a.out.ts + head * a.out.hs, there, a.D, lane >> 5);
+#pragma unroll
+        for (int k = 0; k < S::ks; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) delta -= (float)df[k][i] * (float)of[k][i];
+        delta = both_halves_sum(delta);
+    }
     if (there) {
-        const int64_t at = ((int64_t)kvh * a.Tq + sq.begin) * a.G + r;
-        low = a.part[at] * s2;
-        delta = a.part[(int64_t)a.Tq * a.Hq + at];
+        const float lse = a.lse[(int64_t)head * a.Tq + token];
+        low = lse == -kInf ? -kInf : -lse / a.softmax_scale;
+        if (lane < 32) {
+            const int64_t at = ((int64_t)kvh * a.Tq + sq.begin) * a.G + r;
+            a.part[at] = low;
+            a.part[(int64_t)a.Tq * a.Hq + at] = delta;
+        }
+        low *= s2;
     }
     const int lo = seen(a, r0 / a.G, sq.len, sk.len).lo & ~(kKeys - 1), hi = seen(a, last / a.G, sq.len, sk.len).hi;
     const Seen first = seen(a, min(r0w, last) / a.G, sq.len, sk.len), end = seen(a, min(r0w + 31, last) / a.G, sq.len, sk.len);
@@ -1002,11 +992,9 @@ hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st) {
 hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st) {
     const bool ragged = a.offsets_q != nullptr;
     a.part = static_cast<float *>(ws);
-    if (a.Tq > 0) k_attn_delta<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
+    if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv, kThreads);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (a.Tk > 0) FP8DS_BY_HEAD(k_attn_dkv, most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv, 2 * kThreads);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv, kThreads);
     return hipGetLastError();
 }
 
