@@ -41,6 +41,16 @@ __device__ __forceinline__ int opaque(int v) {
     return v;
 }
 
+// The lane's number, computed where it is used.
+__device__ __forceinline__ int lane_now() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
+__device__ __forceinline__ float uniform_value(float v) { return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v))); }
+// an offset, past every bound where left is negative
+__device__ __forceinline__ uint32_t held(uint32_t off, int left) { return off | ((uint32_t)left & kOutside); }
+
 // ---------------------------------------------------------------------------------- sequences
 struct Span {
     int64_t begin;
@@ -157,6 +167,11 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int s) {
     for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[8 * s + i];
     return r;
 }
+
+// What the scheduler puts next: n reads of LDS, products, or other vector instructions.
+#define group_reads(n) __builtin_amdgcn_sched_group_barrier(0x100, n, 0)
+#define group_products(n) __builtin_amdgcn_sched_group_barrier(0x008, n, 0)
+#define group_values(n) __builtin_amdgcn_sched_group_barrier(0x002, n, 0)
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
@@ -587,57 +602,69 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
 }
 
 // ---------------------------------------------------------------------------------- backward
-// Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  The rows are
-// walked, not divided: a lane's row moves on by 128 (two sets of waves), its further loads lie 16 or 32 rows behind.
-template <int DB> struct GroupLoads {
+// Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  A lane's loads of a
+// tile lie `turn` = 16 or 32 rows apart, its tiles 128 (two sets of waves).  EVEN: G divides `turn`, so that a lane keeps
+// its head and its offset, and only the bases move; otherwise the rows are walked, not divided.
+template <int DB, bool EVEN> struct GroupLoads {
     using S = Shape<DB>;
-    static constexpr int rows_a_turn = S::rows_a_load * kWaves, n = kStepRows / rows_a_turn;       // loads of a wave for one tile
-    int r, p, g;                                                     // the lane's row of the next tile, token after p0, head
-    int p0, g0;                                                      // token and head of the tile's first row
-    uint32_t piece;                                                  // byte in the row, kOutside past the head
+    static constexpr int turn = S::rows_a_load * kWaves, n = kStepRows / turn;       // loads of a wave for one tile
+    int p, g;                                                        // token after p0 and head of the lane's row of the next tile
+    int first, p0, g0;                                               // that tile's first row, its token and head
+    uint32_t off_q, off_o;                                           // EVEN: the lane's offsets; else off_q: its byte in a row
     int wave;
-    __device__ __forceinline__ GroupLoads(int lane, int wave_, int D, int G, int first) : wave(wave_) {
-        const int row = wave * S::rows_a_load + lane / S::pieces;
-        const int c = (lane % S::pieces) ^ S::swz(row);              // loads are 16 or 32 rows apart: the same piece
-        piece = c * 8 < D ? c * 16 : kOutside;
-        r = first + row;
+    __device__ __forceinline__ GroupLoads(int lane, int wave_, int D, int G, int first_, int q_ts, int q_hs, int o_ts, int o_hs)
+        : first(first_), wave(wave_) {
+        const int row = wave * S::rows_a_load + lane / S::pieces, r = first + row;
+        const int c = (lane % S::pieces) ^ S::swz(row);              // the same piece in all loads
         p0 = first / G, g0 = first - p0 * G;
         p = r / G, g = r - p * G;
         p -= p0;
+        off_q = c * 8 < D ? c * 16 : kOutside;                       // past the head: past every bound, whatever is added
+        off_o = off_q + (EVEN ? (uint32_t)(__mul24(p, o_ts) + g * o_hs) * 2u : 0u);
+        if (EVEN) off_q += (uint32_t)(__mul24(p, q_ts) + g * q_hs) * 2u;
     }
     // Q's and dO's rows; the bases: the sequence's first token at the group's first head
     __device__ __forceinline__ void operator()(const uint16_t *q, int q_ts, int q_hs, const uint16_t *o, int o_ts, int o_hs, int G, int rows,
                                                uint8_t *tq, uint8_t *to) {
         const auto rq = bounded(q + (int64_t)p0 * q_ts, 0x7FFFFFFFu), ro = bounded(o + (int64_t)p0 * o_ts, 0x7FFFFFFFu);
-        const int dp = rows_a_turn / G, dg = rows_a_turn - dp * G;   // uniform
+        const int dp = turn / G, dg = turn - dp * G;                 // uniform
+        // rows there are, less one, behind the lane's first
+        const int left = rows - 1 - first - wave * S::rows_a_load - lane_now() / S::pieces;
         int x = p, y = g;
+        off_q = (uint32_t)opaque((int)off_q), off_o = (uint32_t)opaque((int)off_o);
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const bool in = r + i * rows_a_turn < rows && piece != kOutside;
-            const uint32_t oq = piece + (uint32_t)(__mul24(x, q_ts) + y * q_hs) * 2u, oo = piece + (uint32_t)(__mul24(x, o_ts) + y * o_hs) * 2u;
-            load_lds(rq, tq + (i * kWaves + wave) * 1024, in ? oq : kOutside);
-            load_lds(ro, to + (i * kWaves + wave) * 1024, in ? oo : kOutside);
-            y += dg, x += dp;
-            if (y >= G) y -= G, ++x;
+            uint32_t oq = off_q + (uint32_t)(EVEN ? i * dp * q_ts : __mul24(x, q_ts) + y * q_hs) * 2u;
+            uint32_t oo = (EVEN ? off_o : off_q) + (uint32_t)(EVEN ? i * dp * o_ts : __mul24(x, o_ts) + y * o_hs) * 2u;
+            load_lds(rq, tq + (i * kWaves + wave) * 1024, held(oq, left - i * turn));
+            load_lds(ro, to + (i * kWaves + wave) * 1024, held(oo, left - i * turn));
+            if constexpr (!EVEN) {
+                y += dg, x += dp;
+                if (y >= G) y -= G, ++x;
+            }
         }
-        r += 2 * kStepRows;
-        // the lane's row and the tile's first, 128 rows on
+        first += 2 * kStepRows;
         const int tp = 2 * kStepRows / G, tg = 2 * kStepRows - tp * G;
-        g += tg, p += tp;
-        if (g >= G) g -= G, ++p;
-        g0 += tg;
-        const int moved = tp + (g0 >= G);
-        if (g0 >= G) g0 -= G;
-        p0 += moved, p -= moved;
+        if constexpr (EVEN) {
+            p0 += tp;
+        } else {
+            // the lane's row and the tile's first, 128 rows on
+            g += tg, p += tp;
+            if (g >= G) g -= G, ++p;
+            g0 += tg;
+            const int moved = tp + (g0 >= G);
+            if (g0 >= G) g0 -= G;
+            p0 += moved, p -= moved;
+        }
     }
 };
 
 // A block: 128 keys of one key/value head over all query rows of its group that see them.  Two sets of four waves take
 // turns at the steps of 64 rows, 32 keys to each wave of a set; the second set's sums are added to the first's at the end.
-template <int DB>
+template <int DB, bool EVEN>
 __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = kStepRows * S::pitch, kAhead = DB == 4 ? 3 : 4;
+    constexpr int kTile = kStepRows * S::pitch, kAhead = DB < 4 ? 3 : EVEN ? 2 : 1, kRun = 2 * DB;
     __shared__ __align__(1024) uint8_t q0[2 * kTile], q1[2 * kTile], o0[2 * kTile], o1[2 * kTile];     // Q and dO of each set, two turns
     __shared__ __align__(256) float st0[2][2 * kStepRows], st1[2][2 * kStepRows];    // the rows' -lse / scale, then -delta
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6 & 3), set = uniform(threadIdx.x >> 8);
@@ -661,7 +688,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     const int w_first = from(jw), w_end = until(jw + 31);            // rows that any key of the wave sees
     const int all_from = from(jw + 31), all_until = until(jw);       // rows that every key of the wave sees
 
-    GroupLoads<DB> loads(lane, wave, a.D, G, lo + set * kStepRows);
+    GroupLoads<DB, EVEN> loads(lane, wave, a.D, G, lo + set * kStepRows, (int)a.q.ts, (int)a.q.hs, (int)a.dout.ts, (int)a.dout.hs);
     const uint16_t *qp = a.q.p + sq.begin * a.q.ts + (int64_t)kvh * G * a.q.hs;
     const uint16_t *dp = a.dout.p + sq.begin * a.dout.ts + (int64_t)kvh * G * a.dout.hs;
     const int64_t all = (int64_t)a.Tq * a.Hq, row0 = ((int64_t)kvh * a.Tq + sq.begin) * G;
@@ -670,10 +697,10 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
         loads(qp, (int)a.q.ts, (int)a.q.hs, dp, (int)a.dout.ts, (int)a.dout.hs, G, rows, tq + set * kTile, to + set * kTile);
         if (wave < 2)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_stats, (__attribute__((address_space(3))) void *)(ts[set] + wave * kStepRows), 4,
-                                                     (uint32_t)(row0 + r + lane + wave * all) * 4u, 0, 0, 0);
+                                                     held((uint32_t)(row0 + r + lane_now() + wave * all) * 4u, rows - 1 - r - lane_now()), 0, 0, 0);
     };
     Walker<DB> rd(lane);
-    const float s2 = a.softmax_scale * kLog2e;
+    const float s2 = uniform_value(a.softmax_scale * kLog2e);
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -693,72 +720,87 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
             if (r >= w_end || r + 32 <= w_first) continue;
             const uint8_t *tq = step_q + set * kTile + part * 32 * S::pitch, *td = step_o + set * kTile + part * 32 * S::pitch;
             const float *st = step_st[set] + part * 32 + 4 * (lane >> 5);
-            rd.fresh();
-            __builtin_amdgcn_sched_barrier(0);
+            // Four runs of products, kRun each: s and p (dP) along the head, then the sums of dV and dK over the rows.  Their
+            // operands are read kAhead products ahead, and each product takes its share of the other instructions with
+            // it: the exponentials go beside p, the slopes beside dV.
             f32x16 s, p;
-            auto start = [&](f32x16 &v, const float *from) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 x = *reinterpret_cast<const f32x4 *>(from + 8 * i);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) v[4 * i + u] = x[u];
-                }
+            bf16x8 f[kAhead];
+            auto read = [&](int n) __attribute__((always_inline)) {
+                if (n < kRun) return read_row(tq + rd.row(n));
+                if (n < 2 * kRun) return read_row(td + rd.row(n - kRun));
+                const int x = (n % kRun) / DB, d = n % DB;
+                return rd.tr((n < 3 * kRun ? td : tq) + x * 16 * S::pitch, d);
             };
-            start(s, st);
+            auto start = [&](f32x16 &v, const float *from, int i) __attribute__((always_inline)) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(from + 8 * i);
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(tq + rd.row(k)), kf[k], s);
+                for (int u = 0; u < 4; ++u) v[4 * i + u] = x[u];
+            };
             rd.fresh();
-            start(p, st + kStepRows);
-#pragma unroll
-            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(td + rd.row(k)), vf[k], p);
-            // kAhead operands ahead of the products; the second sums' start comes in with the first four
-            __builtin_amdgcn_sched_group_barrier(0x100, 4 + kAhead, 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < 2 * S::ks - 4 - kAhead; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
-                p[i] *= s[i];
+            for (int i = 0; i < 4; ++i) start(s, st, i);
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) f[n] = read(n);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int n = 0; n < kRun; ++n) {
+                const bf16x8 now = f[n % kAhead];
+                f[n % kAhead] = read(n + kAhead);
+                s = mfma(now, kf[n], s);
+                if (n >= kRun - 4) start(p, st + kStepRows, n - (kRun - 4));
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (r < all_from || r + 32 > all_until || r + 32 > rows) {
-                const int k = opaque(key), mine_from = from(k), mine_until = until(k);
+            if (r < all_from || r + 32 > all_until) {
+                const int l = lane_now(), k = jw + (l & 31), mine_from = from(k), mine_until = until(k);
+                const float none = __uint_as_float((uint32_t)opaque((int)0xFF800000u));
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int at = r + (i >> 2) * 8 + 4 * (lane >> 5) + (i & 3);
-                    const bool sees = at >= mine_from && at < mine_until;
-                    s[i] = sees ? s[i] : 0.f;
-                    p[i] = sees ? p[i] : 0.f;
+                    const int at = r + (i >> 2) * 8 + 4 * (l >> 5) + (i & 3);
+                    s[i] = at >= mine_from && at < mine_until ? s[i] : none;
                 }
             }
-            const bf16x8 pf[2] = {pack8(s, 0), pack8(s, 1)}, sf[2] = {pack8(p, 0), pack8(p, 1)};
+            rd.fresh();
             __builtin_amdgcn_sched_barrier(0);
+            bf16x8 pf[2], sf[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                rd.fresh();
+            for (int n = 0; n < kRun; ++n) {
+                const bf16x8 now = f[(n + kRun) % kAhead];
+                f[(n + kRun) % kAhead] = read(n + kRun + kAhead);
+                p = mfma(now, vf[n], p);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    dv[d] = mfma(rd.tr(td + x * 16 * S::pitch, d), pf[x], dv[d]);
-                    dk[d] = mfma(rd.tr(tq + x * 16 * S::pitch, d), sf[x], dk[d]);
+                for (int i = n * 16 / kRun; i < (n + 1) * 16 / kRun; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * s2);
+                if (n == kRun - 1) pf[0] = pack8(s, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            rd.fresh();
+#pragma unroll
+            for (int n = 0; n < kRun; ++n) {
+                const bf16x8 now = f[(n + 2 * kRun) % kAhead];
+                f[(n + 2 * kRun) % kAhead] = read(n + 2 * kRun + kAhead);
+                dv[n % DB] = mfma(now, pf[n / DB], dv[n % DB]);
+                if (n == DB - 1) pf[1] = pack8(s, 1);
+                // the last of p's products has to be through before its values are used
+                if (n >= 2 && n < 6 && kRun >= 8) {
+#pragma unroll
+                    for (int i = (n - 2) * 4; i < (n - 1) * 4; ++i) p[i] *= s[i];
                 }
-            }
-            __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+                if (kRun < 8 && n >= 1) {
 #pragma unroll
-            for (int k = 0; k < 4 * DB - kAhead; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    for (int i = (n - 1) * 16 / (kRun - 1); i < n * 16 / (kRun - 1); ++i) p[i] *= s[i];
+                }
+                if (n == kRun - 2) sf[0] = pack8(p, 0);
+                if (n == kRun - 1) sf[1] = pack8(p, 1);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-            __builtin_amdgcn_sched_barrier(0);
+            rd.fresh();
+#pragma unroll
+            for (int n = 0; n < kRun; ++n) {
+                const bf16x8 now = f[(n + 3 * kRun) % kAhead];
+                if (n + kAhead < kRun) f[(n + 3 * kRun) % kAhead] = read(n + 3 * kRun + kAhead);
+                dk[n % DB] = mfma(now, sf[n / DB], dk[n % DB]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     for (int r = lo; r < hi; r += 4 * kStepRows) {
@@ -770,7 +812,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     FP8DS_WAIT_ALL();
     __syncthreads();
     static_assert(sizeof(q0) >= 2 * DB * 16 * 64 * 4, "an array holds a wave's sums");
-    float *mine = reinterpret_cast<float *>(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? o0 : o1) + lane;
+    float *mine = reinterpret_cast<float *>(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? o0 : o1) + lane_now();
     if (set == 1) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -782,7 +824,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     }
     __syncthreads();
     if (set == 1) return;
-    const int out = opaque(key);
+    const int l = lane_now(), out = jw + (l & 31);
     const bool there = out < sk.len;
     const int64_t token = sk.begin + out;
 #pragma unroll
@@ -801,7 +843,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
             consecutive8(dv[d], s, y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] *= a.softmax_scale;
-            const int at = d * 32 + s * 16 + (lane >> 5) * 8;
+            const int at = d * 32 + s * 16 + (l >> 5) * 8;
             if (there && at < a.D) {
                 *reinterpret_cast<u32x4 *>(a.dk.p + token * a.dk.ts + kvh * a.dk.hs + at) = to_bf16(x);
                 *reinterpret_cast<u32x4 *>(a.dv.p + token * a.dv.ts + kvh * a.dv.hs + at) = to_bf16(y);
@@ -994,7 +1036,13 @@ hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st) {
     a.part = static_cast<float *>(ws);
     if (a.Tq > 0) FP8DS_BY_HEAD(k_attn_dq, most_tiles(a.Tq, a.B, a.G, kRows, ragged) * a.Hkv, kThreads);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.Tk > 0) FP8DS_BY_HEAD(k_attn_dkv, most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv, 2 * kThreads);
+    if (a.Tk > 0) {
+        const dim3 grid((unsigned)(most_tiles(a.Tk, a.B, 1, kRows, ragged) * a.Hkv));
+        const bool even = (a.D <= 64 ? GroupLoads<2, true>::turn : GroupLoads<4, true>::turn) % a.G == 0;
+        if (a.D <= 64) even ? k_attn_dkv<2, true><<<grid, 2 * kThreads, 0, st>>>(a) : k_attn_dkv<2, false><<<grid, 2 * kThreads, 0, st>>>(a);
+        else if (a.D <= 96) even ? k_attn_dkv<3, true><<<grid, 2 * kThreads, 0, st>>>(a) : k_attn_dkv<3, false><<<grid, 2 * kThreads, 0, st>>>(a);
+        else even ? k_attn_dkv<4, true><<<grid, 2 * kThreads, 0, st>>>(a) : k_attn_dkv<4, false><<<grid, 2 * kThreads, 0, st>>>(a);
+    }
     return hipGetLastError();
 }
 
