@@ -68,7 +68,11 @@ extern "C" {
 size_t fp8_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
     if (B < 1 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || D > fp8ds::kAttnMaxHead) return 0;
     if (Tq > fp8ds::kAttnMaxRows / Hq || Tk > fp8ds::kAttnMaxRows / Hkv) return 0;
-    return fp8ds::attention_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+    if (Tq == 0) return 0;
+    // enough for offsets and for equal sequences, with an amax and without
+    const size_t n = fp8ds::attention_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, true, true);
+    const size_t m = Tq % B == 0 && Tk % B == 0 ? fp8ds::attention_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, false, true) : 0;
+    return n > m ? n : m;
 }
 
 int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads out, float *lse, uint8_t *out8,
@@ -88,7 +92,7 @@ int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads o
         if (int st = check_heads(out, Tq, Hq, D, true, 1); st != FP8DS_OK) return st;
     if (!is_aligned(out8, 16) || !all_aligned(4, lse, scale_inv_out, amax_slot) || !is_aligned(scale, 4) || !is_aligned(workspace, 16))
         return FP8DS_ERR_ALIGN;
-    const size_t need = fp8ds::attention_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+    const size_t need = fp8ds::attention_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, offsets_q != nullptr, out8 != nullptr && amax_slot != nullptr);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8DS_ERR_WORKSPACE;
     fp8ds::Attention a{};
     a.q = heads_of(q, Tq, D); a.k = heads_of(k, Tk, D); a.v = heads_of(v, Tk, D); a.out = heads_of(out, Tq, D);

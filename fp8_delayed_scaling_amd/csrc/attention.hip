@@ -20,6 +20,7 @@ constexpr int kKeys = 64;                    // keys of a step
 constexpr int kStepRows = 64;                // query rows of a step
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor's bound
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
+constexpr int kTops = 16, kTopParts = 32;     // rows that are computed again for the amax, shares of their keys
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
 
@@ -248,11 +249,25 @@ struct Emit {
         else w = u32x2{encode4<kE5M2>(y[0], y[1], y[2], y[3]), encode4<kE5M2>(y[4], y[5], y[6], y[7])};
         *reinterpret_cast<u32x2 *>(a.out8 + (token * a.Hq + head) * a.D + d) = w;
     }
-    // every lane of the wave takes part
-    __device__ __forceinline__ void finish(const Attention &a) {
+    // Every lane of the wave takes part.  Outputs made of rounded probabilities leave the wave's largest with its row,
+    // for k_attn_amax; exact ones go straight into the slot.
+    __device__ __forceinline__ void finish(const Attention &a, int64_t row) {
         if (a.out8 == nullptr || a.amax == nullptr) return;
-        const uint32_t m = wave_max_u32(amax);
-        if ((threadIdx.x & 63) == 0) fold_amax_bits(a.amax, m);
+        if (a.top == nullptr) {
+            const uint32_t m = wave_max_u32(amax);
+            if ((threadIdx.x & 63) == 0) fold_amax_bits(a.amax, m);
+            return;
+        }
+        uint64_t best = (uint64_t)amax << 32 | (uint32_t)~(uint32_t)row;             // ties: the lowest row
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const uint64_t other = __shfl_xor((unsigned long long)best, o, 64);
+            best = best > other ? best : other;
+        }
+        if ((threadIdx.x & 63) == 0) {
+            a.top[blockIdx.x * kWaves + (threadIdx.x >> 6)] = (uint32_t)(best >> 32);
+            a.top_row[blockIdx.x * kWaves + (threadIdx.x >> 6)] = (int32_t)~(uint32_t)best;
+        }
     }
 };
 __device__ __forceinline__ void write_inverse(const Attention &a) {
@@ -269,8 +284,9 @@ __device__ __forceinline__ Seen seen(const Attention &a, int pos, int lq, int lk
     return Seen{a.window > 0 ? max(0, at - a.window + 1) : 0, min(lk, at + 1)};
 }
 
-// One step of the running softmax: NKB blocks of 32 keys.
-template <int DB, int NKB> struct Softmax {
+// One step of the running softmax: NKB blocks of 32 keys.  The probabilities enter the second product as bfloat16, with an
+// error of up to 2^-8; EXACT: as three bfloat16, which hold all 24 bits, where bytes and not products are the bound.
+template <int DB, int NKB, bool EXACT> struct Softmax {
     f32x16 o[DB];
     float m = -kInf, l = 0.f;                    // in units of log2; l: of this lane's keys only
     __device__ __forceinline__ Softmax() {
@@ -328,8 +344,25 @@ template <int DB, int NKB> struct Softmax {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const bf16x8 p = pack8(s[kb], x);
+                bf16x8 p2, p3;
+                if constexpr (EXACT) {
+                    f32x16 left;
 #pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] = mfma(read_tr<DB>(sv + (kb * 32 + x * 16) * S::pitch, rd, d), p, o[d]);
+                    for (int i = 0; i < 8; ++i) left[i] = s[kb][8 * x + i] - (float)p[i];
+                    p2 = pack8(left, 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) left[i] -= (float)p2[i];
+                    p3 = pack8(left, 0);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const bf16x8 v = read_tr<DB>(sv + (kb * 32 + x * 16) * S::pitch, rd, d);
+                    o[d] = mfma(v, p, o[d]);
+                    if constexpr (EXACT) {
+                        o[d] = mfma(v, p2, o[d]);
+                        o[d] = mfma(v, p3, o[d]);
+                    }
+                }
             }
     }
 };
@@ -364,7 +397,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     write_inverse(a);
     const int kvh = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, split = rest % a.splits;
     int b, tile;
-    if (!find_tile(a.offsets_q, a.Tq, a.B, a.G, kRows, rest / a.splits, b, tile)) return;
+    if (!find_tile(a.offsets_q, a.Tq, a.B, a.G, kRows, rest / a.splits, b, tile)) {
+        if (a.top != nullptr && a.splits == 1 && lane == 0) a.top[blockIdx.x * kWaves + wave] = 0;
+        return;
+    }
     const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
     const int rows = sq.len * a.G, r0 = tile * kRows, last = min(r0 + kRows, rows) - 1;
     const int r0w = r0 + wave * 32, r = r0w + (lane & 31);
@@ -389,7 +425,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
-    Softmax<DB, 2> sm;
+    Softmax<DB, 2, false> sm;
     if (lo < hi) {
         loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
         loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
@@ -444,7 +480,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
             const int at = d * 32 + s * 16 + (lane >> 5) * 8;
             if (there && at < a.D) emit(a, token, head, at, v);
         }
-    emit.finish(a);
+    emit.finish(a, token * a.Hq + head);
 }
 
 // A block: up to 32 query rows of one key/value head; its waves share the keys.
@@ -481,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
-    Softmax<DB, 1> sm;
+    Softmax<DB, 1, true> sm;
     const int mine = wave * kTile;
     int j = lo + wave * 32;
     if (j < hi) {
@@ -557,7 +593,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
         for (int u = 0; u < 8; ++u) v[u] *= inv;
         emit(a, token, hd, d, v);
     }
-    if (a.splits == 1) emit.finish(a);
+    if (a.splits == 1) emit.finish(a, 0);
 }
 
 // The splits' sums of each row, joined in order.  16 threads a row; rows of no sequence stay as they are.
@@ -598,7 +634,180 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
         for (int u = 0; u < 8; ++u) v[u] *= inv;
         if (d < a.D) emit(a, token, head, d, v);
     }
-    emit.finish(a);
+    emit.finish(a, row);
+}
+
+// The amax.  Outputs made of rounded probabilities tell which rows may hold it: those within 1/64 of the largest (a rounded
+// probability is off by 2^-8 at most), kTops of them at most, one to a wave of k_attn_fwd.  These rows are computed again
+// with probabilities of 32 bits, kTopParts blocks to a row; k_attn_amax_join joins their sums in order.  (One launch whose last
+// blocks join took 17 us at 4 x 2048, 8 of them for the fences; the two take 5 and 3.)
+__global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
+    constexpr int kChunk = kThreads;                                 // keys at a time
+    __shared__ uint32_t red[kWaves];
+    __shared__ float fred[kWaves], prob[kChunk], q[128], acc[16][128];
+    __shared__ int found[kThreads], rows[kTops], all;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    // the waves' outputs, four to a load (a.tops % 4 == 0), the first kHeld of a thread kept
+    constexpr int kHeld = 8;
+    const u32x4 *const tops = reinterpret_cast<const u32x4 *>(a.top);
+    const int n = a.tops / 4;
+    u32x4 held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = t + i * kThreads < n ? tops[t + i * kThreads] : u32x4{0, 0, 0, 0};
+    uint32_t top = 0;
+    auto largest = [&](const u32x4 &x) __attribute__((always_inline)) { top = max(max(max(x.x, x.y), max(x.z, x.w)), top); };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) largest(held[i]);
+#pragma unroll 8
+    for (int i = t + kHeld * kThreads; i < n; i += kThreads) largest(tops[i]);
+    top = block_max_u32<kThreads>(top, red);
+    if (t == 0) red[0] = top;
+    if (t == 0) all = 0;
+    __syncthreads();
+    top = red[0];
+    if (top == 0 || top >= 0x7F800000u) {                            // nothing, or an infinity or NaN, which no rounding made
+        if (blockIdx.x == 0 && t == 0) {
+            fold_amax_bits(a.amax, top);
+            *a.top_done = 0;
+        }
+        return;
+    }
+    // the candidates: as they are found, then the first in the order of the waves
+    const uint32_t least = __float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64));
+    auto find = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
+        if (max(max(x.x, x.y), max(x.z, x.w)) < least) return;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (x[u] >= least) {
+                const int at = atomicAdd(&all, 1);
+                if (at < kThreads) found[at] = 4 * i + u;
+            }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) find(held[i], t + i * kThreads);
+#pragma unroll 8
+    for (int i = t + kHeld * kThreads; i < n; i += kThreads) find(tops[i], i);
+    __syncthreads();
+    if (all <= kThreads) {
+        if (t < all) {
+            int before = 0;
+            for (int i = 0; i < all; ++i) before += found[i] < found[t];
+            if (before < kTops) rows[before] = a.top_row[found[t]];
+        }
+    } else if (t == 0) {
+        for (int i = 0, n = 0; n < kTops; ++i)
+            if (a.top[i] >= least) rows[n++] = a.top_row[i];
+    }
+    __syncthreads();
+    const int c = blockIdx.x / kTopParts, part = blockIdx.x % kTopParts;
+    if (blockIdx.x == 0 && t == 0) *a.top_done = min(all, kTops);    // rows for k_attn_amax_join
+    if (c >= min(all, kTops)) return;
+    const int row = rows[c], token = row / a.Hq, head = row - token * a.Hq, kvh = head / a.G;
+    int b;
+    if (a.offsets_q == nullptr) {
+        b = token / (a.Tq / a.B);
+    } else {
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.offsets_q[mid] <= token) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    }
+    const Span sq = span_of(a.offsets_q, b, a.Tq, a.B), sk = span_of(a.offsets_k, b, a.Tk, a.B);
+    const Seen see = seen(a, token - (int)sq.begin, sq.len, sk.len);
+    const int share = (max(see.hi - see.lo, 0) + kTopParts - 1) / kTopParts;
+    const int k_first = see.lo + part * share, k_end = min(see.hi, k_first + share);
+    if (t < 128) q[t] = t < a.D ? bf16_lo(a.q.p[(int64_t)token * a.q.ts + head * a.q.hs + t]) : 0.f;
+    __syncthreads();
+    const float s2 = a.softmax_scale * kLog2e;
+    const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
+    // o: elements 8 (t % 16) .. + 7 over every 16th key
+    const int d8 = (t & 15) * 8;
+    float m = -kInf, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = k_first; j < k_end; j += kChunk) {
+        float s = -kInf;
+        if (j + t < k_end) {
+            const uint16_t *row_k = kp + (int64_t)(j + t) * a.k.ts;
+            s = 0.f;
+            u32x4 x[16];
+#pragma unroll
+            for (int d = 0; d < 16; ++d) x[d] = d * 8 < a.D ? *reinterpret_cast<const u32x4 *>(row_k + d * 8) : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s = __builtin_fmaf(q[d * 8 + 2 * i + 1], bf16_hi(x[d][i]), __builtin_fmaf(q[d * 8 + 2 * i], bf16_lo(x[d][i]), s));
+            s *= s2;
+        }
+        float mx = s;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+        if (lane == 0) fred[wave] = mx;
+        __syncthreads();
+        const float mn = fmaxf(fmaxf(m, fmaxf(fred[0], fred[1])), fmaxf(fred[2], fred[3])), ref = mn == -kInf ? 0.f : mn;
+        const float al = __builtin_amdgcn_exp2f(m - ref), p = __builtin_amdgcn_exp2f(s - ref);
+        m = mn;
+        l = l * al + p;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) o[u] *= al;
+        prob[t] = p;
+        __syncthreads();
+        u32x4 x[kChunk / 16];
+#pragma unroll
+        for (int i = 0; i < kChunk / 16; ++i) {
+            const int key = j + (t >> 4) + 16 * i;
+            x[i] = key < k_end && d8 < a.D ? *reinterpret_cast<const u32x4 *>(vp + (int64_t)key * a.v.ts + d8) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk / 16; ++i) {
+            const float p = prob[(t >> 4) + 16 * i];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                o[2 * u] = __builtin_fmaf(p, bf16_lo(x[i][u]), o[2 * u]);
+                o[2 * u + 1] = __builtin_fmaf(p, bf16_hi(x[i][u]), o[2 * u + 1]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc[t >> 4][d8 + u] = o[u];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
+    if (lane == 0) fred[wave] = l;
+    __syncthreads();
+    float *mine_part = a.top_part + (int64_t)blockIdx.x * 130;
+    if (t < 128) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += acc[i][t];
+        mine_part[t] = sum;
+    }
+    if (t == 128) {
+        mine_part[128] = m;
+        mine_part[129] = fred[0] + fred[1] + fred[2] + fred[3];
+    }
+}
+
+__global__ __launch_bounds__(128) void k_attn_amax_join(const Attention a) {
+    __shared__ uint32_t red[2];
+    const int t = threadIdx.x;                                       // the element
+    if ((int)blockIdx.x >= *a.top_done) return;
+    const float *parts = a.top_part + (int64_t)blockIdx.x * kTopParts * 130;
+    float pm[kTopParts], pl[kTopParts], pv[kTopParts], m = -kInf, sum = 0.f, v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTopParts; ++i) pm[i] = parts[i * 130 + 128], pl[i] = parts[i * 130 + 129], pv[i] = parts[i * 130 + t];
+#pragma unroll
+    for (int i = 0; i < kTopParts; ++i) m = fmaxf(m, pm[i]);
+#pragma unroll
+    for (int i = 0; i < kTopParts; ++i) {
+        const float w = pm[i] == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm[i] - m);
+        sum += w * pl[i];
+        v += w * pv[i];
+    }
+    const uint32_t best = block_max_u32<128>(sum > 0.f ? __float_as_uint(v / sum) & 0x7FFFFFFFu : 0u, red);
+    if (t == 0) fold_amax_bits(a.amax, best);
 }
 
 // ---------------------------------------------------------------------------------- backward
@@ -1000,15 +1209,26 @@ bool attention_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, 
            most_tiles(Tk, B, 1, kRows, ragged) * Hkv <= kMostBlocks;
 }
 
-size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
-    if (B == 0 || Tq == 0) return 0;
-    int64_t s = 1;
-    for (bool ragged : {false, true}) {
-        if (!ragged && (Tq % B != 0 || Tk % B != 0)) continue;
-        const int64_t n = fwd_plan(Tq, Tk, B, Hkv, Hq / Hkv, ragged).splits;
-        if (n > s) s = n;
+// The forward's workspace: the splits' sums and stats, then what the amax takes.
+struct Room {
+    size_t sums, stats, top, top_row, top_part, top_done, bytes;
+    int64_t tops;
+    Room(const Plan &p, int64_t Tq, int64_t Hq, int64_t D, bool amax) {
+        const auto up = [](size_t n) { return (n + 15) & ~(size_t)15; };
+        const size_t rows = (size_t)(Tq * Hq), split = p.splits > 1 ? (size_t)p.splits : 0;
+        tops = p.few || !amax ? 0 : (p.splits > 1 ? (int64_t)(rows + 15) / 16 : p.blocks) * kWaves;
+        sums = 0;
+        stats = split * rows * D * 4;                                // D % 8 == 0
+        top = stats + up(split * rows * 8);
+        top_row = top + up((size_t)tops * 4);
+        top_part = top_row + up((size_t)tops * 4);
+        top_done = top_part + (tops > 0 ? kTops * kTopParts * 130 * 4 : 0);
+        bytes = top_done + (tops > 0 ? 16 : 0);
     }
-    return s > 1 ? (size_t)(s * Tq * Hq * (D + 2) * 4) : 0;
+};
+
+size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, bool ragged, bool amax) {
+    return Room(fwd_plan(Tq, Tk, B, Hkv, Hq / Hkv, ragged), Tq, Hq, D, amax).bytes;
 }
 size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq) { return (size_t)(Tq * Hq * 8); }
 
@@ -1022,12 +1242,29 @@ size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq) { return (size_t)(T
 
 hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st) {
     const Plan p = fwd_plan(a.Tq, a.Tk, a.B, a.Hkv, a.G, a.offsets_q != nullptr);
+    const Room room(p, a.Tq, a.Hq, a.D, a.out8 != nullptr && a.amax != nullptr);
+    uint8_t *const base = static_cast<uint8_t *>(ws);
     a.splits = (int)p.splits;
-    a.part = static_cast<float *>(ws);
+    a.part = reinterpret_cast<float *>(base);
+    if (room.tops > 0) {
+        a.tops = (int)room.tops;
+        a.top = reinterpret_cast<uint32_t *>(base + room.top);
+        a.top_row = reinterpret_cast<int32_t *>(base + room.top_row);
+        a.top_part = reinterpret_cast<float *>(base + room.top_part);
+        a.top_done = reinterpret_cast<int32_t *>(base + room.top_done);
+    }
     if (p.few) FP8DS_BY_HEAD(k_attn_fwd_few, p.blocks, kThreads);
     else FP8DS_BY_HEAD(k_attn_fwd, p.blocks, kThreads);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess || a.splits == 1) return e;
-    k_attn_join<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (a.splits > 1) {
+        k_attn_join<<<(unsigned)(((int64_t)a.Tq * a.Hq + 15) / 16), kThreads, 0, st>>>(a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    if (a.top != nullptr) {
+        k_attn_amax<<<kTops * kTopParts, kThreads, 0, st>>>(a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        k_attn_amax_join<<<kTops, 128, 0, st>>>(a);
+    }
     return hipGetLastError();
 }
 

@@ -132,15 +132,20 @@ struct Attention {
     float softmax_scale;
     int fmt, causal, window;                 // window 0: none
     int B, Tq, Tk, Hq, Hkv, G, D;
-    // set by the launcher
-    int splits;
-    float *part;
+    // set by the launcher: splits of the keys, their sums or the backward's row values; the waves' largest
+    // outputs with their rows, and what is needed to compute the largest of all again (nullptr: not wanted)
+    int splits, tops;
+    float *part, *top_part;
+    uint32_t *top;
+    int32_t *top_row;
+    int32_t *top_done;
 };
 constexpr int64_t kAttnMaxHead = 128;
 constexpr int64_t kAttnMaxStride = INT64_C(1) << 23;     // between tokens: 64 rows' offsets stay below 2^31
 constexpr int64_t kAttnMaxRows = INT64_C(1) << 28;       // tokens x heads
 bool attention_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, bool ragged);
-size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+// of a batch with offsets (ragged) or of equal sequences, with the amax of its output or without
+size_t attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, bool ragged, bool amax);
 size_t attention_bwd_workspace_bytes(int64_t Tq, int64_t Hq);
 hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st);
 hipError_t launch_attention_bwd(Attention a, void *ws, hipStream_t st);

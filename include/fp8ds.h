@@ -475,8 +475,9 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * aligned; T * heads <= 2^28; the heads that share a key/value head lie within 2^30 elements.
  * softmax_scale > 0; window only with causal.  Scores, softmax and sums are float32; the probabilities are
  * rounded to bfloat16 as operands of the matrix cores.  A NaN or an infinity in q, k or v may reach every row
- * of its sequence, those that do not see it too.  workspace: fp8_attention_workspace_bytes (may be 0: NULL),
- * 16-byte aligned, no initialisation; calls that overlap in time must not share it.
+ * of its sequence, those that do not see it too.  workspace: fp8_attention_workspace_bytes is enough for any call of
+ * these sizes (one that splits nothing and wants no amax takes none: NULL), 16-byte aligned, no initialisation; calls
+ * that overlap in time must not share it.
  */
 typedef struct {
     uint16_t *data;

@@ -69,6 +69,8 @@ def check_forward(q, k, v, fp8=False, **kw):
         close(codes.view(torch.float8_e4m3fn).float()[rows], y[rows],
               (e_out * s * (1 + E4M3_HALF_STEP) + E4M3_HALF_STEP * y.abs() + E4M3_LOWEST)[rows])
         amax = w_out[rows].abs().max() if bool(rows.any()) else torch.zeros((), device=DEV).double()
+        # outputs within 1/64 of the largest are computed again with unrounded probabilities, one a wave: what their
+        # rounding is off by is left only where two rows of one wave are nearer than it
         assert abs(f["amax_slot"].item() - amax.item()) <= float(e_out.max())
         assert f["scale_inv_out"].item() == (torch.ones(1) / torch.tensor([s])).item()
     return out, lse
@@ -247,14 +249,46 @@ def test_only_codes_and_no_lse():
     q, k, v, _ = inputs(13, 100, 100, 4, 2, 128)
     want = torch.empty(100, 4 * 128, dtype=torch.uint8, device=DEV)
     s, amax = torch.full((1,), 60.0, device=DEV), torch.zeros(1, device=DEV)
-    F.fp8_attention_fwd(q, k, v, torch.empty_like(q), None, out8=want, scale=s, amax_slot=amax)
+    ws = workspace(F.fp8_attention_workspace_bytes, q, k, 1)
+    F.fp8_attention_fwd(q, k, v, torch.empty_like(q), None, out8=want, scale=s, amax_slot=amax, workspace=ws)
     got, amax2 = torch.empty_like(want), torch.full((1,), 99.0, device=DEV)
-    F.fp8_attention_fwd(q, k, v, None, None, out8=got, scale=s, amax_slot=amax2)
+    F.fp8_attention_fwd(q, k, v, None, None, out8=got, scale=s, amax_slot=amax2, workspace=ws)
     assert torch.equal(got, want) and amax2.item() == 99.0        # an amax that is larger stays
     e5 = torch.empty_like(want)
     F.fp8_attention_fwd(q, k, v, None, None, out8=e5, scale=s, fmt=F.E5M2)
     w, _, e, _, _ = ref.forward(q, k, v)
     close(e5.view(torch.float8_e5m2).float().view(q.shape), w * 60, e * 60 * 1.125 + 2.0 ** -3 * (w * 60).abs() + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("B,lq,lk,Hq,Hkv,D,causal,ragged", [
+    (1, 500, 500, 8, 2, 128, True, False), (4, 300, 300, 4, 4, 64, False, False), (3, 1, 3000, 8, 1, 128, True, False), (1, 200, 5000, 4, 2, 96, True, True),
+    (1, 64, 40, 4, 2, 128, True, False), (5, 129, 400, 6, 3, 72, False, True), (2, 700, 700, 16, 2, 128, True, True)])
+def test_amax_is_that_of_unrounded_probabilities(B, lq, lk, Hq, Hkv, D, causal, ragged):
+    """To the float32 roundings of the largest output: its scores, exponentials and sums."""
+    for seed in range(4):
+        q, k, v, _ = inputs(30 + seed, B * lq, B * lk, Hq, Hkv, D)
+        kw = dict(causal=causal, batch=B)
+        if ragged:
+            kw.update(offsets_q=offsets([lq] * B), offsets_k=offsets([lk] * B))
+        f = run_forward(q, k, v, fp8=True, **kw)[2]
+        out = ref.forward(q, k, v, **kw)[0]
+        at = out.abs().flatten().argmax().item()
+        token, head = at // (Hq * D), at // D % Hq
+        # what the float32 parts of this output's error allow (its terms' magnitudes times each one's relative error)
+        hidden = next(x for x in ref.heads(q, k, v, **kw) if x[0][0] <= token < x[0][1] and x[2] == head)
+        p, V, eps = hidden[8][token - hidden[0][0]], hidden[7], hidden[10][token - hidden[0][0]]
+        bound = (p @ V.abs())[at % D] * (3 * eps + 2 ** -22)
+        assert abs(f["amax_slot"].item() - out.abs().max().item()) <= bound
+
+
+def test_amax_of_equal_rows():
+    """Every row a candidate, more than are computed again."""
+    q, k, v = torch.zeros(600, 4, 64, device=DEV).bfloat16(), torch.zeros(600, 4, 64, device=DEV).bfloat16(), torch.ones(600, 4, 64, device=DEV).bfloat16()
+    assert run_forward(q, k, v, fp8=True)[2]["amax_slot"].item() == 1.0
+    v[:] = 0
+    assert run_forward(q, k, v, fp8=True)[2]["amax_slot"].item() == 0.0
+    v[7, 2, 5] = math.inf
+    assert not math.isfinite(run_forward(q, k, v, fp8=True)[2]["amax_slot"].item())
 
 
 def test_repeats_bit_for_bit():
@@ -297,10 +331,11 @@ def test_captured_and_replayed():
     out8, s, amax = torch.empty(256, 1024, dtype=torch.uint8, device=DEV), torch.full((1,), 60.0, device=DEV), torch.zeros(1, device=DEV)
     dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
     one = torch.empty_like(long_q)
+    ws_fwd = workspace(F.fp8_attention_workspace_bytes, q, k, 2)
     ws, ws_long = workspace(F.fp8_attention_bwd_workspace_bytes, q, k, 2), workspace(F.fp8_attention_workspace_bytes, long_q, long_k, 2)
 
     def step():
-        F.fp8_attention_fwd(q, k, v, out, lse, batch=2, out8=out8, scale=s, amax_slot=amax)
+        F.fp8_attention_fwd(q, k, v, out, lse, batch=2, out8=out8, scale=s, amax_slot=amax, workspace=ws_fwd)
         F.fp8_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, ws, batch=2)
         F.fp8_attention_fwd(long_q, long_k, long_v, one, None, lens_q, lens_k, workspace=ws_long)
 
