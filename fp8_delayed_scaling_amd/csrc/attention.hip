@@ -390,7 +390,7 @@ __device__ __forceinline__ float *part_stats(const Attention &a, int split) {
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = kKeys * S::pitch;
+    constexpr int kTile = kKeys * S::pitch, kRun = 2 * DB, kAhead = 3;
     // two turns of K and V: arrays of their own, so that reading one does not wait for the loads into the other
     __shared__ __align__(1024) uint8_t k0[kTile], k1[kTile], v0[kTile], v1[kTile];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -423,9 +423,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
 
     const RowLoads<DB, kKeys, kWaves> loads_k(lane, wave, a.D, a.k.ts), loads_v(lane, wave, a.D, a.v.ts);
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
-    const Reader<DB> rd(lane);
-    const float s2 = a.softmax_scale * kLog2e;
-    Softmax<DB, 2, false> sm;
+    Walker<DB> rd(lane);
+    const float s2 = uniform_value(a.softmax_scale * kLog2e);
+    f32x16 o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float m = -kInf, ref = 0.f, l = 0.f;         // the sums' reference in units of log2 (ref: 0 for none), this lane's keys' sum
     if (lo < hi) {
         loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
         loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
@@ -438,7 +443,102 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
             loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k);
             loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v);
         }
-        sm.step(tk, tv, rd, qf, s2, next > first.hi || j < end.lo, j, see, lane);
+        const bool masked = next > first.hi || j < end.lo;
+        // Four runs of products, kRun each: the scores of 32 keys, of the next 32, and the sums over either.  The first
+        // 32 keys' exponentials go beside the second run, the others' beside the third; operands are read kAhead ahead.
+        // The exponentials are taken about the reference as it is, and again where a score proves to be past 2^8 of it.
+        f32x16 s[2];
+        bf16x8 f[kAhead], p[2][2];
+        float part[2], mx;
+        auto read = [&](int n) __attribute__((always_inline)) {
+            if (n < 2 * kRun) return read_row(tk + (n / kRun) * 32 * S::pitch + rd.row(n % kRun));
+            const int kb = n / kRun - 2, x = (n % kRun) / DB, d = n % DB;
+            return rd.tr(tv + (kb * 32 + x * 16) * S::pitch, d);
+        };
+        auto mask = [&](int kb) __attribute__((always_inline)) {
+            if (!masked) return;
+            const int key0 = j + kb * 32 + 4 * (lane >> 5);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int key = key0 + (i >> 2) * 8 + (i & 3);
+                s[kb][i] = key >= see.lo && key < see.hi ? s[kb][i] : -kInf;
+            }
+        };
+        // share n of kRun of the exponentials of a run's scores; the last packs them
+        auto values = [&](int kb, int n) __attribute__((always_inline)) {
+            if (n == 0) mx = s[kb][0], part[kb] = 0.f;
+#pragma unroll
+            for (int i = n * 16 / kRun; i < (n + 1) * 16 / kRun; ++i) {
+                mx = fmaxf(mx, s[kb][i]);
+                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], s2, -ref));
+                asm volatile("" : "+v"(e));          // here, not behind the branch that they might not reach
+                part[kb] += e;
+                p[kb][i / 8][i % 8] = (__bf16)e;
+            }
+        };
+        auto settle = [&](int kb) __attribute__((always_inline)) {
+            mx = both_halves_max(mx) * s2;
+            if (__any(mx > m + 8.f)) {
+                const float mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                ref = mn == -kInf ? 0.f : mn;
+                l *= al;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= al;
+#pragma unroll
+                for (int n = 0; n < kRun; ++n) values(kb, n);
+            }
+            l += part[kb];
+        };
+        rd.fresh();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.f;
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) f[n] = read(n);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kRun; ++n) {
+            const bf16x8 now = f[n % kAhead];
+            f[n % kAhead] = read(n + kAhead);
+            s[0] = mfma(now, qf[n], s[0]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        mask(0);
+        rd.fresh();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kRun; ++n) {
+            const bf16x8 now = f[(n + kRun) % kAhead];
+            f[(n + kRun) % kAhead] = read(n + kRun + kAhead);
+            s[1] = mfma(now, qf[n], s[1]);
+            values(0, n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        settle(0);
+        mask(1);
+        rd.fresh();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kRun; ++n) {
+            const bf16x8 now = f[(n + 2 * kRun) % kAhead];
+            f[(n + 2 * kRun) % kAhead] = read(n + 2 * kRun + kAhead);
+            o[n % DB] = mfma(now, p[0][n / DB], o[n % DB]);
+            values(1, n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        settle(1);
+        rd.fresh();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kRun; ++n) {
+            const bf16x8 now = f[(n + 3 * kRun) % kAhead];
+            if (n + kAhead < kRun) f[(n + 3 * kRun) % kAhead] = read(n + 3 * kRun + kAhead);
+            o[n % DB] = mfma(now, p[1][n / DB], o[n % DB]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     // a branch around a step, or out of the loop between two, would have the sums copied at each
     int j = lo;
@@ -447,13 +547,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
         turn(j + kKeys, k1, v1, k0, v0);
     }
     if (j < hi) turn(j, k0, v0, k1, v1);
-    const float l = both_halves_sum(sm.l);
+    l = both_halves_sum(l);
     if (a.splits > 1) {
         if (!there) return;
         const int64_t row = token * a.Hq + head;
         if (lane < 32) {
             float *st = part_stats(a, split) + row * 2;
-            st[0] = sm.m;
+            st[0] = m;
             st[1] = l;
         }
         float *to = part_sums(a, split) + row * a.D;
@@ -462,19 +562,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = d * 32 + i * 8 + (lane >> 5) * 4;
-                if (at < a.D) *reinterpret_cast<f32x4 *>(to + at) = f32x4{sm.o[d][4 * i], sm.o[d][4 * i + 1], sm.o[d][4 * i + 2], sm.o[d][4 * i + 3]};
+                if (at < a.D) *reinterpret_cast<f32x4 *>(to + at) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
             }
         return;
     }
     Emit emit(a);
     const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;       // a NaN stays one
-    if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (sm.m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float v[8];
-            consecutive8(sm.o[d], s, v);
+            consecutive8(o[d], s, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= inv;
             const int at = d * 32 + s * 16 + (lane >> 5) * 8;
