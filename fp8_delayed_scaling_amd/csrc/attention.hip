@@ -234,13 +234,16 @@ __device__ __forceinline__ u32x4 to_bf16(const float (&v)[8]) {
 // Eight values of one output row: bfloat16, codes, the largest magnitude.
 struct Emit {
     float scale;
-    uint32_t amax = 0;
+    uint64_t best = 0;                           // the largest magnitude's bits, then the row's complement: ties to the lowest
     __device__ __forceinline__ explicit Emit(const Attention &a) : scale(a.out8 != nullptr ? *a.scale : 1.f) {}
     __device__ __forceinline__ void operator()(const Attention &a, int64_t token, int head, int d, const float (&v)[8]) {
         if (a.out.p != nullptr) *reinterpret_cast<u32x4 *>(a.out.p + token * a.out.ts + head * a.out.hs + d) = to_bf16(v);
         if (a.out8 == nullptr) return;
+        uint32_t amax = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        const uint64_t mine = (uint64_t)amax << 32 | (uint32_t)~(uint32_t)(token * a.Hq + head);
+        best = best > mine ? best : mine;
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = v[i] * scale;
@@ -251,20 +254,17 @@ struct Emit {
     }
     // Every lane of the wave takes part.  Outputs made of rounded probabilities leave the wave's largest with its row,
     // for k_attn_amax; exact ones go straight into the slot.
-    __device__ __forceinline__ void finish(const Attention &a, int64_t row) {
+    __device__ __forceinline__ void finish(const Attention &a) {
         if (a.out8 == nullptr || a.amax == nullptr) return;
-        if (a.top == nullptr) {
-            const uint32_t m = wave_max_u32(amax);
-            if ((threadIdx.x & 63) == 0) fold_amax_bits(a.amax, m);
-            return;
-        }
-        uint64_t best = (uint64_t)amax << 32 | (uint32_t)~(uint32_t)row;             // ties: the lowest row
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) {
             const uint64_t other = __shfl_xor((unsigned long long)best, o, 64);
             best = best > other ? best : other;
         }
-        if ((threadIdx.x & 63) == 0) {
+        if ((threadIdx.x & 63) != 0) return;
+        if (a.top == nullptr) {
+            fold_amax_bits(a.amax, (uint32_t)(best >> 32));
+        } else {
             a.top[blockIdx.x * kWaves + (threadIdx.x >> 6)] = (uint32_t)(best >> 32);
             a.top_row[blockIdx.x * kWaves + (threadIdx.x >> 6)] = (int32_t)~(uint32_t)best;
         }
@@ -367,15 +367,20 @@ template <int DB, int NKB, bool EXACT> struct Softmax {
     }
 };
 
-// The lane's query row as an operand: elements 16 k + 8 (l / 32) .. + 7.
+// The lane's row as an operand: elements 16 k + 8 (l / 32) .. + 7, zeros past the head or where there is no row.  Without
+// a branch: what is not there is read from `any`, a row that is.
 template <int DB>
-__device__ __forceinline__ void load_query(bf16x8 (&f)[2 * DB], const uint16_t *row, bool there, int D, int half) {
+__device__ __forceinline__ void load_query(bf16x8 (&f)[2 * DB], const uint16_t *row, const uint16_t *any, bool there, int D, int half) {
+    const uint16_t *from = there ? row : any;
+    u32x4 v[2 * DB];
+#pragma unroll
+    for (int k = 0; k < 2 * DB; ++k) v[k] = *reinterpret_cast<const u32x4 *>(from + (k * 16 + half * 8 < D ? k * 16 + half * 8 : 0));
 #pragma unroll
     for (int k = 0; k < 2 * DB; ++k) {
-        const int d = k * 16 + half * 8;
-        u32x4 v = {0, 0, 0, 0};
-        if (there && d < D) v = *reinterpret_cast<const u32x4 *>(row + d);
-        f[k] = __builtin_bit_cast(bf16x8, v);
+        const bool in = there && k * 16 + half * 8 < D;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[k][u] = in ? v[k][u] : 0u;
+        f[k] = __builtin_bit_cast(bf16x8, v[k]);
     }
 }
 
@@ -408,7 +413,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     const bool there = r < rows;
     const int64_t token = sq.begin + pos;
     bf16x8 qf[S::ks];
-    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
+    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
 
     // keys of the block, of the wave, of the lane
     int lo = seen(a, r0 / a.G, sq.len, sk.len).lo & ~(kKeys - 1), hi = seen(a, last / a.G, sq.len, sk.len).hi;
@@ -566,21 +571,40 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
             }
         return;
     }
-    Emit emit(a);
     const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;       // a NaN stays one
     if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    // The rows go out through LDS, kLanes lanes to a row and 8 elements to a lane, so that the casts are one short loop: as
+    // straight code from the registers they took more of the instruction cache than all else.
+    constexpr int kLanes = DB == 2 ? 8 : 16, kPieces = 2 * kLanes;   // 16-byte pieces of a row; lane l's row keeps them at p ^ l
+    FP8DS_WAIT_ALL();
+    FP8DS_BARRIER();
+    uint8_t *const stage = wave == 0 ? k0 : wave == 1 ? k1 : wave == 2 ? v0 : v1;
+    static_assert(kTile >= 32 * kPieces * 16, "an array holds a wave's rows");
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            float v[8];
-            consecutive8(o[d], s, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= inv;
-            const int at = d * 32 + s * 16 + (lane >> 5) * 8;
-            if (there && at < a.D) emit(a, token, head, at, v);
+        for (int i = 0; i < 4; ++i) {
+            const int x = lane & 31, piece = (8 * d + 2 * i + (lane >> 5)) ^ (x & (kPieces - 1));
+            *reinterpret_cast<f32x4 *>(stage + (x * kPieces + piece) * 16) = f32x4{o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
         }
-    emit.finish(a, token * a.Hq + head);
+    FP8DS_WAIT_LGKM();
+    asm volatile("" ::: "memory");
+    Emit emit(a);
+    const int at = lane % kLanes * 8;
+#pragma unroll 1
+    for (int x = lane / kLanes; x < 32; x += 64 / kLanes) {
+        const int rr = r0w + x, p = rr / a.G;
+        if (rr >= rows || at >= a.D) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(stage + (x * kPieces + ((at / 4 + i) ^ (x & (kPieces - 1)))) * 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[4 * i + u] = y[u];
+        }
+        emit(a, sq.begin + p, kvh * a.G + rr - p * a.G, at, v);
+    }
+    emit.finish(a);
 }
 
 // A block: up to 32 query rows of one key/value head; its waves share the keys.
@@ -603,7 +627,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     const int r = r0 + (lane & 31), pos = r / a.G, head = kvh * a.G + r - pos * a.G;
     const bool there = r < rows;
     bf16x8 qf[S::ks];
-    load_query<DB>(qf, a.q.p + (sq.begin + pos) * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
+    load_query<DB>(qf, a.q.p + (sq.begin + pos) * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
     const Seen first = seen(a, r0 / a.G, sq.len, sk.len), end = seen(a, last / a.G, sq.len, sk.len);
     const Seen see = seen(a, pos, sq.len, sk.len);         // rows past the last compute what is never written
     constexpr int kStep = kWaves * 32;
@@ -693,7 +717,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
         for (int u = 0; u < 8; ++u) v[u] *= inv;
         emit(a, token, hd, d, v);
     }
-    if (a.splits == 1) emit.finish(a, 0);
+    if (a.splits == 1) emit.finish(a);
 }
 
 // The splits' sums of each row, joined in order.  16 threads a row; rows of no sequence stay as they are.
@@ -734,7 +758,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
         for (int u = 0; u < 8; ++u) v[u] *= inv;
         if (d < a.D) emit(a, token, head, d, v);
     }
-    emit.finish(a, row);
+    emit.finish(a);
 }
 
 // The amax.  Outputs made of rounded probabilities tell which rows may hold it: those within 1/64 of the largest (a rounded
@@ -985,8 +1009,8 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
     const int G = a.G, rows = sq.len * G, j0 = tile * kRows, past = sk.len - sq.len;
     const int jw = j0 + wave * 32, key = jw + (lane & 31);
     bf16x8 kf[S::ks], vf[S::ks];
-    load_query<DB>(kf, a.k.p + (sk.begin + key) * a.k.ts + kvh * a.k.hs, key < sk.len, a.D, lane >> 5);
-    load_query<DB>(vf, a.v.p + (sk.begin + key) * a.v.ts + kvh * a.v.hs, key < sk.len, a.D, lane >> 5);
+    load_query<DB>(kf, a.k.p + (sk.begin + key) * a.k.ts + kvh * a.k.hs, a.k.p, key < sk.len, a.D, lane >> 5);
+    load_query<DB>(vf, a.v.p + (sk.begin + key) * a.v.ts + kvh * a.v.hs, a.v.p, key < sk.len, a.D, lane >> 5);
 
     // query rows that see key j: [(j - past) G, (j - past + window) G)
     auto from = [&](int j) { return a.causal ? (int)min(max((int64_t)(j - past) * G, (int64_t)0), (int64_t)rows) : 0; };
@@ -1178,14 +1202,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     const bool there = r < rows;
     const int64_t token = sq.begin + pos;
     bf16x8 qf[S::ks], df[S::ks];
-    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, there, a.D, lane >> 5);
-    load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, there, a.D, lane >> 5);
+    load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
+    load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, a.dout.p, there, a.D, lane >> 5);
     const float s2 = a.softmax_scale * kLog2e;
     // -lse / scale and -<dout, out> of the row, kept for the keys' gradients
     float low = -kInf, delta = 0.f;
     {
         bf16x8 of[S::ks];
-        load_query<DB>(of, a.out.p + token * a.out.ts + head * a.out.hs, there, a.D, lane >> 5);
+        load_query<DB>(of, a.out.p + token * a.out.ts + head * a.out.hs, a.out.p, there, a.D, lane >> 5);
 #pragma unroll
         for (int k = 0; k < S::ks; ++k)
 #pragma unroll
