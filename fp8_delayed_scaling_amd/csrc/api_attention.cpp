@@ -149,7 +149,7 @@ int fp8_moe_route(const void *logits, int dtype, int64_t ld, int64_t T, int64_t 
     if (int st = check_route(logits, dtype, ld, T, E, top); st != FP8DS_OK) return st;
     if ((T > 0 && (experts == nullptr || weights == nullptr || lse == nullptr)) || counts == nullptr || prob_sum == nullptr || loss == nullptr)
         return FP8DS_ERR_NULL;
-    if (!all_aligned(4, experts, counts) || !all_aligned(4, weights, lse, prob_sum, loss) || !is_aligned(workspace, 4)) return FP8DS_ERR_ALIGN;
+    if (!all_aligned(4, experts, counts) || !all_aligned(4, weights, lse, prob_sum, loss) || !is_aligned(workspace, 8)) return FP8DS_ERR_ALIGN;
     const size_t need = fp8ds::moe_route_workspace_bytes(T, E);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8DS_ERR_WORKSPACE;
     fp8ds::Route a{};

@@ -163,9 +163,9 @@ struct Route {
     const float *dweights, *dloss;
     void *dlogits;
     int64_t ld_d;
-    // set by the launcher: the blocks' parts
-    float *part_sum;
-    int32_t *part_cnt;
+    // set by the launcher: the blocks' sums and counts, and their live rows
+    unsigned int __attribute__((ext_vector_type(2))) *part, *part_loss;
+    int32_t *part_live;
 };
 size_t moe_route_workspace_bytes(int64_t T, int64_t E);
 hipError_t launch_moe_route(Route a, void *ws, hipStream_t st);

@@ -525,7 +525,7 @@ int fp8_attention_bwd(fp8ds_heads dout, fp8ds_heads q, fp8ds_heads k, fp8ds_head
  * logits: [T, E] float32 or bfloat16 (dtype, an fp8ds_out_dtype), row stride ld >= E.  experts [T, top] int32, what
  * fp8_moe_plan reads; weights [T, top], lse [T], prob_sum [E], loss [1] float32; counts [E + 1] int32.  1 <= E <= 1024,
  * 1 <= top <= E.  Sums are float32 in a fixed order.  workspace: fp8_moe_route_workspace_bytes (0 for small T:
- * NULL), 4-byte aligned, no initialisation; calls that overlap in time must not share it.
+ * NULL), 8-byte aligned, no initialisation; calls that overlap in time must not share it.
  *
  * fp8_moe_route_bwd -- dlogits (type of logits, row stride ld_d) from dweights [T, top] and *dloss, either may be NULL:
  * counts are constants, weights and prob_sum are functions of the logits.  experts, weights, lse, counts: what the
