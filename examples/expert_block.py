@@ -3,6 +3,7 @@ stream, tokens sorted by expert, two FP8 products with their gradients, the weig
 
     python examples/expert_block.py        # one MI355X: a few steps, the loss and the time of each
 
+    choice, weights, balance loss of the router's logits                 fp8_moe_route
     x = resid + gate * norm(o)      h = norm(x), as FP8 codes            fp8_norm_residual_fwd
     hs = h in expert order, and its transpose                            fp8_moe_plan, fp8_moe_sort_codes
     u = hs W1[e]^T      a = relu(u)^2, cast      ys = a W2[e]^T          fp8_grouped_gemm, fp8_cast_transpose
@@ -22,6 +23,29 @@ import fp8_delayed_scaling_amd as F  # noqa: E402
 ALIGN = 16
 H_, ACT, W1_, W2_, DY, DU = range(6)          # the scaled tensors
 FORMATS = [F.E4M3, F.E4M3, F.E4M3, F.E4M3, F.E5M2, F.E5M2]
+
+
+class Router:
+    """Scores of the residual stream, the choice of experts they make, and the gradients back to them."""
+
+    def __init__(self, tokens, width, experts, top, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        f32, i32 = dict(device="cuda", dtype=torch.float32), dict(device="cuda", dtype=torch.int32)
+        self.w = torch.randn(experts, width, device="cuda", generator=g) * width ** -0.5
+        self.choice, self.weights, self.lse = torch.empty(tokens, top, **i32), torch.empty(tokens, top, **f32), torch.empty(tokens, **f32)
+        self.counts, self.prob_sum, self.loss = torch.empty(experts + 1, **i32), torch.empty(experts, **f32), torch.empty(1, **f32)
+        self.dlogits = torch.empty(tokens, experts, **f32)
+        self.ws = torch.empty(max(8, F.fp8_moe_route_workspace_bytes(tokens, experts)), device="cuda", dtype=torch.uint8)
+
+    def forward(self, x):
+        self.x, self.logits = x.float(), x.float() @ self.w.t()
+        F.fp8_moe_route(self.logits, self.choice, self.weights, self.lse, self.counts, self.prob_sum, self.loss, self.ws)
+        return self.choice, self.weights
+
+    def backward(self, dweights, dloss):
+        """Leaves the gradients in dw and dx."""
+        F.fp8_moe_route_bwd(self.logits, self.choice, self.weights, self.lse, self.counts, dweights, dloss, self.dlogits)
+        self.dw, self.dx = self.dlogits.t() @ self.x, self.dlogits @ self.w
 
 
 class ExpertBlock:
@@ -117,23 +141,23 @@ def main(tokens=8192, width=4096, hidden=2048, experts=64, top=4, steps=6):
     bf = dict(device="cuda", dtype=torch.bfloat16)
     o, resid = torch.randn(tokens, width, generator=g, **bf), torch.randn(tokens, width, generator=g, **bf)
     target = torch.randn(tokens, width, generator=g, **bf)
-    scores = torch.randn(tokens, experts, device="cuda", generator=g)
-    best, choice = torch.topk(scores, top, dim=1)
-    choice, weights = choice.to(torch.int32), torch.softmax(best, dim=1)
+    router, dloss = Router(tokens, width, experts, top), torch.full((1,), 0.01, device="cuda")
     for step in range(steps):
         begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         begin.record()
-        x, y = block.forward(o, resid, choice, weights)
+        x, y = block.forward(o, resid, *router.forward(resid))
         err = (x.float() + y.float() - target.float())
         grad = (err / tokens).bfloat16()
         block.backward(grad, grad)
+        router.backward(block.dweights, dloss)
         with torch.no_grad():
+            router.w.sub_(router.dw * (0.03 * router.w.norm() / router.dw.norm()))
             for w, dw in ((block.w1, block.dw1), (block.w2, block.dw2)):
                 w.sub_((dw * (0.03 * w.float().norm() / dw.norm())).bfloat16())      # a fixed part of the weights' size
         block.update_scales()
         end.record()
         torch.cuda.synchronize()
-        print(f"step {step}: loss {err.square().mean().item():.4f}, {begin.elapsed_time(end):.2f} ms", flush=True)
+        print(f"step {step}: loss {err.square().mean().item():.4f}, balance {router.loss.item():.3f}, {begin.elapsed_time(end):.2f} ms", flush=True)
 
 
 if __name__ == "__main__":

@@ -1312,13 +1312,16 @@ struct Plan {
     bool few;
     int64_t blocks, splits;
 };
-// Few query rows to a sequence: the waves share the keys.  Few blocks: the keys are split.
+// Few query rows to a sequence (32 at the mean: one block of 32): the waves share the keys.  Fewer blocks than the GPU
+// holds at a time (one block of few rows to a CU, two of the others): the keys are split, into as many parts as bring the
+// blocks nearest to that.  16 sequences of up to 4096 keys, 8 key heads, 144 blocks: 44.4 us whole, 37.7 in two parts, 40.5
+// in three, 39.9 in four, 49 in eight.
 Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ragged) {
     Plan p;
     p.few = Tq * G <= kFewRows * B;
     const int64_t tiles = most_tiles(Tq, B, G, p.few ? kFewRows : kRows, ragged) * Hkv;
-    const int64_t want = p.few ? 2 * kCUs : 2 * kCUs, shortest = p.few ? 256 : 512;
-    int64_t s = tiles > 0 ? want / tiles : 1;
+    const int64_t slots = p.few ? kCUs : 2 * kCUs, shortest = p.few ? 256 : 512;
+    int64_t s = tiles > 0 ? (slots + tiles / 2) / tiles : 1;
     const int64_t most = Tk / B / shortest;
     if (s > most) s = most;
     p.splits = s < 1 ? 1 : s > 64 ? 64 : s;
