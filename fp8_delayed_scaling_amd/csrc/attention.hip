@@ -1189,7 +1189,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = kKeys * S::pitch;
+    constexpr int kTile = kKeys * S::pitch, kRun = 2 * DB, kAhead = 3;
     __shared__ __align__(1024) uint8_t k0[kTile], k1[kTile], v0[kTile], v1[kTile];      // as in the forward
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hkv;
@@ -1204,7 +1204,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     bf16x8 qf[S::ks], df[S::ks];
     load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
     load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, a.dout.p, there, a.D, lane >> 5);
-    const float s2 = a.softmax_scale * kLog2e;
+    const float s2 = uniform_value(a.softmax_scale * kLog2e);
     // -lse / scale and -<dout, out> of the row, kept for the keys' gradients
     float low = -kInf, delta = 0.f;
     {
@@ -1231,7 +1231,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     const Seen see = seen(a, pos, sq.len, sk.len);         // rows past the last compute what is never written
     const RowLoads<DB, kKeys, kWaves> loads_k(lane, wave, a.D, a.k.ts), loads_v(lane, wave, a.D, a.v.ts);
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
-    const Reader<DB> rd(lane);
+    Walker<DB> rd(lane);
     f32x16 dq[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -1251,35 +1251,75 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
         }
         if (j >= end.hi || next <= first.lo) return;
         const bool masked = next > first.hi || j < end.lo;
+        // Six runs of products, kRun each: scores and dP of 32 keys, of the next 32, and the sums over either.  As in the keys'
+        // gradients: operands kAhead products ahead, the exponentials beside dP, the slopes beside the run after it.
+        f32x16 s[2], p[2];
+        bf16x8 f[kAhead], sf[2][2];
+        auto read = [&](int n) __attribute__((always_inline)) {
+            const int run = n / kRun, i = n % kRun;
+            if (run < 4) return read_row((run & 1 ? tv : tk) + (run >> 1) * 32 * S::pitch + rd.row(i));
+            return rd.tr(tk + ((run - 4) * 32 + i / DB * 16) * S::pitch, i % DB);
+        };
+        auto step = [&](int n) __attribute__((always_inline)) {      // the operand of product n; the one kAhead on is read
+            const bf16x8 now = f[n % kAhead];
+            if (n + kAhead < 6 * kRun) f[n % kAhead] = read(n + kAhead);
+            return now;
+        };
+        auto slopes = [&](int kb, int n) __attribute__((always_inline)) {     // from the third product on: dP's last is through
+            if (n >= 2) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const uint8_t *rk = tk + kb * 32 * S::pitch, *rv = tv + kb * 32 * S::pitch;
-            f32x16 s, p;
+                for (int i = (n - 2) * 16 / (kRun - 2); i < (n - 1) * 16 / (kRun - 2); ++i) p[kb][i] *= s[kb][i];
+            }
+            if (n == kRun - 1) sf[kb][0] = pack8(p[kb], 0), sf[kb][1] = pack8(p[kb], 1);
+        };
+        rd.fresh();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[i] = 0.f;
-                p[i] = delta;
+                s[kb][i] = 0.f;
+                p[kb][i] = delta;
             }
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) s = mfma(read_row(rk + rd.row[k]), qf[k], s);
+        for (int n = 0; n < kAhead; ++n) f[n] = read(n);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int k = 0; k < S::ks; ++k) p = mfma(read_row(rv + rd.row[k]), df[k], p);
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, low));
+            for (int n = 0; n < kRun; ++n) {
+                s[kb] = mfma(step(2 * kb * kRun + n), qf[n], s[kb]);
+                if (kb == 1) slopes(0, n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if (masked) {
                 const int h4 = j + kb * 32 + 4 * (lane >> 5);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int key = h4 + (i >> 2) * 8 + (i & 3);
-                    p[i] = key >= see.lo && key < see.hi ? p[i] : 0.f;
+                    s[kb][i] = key >= see.lo && key < see.hi ? s[kb][i] : -kInf;
                 }
             }
+            rd.fresh();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const bf16x8 sf = pack8(p, x);
+            for (int n = 0; n < kRun; ++n) {
+                p[kb] = mfma(step((2 * kb + 1) * kRun + n), df[n], p[kb]);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) dq[d] = mfma(read_tr<DB>(rk + x * 16 * S::pitch, rd, d), sf, dq[d]);
+                for (int i = n * 16 / kRun; i < (n + 1) * 16 / kRun; ++i) s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], s2, low));
+                __builtin_amdgcn_sched_barrier(0);
             }
+            rd.fresh();
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int n = 0; n < kRun; ++n) {
+                dq[n % DB] = mfma(step((4 + kb) * kRun + n), sf[kb][n / DB], dq[n % DB]);
+                if (kb == 0) slopes(1, n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            rd.fresh();
         }
     };
     for (int j = lo; j < hi; j += 2 * kKeys) {
