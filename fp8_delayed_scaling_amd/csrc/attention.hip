@@ -272,6 +272,7 @@ struct Emit {
 };
 __device__ __forceinline__ void write_inverse(const Attention &a) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.out8 != nullptr && a.sinv != nullptr) *a.sinv = 1.0f / *a.scale;
+    if (blockIdx.x == 0 && threadIdx.x < kTops && a.top != nullptr) a.top_done[threadIdx.x] = 0;      // k_attn_amax counts there
 }
 
 // Keys that query row `pos` of a sequence may see: [lo, hi).
@@ -763,13 +764,17 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
 
 // The amax.  Outputs made of rounded probabilities tell which rows may hold it: those within 1/64 of the largest (a rounded
 // probability is off by 2^-8 at most), kTops of them at most, one to a wave of k_attn_fwd.  These rows are computed again
-// with probabilities of 32 bits, kTopParts blocks to a row; k_attn_amax_join joins their sums in order.  (One launch whose last
-// blocks join took 17 us at 4 x 2048, 8 of them for the fences; the two take 5 and 3.)
+// with probabilities of 32 bits, kTopParts blocks to a row, and the last block of a row to come joins their sums in order.  The
+// sums pass between the blocks by accesses of their own to memory that all XCDs see: a fence would write a whole L2 back
+// (17 us at 4 x 2048 with fences, 13 in two launches).
+__device__ __forceinline__ void shared_store(float *p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float shared_load(const float *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
 __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     constexpr int kChunk = kThreads;                                 // keys at a time
     __shared__ uint32_t red[kWaves];
     __shared__ float fred[kWaves], prob[kChunk], q[128], acc[16][128];
-    __shared__ int found[kThreads], rows[kTops], all;
+    __shared__ int found[kThreads], rows[kTops], all, last;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     // the waves' outputs, four to a load (a.tops % 4 == 0), the first kHeld of a thread kept
     constexpr int kHeld = 8;
@@ -790,10 +795,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     __syncthreads();
     top = red[0];
     if (top == 0 || top >= 0x7F800000u) {                            // nothing, or an infinity or NaN, which no rounding made
-        if (blockIdx.x == 0 && t == 0) {
-            fold_amax_bits(a.amax, top);
-            *a.top_done = 0;
-        }
+        if (blockIdx.x == 0 && t == 0) fold_amax_bits(a.amax, top);
         return;
     }
     // the candidates: as they are found, then the first in the order of the waves
@@ -824,7 +826,6 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     }
     __syncthreads();
     const int c = blockIdx.x / kTopParts, part = blockIdx.x % kTopParts;
-    if (blockIdx.x == 0 && t == 0) *a.top_done = min(all, kTops);    // rows for k_attn_amax_join
     if (c >= min(all, kTops)) return;
     const int row = rows[c], token = row / a.Hq, head = row - token * a.Hq, kvh = head / a.G;
     int b;
@@ -906,22 +907,22 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += acc[i][t];
-        mine_part[t] = sum;
+        shared_store(mine_part + t, sum);
     }
     if (t == 128) {
-        mine_part[128] = m;
-        mine_part[129] = fred[0] + fred[1] + fred[2] + fred[3];
+        shared_store(mine_part + 128, m);
+        shared_store(mine_part + 129, fred[0] + fred[1] + fred[2] + fred[3]);
     }
-}
-
-__global__ __launch_bounds__(128) void k_attn_amax_join(const Attention a) {
-    __shared__ uint32_t red[2];
-    const int t = threadIdx.x;                                       // the element
-    if ((int)blockIdx.x >= *a.top_done) return;
-    const float *parts = a.top_part + (int64_t)blockIdx.x * kTopParts * 130;
-    float pm[kTopParts], pl[kTopParts], pv[kTopParts], m = -kInf, sum = 0.f, v = 0.f;
+    FP8DS_WAIT_VM(0);                                                // this wave's stores have arrived
+    __syncthreads();
+    if (t == 0) last = __hip_atomic_fetch_add(&a.top_done[c], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (last != kTopParts - 1 || t >= 128) return;
+    const float *parts = a.top_part + (int64_t)c * kTopParts * 130;
+    float pm[kTopParts], pl[kTopParts], pv[kTopParts], sum = 0.f, v = 0.f;
+    m = -kInf;
 #pragma unroll
-    for (int i = 0; i < kTopParts; ++i) pm[i] = parts[i * 130 + 128], pl[i] = parts[i * 130 + 129], pv[i] = parts[i * 130 + t];
+    for (int i = 0; i < kTopParts; ++i) pm[i] = shared_load(parts + i * 130 + 128), pl[i] = shared_load(parts + i * 130 + 129), pv[i] = shared_load(parts + i * 130 + t);
 #pragma unroll
     for (int i = 0; i < kTopParts; ++i) m = fmaxf(m, pm[i]);
 #pragma unroll
@@ -930,8 +931,8 @@ __global__ __launch_bounds__(128) void k_attn_amax_join(const Attention a) {
         sum += w * pl[i];
         v += w * pv[i];
     }
-    const uint32_t best = block_max_u32<128>(sum > 0.f ? __float_as_uint(v / sum) & 0x7FFFFFFFu : 0u, red);
-    if (t == 0) fold_amax_bits(a.amax, best);
+    const uint32_t best = wave_max_u32(sum > 0.f ? __float_as_uint(v / sum) & 0x7FFFFFFFu : 0u);
+    if (lane == 0) fold_amax_bits(a.amax, best);
 }
 
 // ---------------------------------------------------------------------------------- backward
@@ -1390,7 +1391,7 @@ struct Room {
         top_row = top + up((size_t)tops * 4);
         top_part = top_row + up((size_t)tops * 4);
         top_done = top_part + (tops > 0 ? kTops * kTopParts * 130 * 4 : 0);
-        bytes = top_done + (tops > 0 ? 16 : 0);
+        bytes = top_done + (tops > 0 ? kTops * 4 : 0);
     }
 };
 
@@ -1429,8 +1430,6 @@ hipError_t launch_attention_fwd(Attention a, void *ws, hipStream_t st) {
     }
     if (a.top != nullptr) {
         k_attn_amax<<<kTops * kTopParts, kThreads, 0, st>>>(a);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-        k_attn_amax_join<<<kTops, 128, 0, st>>>(a);
     }
     return hipGetLastError();
 }
