@@ -1206,8 +1206,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
     load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, a.dout.p, there, a.D, lane >> 5);
     const float s2 = uniform_value(a.softmax_scale * kLog2e);
-    // -lse / scale and -<dout, out> of the row, kept for the keys' gradients
-    float low = -kInf, delta = 0.f;
+    // -lse / scale and -<dout, out> of the row.  The output was rounded to bfloat16, which is off by up to 2^-8 of its terms
+    // there; the sum of the slopes P (dP - <dout, out>) is what is missing, so that the keys' gradients get the exact one.
+    float low = -kInf, delta = 0.f, slope_sum = 0.f;
     {
         bf16x8 of[S::ks];
         load_query<DB>(of, a.out.p + token * a.out.ts + head * a.out.hs, a.out.p, there, a.D, lane >> 5);
@@ -1220,11 +1221,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     if (there) {
         const float lse = a.lse[(int64_t)head * a.Tq + token];
         low = lse == -kInf ? -kInf : -lse / a.softmax_scale;
-        if (lane < 32) {
-            const int64_t at = ((int64_t)kvh * a.Tq + sq.begin) * a.G + r;
-            a.part[at] = low;
-            a.part[(int64_t)a.Tq * a.Hq + at] = delta;
-        }
+        if (lane < 32) a.part[((int64_t)kvh * a.Tq + sq.begin) * a.G + r] = low;
         low *= s2;
     }
     const int lo = seen(a, r0 / a.G, sq.len, sk.len).lo & ~(kKeys - 1), hi = seen(a, last / a.G, sq.len, sk.len).hi;
@@ -1269,7 +1266,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
         auto slopes = [&](int kb, int n) __attribute__((always_inline)) {     // from the third product on: dP's last is through
             if (n >= 2) {
 #pragma unroll
-                for (int i = (n - 2) * 16 / (kRun - 2); i < (n - 1) * 16 / (kRun - 2); ++i) p[kb][i] *= s[kb][i];
+                for (int i = (n - 2) * 16 / (kRun - 2); i < (n - 1) * 16 / (kRun - 2); ++i) {
+                    p[kb][i] *= s[kb][i];
+                    slope_sum += p[kb][i];
+                }
             }
             if (n == kRun - 1) sf[kb][0] = pack8(p[kb], 0), sf[kb][1] = pack8(p[kb], 1);
         };
@@ -1328,6 +1328,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
         if (j + kKeys >= hi) break;
         turn(j + kKeys, k1, v1, k0, v0);
     }
+    slope_sum = both_halves_sum(slope_sum);
+    if (there && lane < 32) a.part[(int64_t)a.Tq * a.Hq + ((int64_t)kvh * a.Tq + sq.begin) * a.G + r] = delta - slope_sum;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
