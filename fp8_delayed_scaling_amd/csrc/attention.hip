@@ -11,7 +11,6 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
-typedef short i16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kRows = 128;                   // query rows (or keys) of a block, 32 to a wave
@@ -169,11 +168,6 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int s) {
     return r;
 }
 
-// What the scheduler puts next: n reads of LDS, products, or other vector instructions.
-#define group_reads(n) __builtin_amdgcn_sched_group_barrier(0x100, n, 0)
-#define group_products(n) __builtin_amdgcn_sched_group_barrier(0x008, n, 0)
-#define group_values(n) __builtin_amdgcn_sched_group_barrier(0x002, n, 0)
-
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     const uint64_t u = (uint64_t)(uint32_t)uniform((int)a) | (uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32;
@@ -285,9 +279,9 @@ __device__ __forceinline__ Seen seen(const Attention &a, int pos, int lq, int lk
     return Seen{a.window > 0 ? max(0, at - a.window + 1) : 0, min(lk, at + 1)};
 }
 
-// One step of the running softmax: NKB blocks of 32 keys.  The probabilities enter the second product as bfloat16, with an
-// error of up to 2^-8; EXACT: as three bfloat16, which hold all 24 bits, where bytes and not products are the bound.
-template <int DB, int NKB, bool EXACT> struct Softmax {
+// The running softmax of k_attn_fwd_few, 32 keys a step.  Its probabilities enter the second product as three bfloat16, which
+// hold all 24 bits: bytes and not products are the bound there, so exact ones cost nothing (k_attn_fwd rounds them to one).
+template <int DB> struct Softmax {
     f32x16 o[DB];
     float m = -kInf, l = 0.f;                    // in units of log2; l: of this lane's keys only
     __device__ __forceinline__ Softmax() {
@@ -299,29 +293,22 @@ template <int DB, int NKB, bool EXACT> struct Softmax {
     __device__ __forceinline__ void step(const uint8_t *sk, const uint8_t *sv, const Reader<DB> &rd, const bf16x8 (&qf)[2 * DB],
                                          float s2, bool masked, int key0, Seen see, int lane) {
         using S = Shape<DB>;
-        f32x16 s[NKB];
+        f32x16 s;
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < S::ks; ++k) s[kb] = mfma(read_row(sk + kb * 32 * S::pitch + rd.row[k]), qf[k], s[kb]);
-        }
+        for (int k = 0; k < S::ks; ++k) s = mfma(read_row(sk + rd.row[k]), qf[k], s);
         if (masked) {
             const int h4 = key0 + 4 * (lane >> 5);
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = h4 + kb * 32 + (i >> 2) * 8 + (i & 3);
-                    s[kb][i] = key >= see.lo && key < see.hi ? s[kb][i] : -kInf;
-                }
+            for (int i = 0; i < 16; ++i) {
+                const int key = h4 + (i >> 2) * 8 + (i & 3);
+                s[i] = key >= see.lo && key < see.hi ? s[i] : -kInf;
+            }
         }
-        float mx = s[0][0];
+        float mx = s[0];
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
         mx = both_halves_max(mx) * s2;
         if (__any(mx > m + 8.f)) {               // no lane past 2^8 of its reference: the sums are kept as they are
             const float mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
@@ -334,37 +321,28 @@ template <int DB, int NKB, bool EXACT> struct Softmax {
         }
         const float ref = m == -kInf ? 0.f : m;
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, -ref));
+            l += s[i];
+        }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], s2, -ref));
-                l += s[kb][i];
+        for (int x = 0; x < 2; ++x) {
+            f32x16 left;
+            const bf16x8 p = pack8(s, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) left[i] = s[8 * x + i] - (float)p[i];
+            const bf16x8 p2 = pack8(left, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) left[i] -= (float)p2[i];
+            const bf16x8 p3 = pack8(left, 0);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const bf16x8 v = read_tr<DB>(sv + x * 16 * S::pitch, rd, d);
+                o[d] = mfma(v, p, o[d]);
+                o[d] = mfma(v, p2, o[d]);
+                o[d] = mfma(v, p3, o[d]);
             }
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const bf16x8 p = pack8(s[kb], x);
-                bf16x8 p2, p3;
-                if constexpr (EXACT) {
-                    f32x16 left;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) left[i] = s[kb][8 * x + i] - (float)p[i];
-                    p2 = pack8(left, 0);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) left[i] -= (float)p2[i];
-                    p3 = pack8(left, 0);
-                }
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const bf16x8 v = read_tr<DB>(sv + (kb * 32 + x * 16) * S::pitch, rd, d);
-                    o[d] = mfma(v, p, o[d]);
-                    if constexpr (EXACT) {
-                        o[d] = mfma(v, p2, o[d]);
-                        o[d] = mfma(v, p3, o[d]);
-                    }
-                }
-            }
+        }
     }
 };
 
@@ -642,7 +620,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
-    Softmax<DB, 1, true> sm;
+    Softmax<DB> sm;
     const int mine = wave * kTile;
     int j = lo + wave * 32;
     if (j < hi) {
@@ -772,7 +750,7 @@ __device__ __forceinline__ float shared_load(const float *p) { return __hip_atom
 
 __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     constexpr int kChunk = kThreads;                                 // keys at a time
-    __shared__ uint32_t red[kWaves];
+    __shared__ uint32_t red[kWaves], value[kThreads];
     __shared__ float fred[kWaves], prob[kChunk], q[128], acc[16][128];
     __shared__ int found[kThreads], rows[kTops], all, last;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -798,31 +776,38 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         if (blockIdx.x == 0 && t == 0) fold_amax_bits(a.amax, top);
         return;
     }
-    // the candidates: as they are found, then the first in the order of the waves
-    const uint32_t least = __float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64));
+    // the candidates as they are found, then the kTops largest of them, of equal ones the first in the order of the waves
+    uint32_t least = max(__float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64)), 1u);
     auto find = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
         if (max(max(x.x, x.y), max(x.z, x.w)) < least) return;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (x[u] >= least) {
                 const int at = atomicAdd(&all, 1);
-                if (at < kThreads) found[at] = 4 * i + u;
+                if (at < kThreads) found[at] = 4 * i + u, value[at] = x[u];
             }
     };
+    for (;;) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) find(held[i], t + i * kThreads);
+        for (int i = 0; i < kHeld; ++i) find(held[i], t + i * kThreads);
 #pragma unroll 8
-    for (int i = t + kHeld * kThreads; i < n; i += kThreads) find(tops[i], i);
-    __syncthreads();
+        for (int i = t + kHeld * kThreads; i < n; i += kThreads) find(tops[i], i);
+        __syncthreads();
+        if (all <= kThreads || least == top) break;                  // (the same in all threads)
+        __syncthreads();
+        if (t == 0) all = 0;
+        least += (top - least + 1) / 2;                              // too many: only the upper half
+        __syncthreads();
+    }
     if (all <= kThreads) {
         if (t < all) {
             int before = 0;
-            for (int i = 0; i < all; ++i) before += found[i] < found[t];
+            for (int i = 0; i < all; ++i) before += value[i] > value[t] || (value[i] == value[t] && found[i] < found[t]);
             if (before < kTops) rows[before] = a.top_row[found[t]];
         }
-    } else if (t == 0) {
+    } else if (t == 0) {                                             // all of them as large as the largest
         for (int i = 0, n = 0; n < kTops; ++i)
-            if (a.top[i] >= least) rows[n++] = a.top_row[i];
+            if (a.top[i] == top) rows[n++] = a.top_row[i];
     }
     __syncthreads();
     const int c = blockIdx.x / kTopParts, part = blockIdx.x % kTopParts;
