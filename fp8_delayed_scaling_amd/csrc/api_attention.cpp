@@ -26,7 +26,11 @@ inline bool size_ok(int64_t rows, int64_t cols) {
 // T tokens with `top` choices each, in 32-bit numbers.
 inline bool choices_ok(int64_t T, int64_t top) { return T >= 0 && top >= 1 && top <= INT_MAX && T <= INT_MAX / top; }
 
-// Tokens of heads at strides of their own.  `rows`: heads of neighbouring tokens that a kernel reaches from one base.
+// lse / softmax_scale and softmax_scale * log2(e) stay finite
+constexpr float kScaleMin = 1e-30f, kScaleMax = 1e30f;
+
+// Tokens of heads at strides of their own.  `group`: heads of neighbouring tokens that a kernel reaches from one base, by byte
+// offsets below 2^31 (up to 34 tokens on).
 int check_heads(const fp8ds_heads &h, int64_t T, int64_t H, int64_t D, bool output, int64_t group) {
     if (T == 0) return FP8DS_OK;
     if (h.token_stride < 0 || h.head_stride < 0) return FP8DS_ERR_SHAPE;
@@ -46,7 +50,7 @@ int check_attention(const int32_t *offsets_q, const int32_t *offsets_k, int64_t 
     if (Tq > fp8ds::kAttnMaxRows / Hq || Tk > fp8ds::kAttnMaxRows / Hkv) return FP8DS_ERR_SHAPE;
     if ((offsets_q == nullptr) != (offsets_k == nullptr)) return FP8DS_ERR_NULL;
     if (offsets_q == nullptr && B > 0 && (Tq % B != 0 || Tk % B != 0)) return FP8DS_ERR_SHAPE;
-    if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f || window < 0 || (window > 0 && causal == 0)) return FP8DS_ERR_ARG;
+    if (!(softmax_scale >= kScaleMin && softmax_scale <= kScaleMax) || window < 0 || (window > 0 && causal == 0)) return FP8DS_ERR_ARG;
     if (!all_aligned(4, offsets_q, offsets_k)) return FP8DS_ERR_ALIGN;
     return fp8ds::attention_fits(Tq, Tk, B, Hq, Hkv, offsets_q != nullptr) ? FP8DS_OK : FP8DS_ERR_SHAPE;
 }

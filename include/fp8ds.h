@@ -473,8 +473,10 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  *
  * D % 8 == 0, 8 <= D <= 128; strides % 8 == 0; token strides >= D (one token: any) and below 2^23; data 16-byte
  * aligned; T * heads <= 2^28; the heads that share a key/value head lie within 2^30 elements.
- * softmax_scale > 0; window only with causal.  Scores, softmax and sums are float32; the probabilities are
- * rounded to bfloat16 as operands of the matrix cores.  A NaN or an infinity in q, k or v may reach every row
+ * 1e-30 <= softmax_scale <= 1e30; window only with causal.  Scores, softmax and sums are float32; the probabilities
+ * are rounded to bfloat16 as operands of the matrix cores (with up to 32 rows Tq * Hq / Hkv to a sequence they are not),
+ * which puts o off by up to 2^-8 of sum_j p |v|.  The amax is that of unrounded probabilities: the rows that may hold it
+ * are computed again, the 16 largest of those within 1/64 of the largest.  A NaN or an infinity in q, k or v may reach every row
  * of its sequence, those that do not see it too.  workspace: fp8_attention_workspace_bytes is enough for any call of
  * these sizes (one that splits nothing and wants no amax takes none: NULL), 16-byte aligned, no initialisation; calls
  * that overlap in time must not share it.
@@ -499,7 +501,8 @@ int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads o
  *   dk[j] = softmax_scale * sum_i ds[i, j] * q[i],  dv[j] = sum_i p[i, j] * dout[i]    (over the heads that share k, v)
  *
  * out, lse: what the forward wrote.  dq, dk, dv: bfloat16, strided as q, k, v may be (no two elements in one
- * place), so that they can be slices of the QKV layer's output gradient; rows of no sequence are not written.
+ * place, none in an input's), so that they can be slices of the QKV layer's output gradient; rows of no sequence are
+ * not written.
  * The rest as fp8_attention_fwd.  p and ds are rounded to bfloat16 as operands; every sum is float32 in a
  * fixed order: the same run to run.
  */

@@ -187,3 +187,20 @@ def test_route_binding_checks():
 
 def test_structure_of_heads():
     assert ctypes.sizeof(F._Heads) == 24
+
+
+@pytest.mark.parametrize("name,ok", [("fp8_attention_fwd", FWD), ("fp8_attention_bwd", BWD)])
+def test_softmax_scale_range(name, ok):
+    """lse / softmax_scale and softmax_scale * log2(e) have to stay finite."""
+    call = _call(name, ok)
+    assert call(sc=1e-31) == -7 and call(sc=1e31) == -7 and call(sc=3e38) == -7
+    assert call(sc=1e-29, B=0) == 0 and call(sc=1e29, B=0) == 0
+
+
+def test_attention_group_reach():
+    """Heads that share a key/value head are reached by 32-bit byte offsets from one base, 34 tokens on at most."""
+    call = _call("fp8_attention_bwd", BWD)
+    reach = (1 << 30) // 2 - 34 * 256 // 2 - 64
+    for n in ("q", "do"):
+        assert call(**{n: H(hs=(reach // 8 + 1) * 8)}) == -2
+        assert call(**{n: H(hs=reach // 8 * 8)}, ws=None) == -5        # passes: the next refusal is the workspace's
