@@ -19,6 +19,7 @@ constexpr int kKeys = 64;                    // keys of a step
 constexpr int kStepRows = 64;                // query rows of a step
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor's bound
 constexpr int kBufDesc3 = 0x00020000;        // raw buffer descriptor, bounds checked in bytes
+constexpr int kMostSplits = 64;              // of the keys
 constexpr int kTops = 16, kTopParts = 32;     // rows that are computed again for the amax, shares of their keys
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
@@ -363,6 +364,10 @@ __device__ __forceinline__ void load_query(bf16x8 (&f)[2 * DB], const uint16_t *
     }
 }
 
+// What a part's sums count in the whole: about its reference m, against the whole's.  Without a key that counts l is 0, or NaN
+// where the scores were, and stays one.
+__device__ __forceinline__ float part_weight(float m, float l, float whole) { return m == -kInf ? l * 0.f : __builtin_amdgcn_exp2f(m - whole); }
+
 __device__ __forceinline__ float *part_sums(const Attention &a, int split) { return a.part + ((int64_t)split * a.Tq * a.Hq) * a.D; }
 __device__ __forceinline__ float *part_stats(const Attention &a, int split) {
     return a.part + (int64_t)a.splits * a.Tq * a.Hq * a.D + (int64_t)split * a.Tq * a.Hq * 2;
@@ -673,7 +678,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
         for (int i = 0; i < kWaves; ++i) m = fmaxf(m, stats[i][x][0]);
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
-            const float wt = stats[i][x][0] == -kInf ? 0.f : __builtin_amdgcn_exp2f(stats[i][x][0] - m);
+            const float wt = part_weight(stats[i][x][0], stats[i][x][1], m);
             sum += stats[i][x][1] * wt;
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[u] += reinterpret_cast<const float *>(sums[i])[x * kPitch + d + u] * wt;
@@ -718,19 +723,39 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
     }
     Emit emit(a);
     if (there) {
-        float m = -kInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < a.splits; ++i) m = fmaxf(m, part_stats(a, i)[row * 2]);
-        for (int i = 0; i < a.splits; ++i) {
-            const float *st = part_stats(a, i) + row * 2;
-            if (st[0] == -kInf) continue;
-            const float wt = __builtin_amdgcn_exp2f(st[0] - m);
-            sum += st[1] * wt;
-            if (d < a.D) {
-                const float *from = part_sums(a, i) + row * a.D + d;
+        // lane l of the row takes the stats of the splits l, l + 16, ...
+        constexpr int kTurns = kMostSplits / 16;
+        float w[kTurns], m = -kInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float2 st[kTurns];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] += from[u] * wt;
-            }
+        for (int n = 0; n < kTurns; ++n) {
+            const int i = n * 16 + (threadIdx.x & 15);
+            st[n] = i < a.splits ? *reinterpret_cast<const float2 *>(part_stats(a, i) + row * 2) : make_float2(-kInf, 0.f);
+            m = fmaxf(m, st[n].x);
         }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 16));
+#pragma unroll
+        for (int n = 0; n < kTurns; ++n) {
+            w[n] = part_weight(st[n].x, st[n].y, m);
+            sum += st[n].y * w[n];
+        }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 16);
+        const float *from = part_sums(a, 0) + row * a.D + (d < a.D ? d : 0);
+        const int64_t next = (int64_t)a.Tq * a.Hq * a.D;
+#pragma unroll
+        for (int n = 0; n < kTurns; ++n)
+#pragma unroll 8
+            for (int i = n * 16; i < min(a.splits, n * 16 + 16); ++i) {
+                const float wt = __shfl(w[n], i & 15, 16);
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(from + i * next), hi = *reinterpret_cast<const f32x4 *>(from + i * next + 4);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    v[u] += lo[u] * wt;
+                    v[4 + u] += hi[u] * wt;
+                }
+            }
         const float inv = sum > 0.f ? 1.0f / sum : sum == 0.f ? 0.f : sum;
         if (d == 0 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = sum == 0.f ? -kInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 #pragma unroll
@@ -1352,7 +1377,7 @@ Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ra
     int64_t s = tiles > 0 ? (slots + tiles / 2) / tiles : 1;
     const int64_t most = Tk / B / shortest;
     if (s > most) s = most;
-    p.splits = s < 1 ? 1 : s > 64 ? 64 : s;
+    p.splits = s < 1 ? 1 : s > kMostSplits ? kMostSplits : s;
     p.blocks = tiles * p.splits;
     return p;
 }

@@ -129,3 +129,17 @@ def test_one_expert_twice():
     mag.scatter_add_(1, at, part.abs())
     # p: the float32 lse and the exponential of a difference of numbers below 16, three roundings of at most 2^-21 each; sums of 23 terms
     assert bool(((got.double() - want).abs() <= mag * (3 * 16 * 2.0 ** -23 + 26 * 2.0 ** -24)).all())
+
+
+@pytest.mark.parametrize("lq,lk", [(1, 300), (1, 6000), (4, 4000), (200, 300), (200, 6000)])
+def test_a_row_that_is_not_a_number(lq, lk):
+    """A query of NaNs gives NaNs, also where its keys are shared among waves or blocks, and no other row does."""
+    q, k, v, dout = inputs(6, 2 * lq, 2 * lk, 4, 2, 64)
+    want = run_forward(q, k, v, batch=2)
+    q[0, 1] = torch.nan
+    out, lse, _ = run_forward(q, k, v, batch=2)
+    assert bool(out[0, 1].isnan().all()) and bool(lse[1, 0].isnan())
+    out[0, 1], lse[1, 0] = want[0][0, 1], want[1][1, 0]
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    f = run_forward(q, k, v, batch=2, fp8=True)[2]
+    assert bool((f["out8"].view(q.shape)[0, 1] == 0x7F).all()) and f["amax_slot"].isnan().all()
