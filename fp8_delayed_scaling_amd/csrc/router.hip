@@ -11,7 +11,6 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kMostBlocks = 256;
-constexpr int64_t kOneBlock = 128;           // rows that one block takes, finishing them itself
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
 
@@ -455,15 +454,20 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const Route a) {
 }
 
 namespace {
-int64_t route_blocks(int64_t T) {
-    if (T <= kOneBlock) return 1;
+// Rows that one block takes in one turn (64 of up to 256 experts, 16 of more) it finishes by itself, in one launch; more rows
+// are spread, and joined in a second.  us with one block and with several, bfloat16: 64 rows of 64 experts, 4 choices 5.3
+// and 7.2, 128 rows 7.1 and 7.4; 64 rows of 256, 8 choices 11.9 and 15.7, 128 rows 18.7 and 16.0; 64 rows of 1024 (four
+// turns) 32.5 and 16.6.  256 blocks, one to a CU, at most: 32768 rows of 256 experts 25.5, with 128 blocks 39, with 512
+// 30.9 (the second block of a CU waits for the first's LDS); 8192 rows of 64 9.4, 9.8 and 11.7.
+int64_t route_blocks(int64_t T, int64_t E) {
+    if (T <= (E <= 256 ? 4 : 1) * kWaves) return 1;
     const int64_t n = (T + kWaves - 1) / kWaves;
     return n < kMostBlocks ? n : kMostBlocks;
 }
 }  // namespace
 
 size_t moe_route_workspace_bytes(int64_t T, int64_t E) {
-    const int64_t nb = route_blocks(T);
+    const int64_t nb = route_blocks(T, E);
     return nb > 1 ? (size_t)(nb * (2 * E + 1) * 4 + kMoeMaxExperts / 64 * 8) : 0;
 }
 
@@ -474,7 +478,7 @@ size_t moe_route_workspace_bytes(int64_t T, int64_t E) {
     } while (0)
 
 hipError_t launch_moe_route(Route a, void *ws, hipStream_t st) {
-    const int64_t nb = route_blocks(a.T);
+    const int64_t nb = route_blocks(a.T, a.E);
     a.part = static_cast<u32x2 *>(ws);
     a.part_loss = a.part + nb * a.E;
     a.part_live = reinterpret_cast<int32_t *>(a.part_loss + kMoeMaxExperts / 64);
