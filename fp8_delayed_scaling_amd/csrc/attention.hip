@@ -1,4 +1,25 @@
 // attention.hip -- attention between the QKV layer and the projection, forward and backward, on gfx950.
+//
+// Forward, one pass over the keys with a running reference m and sum l of each query row (scores in units of log2):
+//   S^T = K Q^T,  P = exp2(S scale log2(e) - m),  O^T += V^T P^T,  l += sum P;   out = O / l, lse = (m + log2 l) ln 2
+// The reference moves, and O and l are rescaled, only where a score passes it by 2^8: all quotients stay what they are.
+// Backward, from lse, without a sum over the row:
+//   P = exp2((S - lse / scale) scale log2(e)),  dS = P (dO V^T - <dO, O>)
+//   dQ = scale dS K (k_attn_dq, by query rows);  dV = P^T dO,  dK = scale dS^T Q (k_attn_dkv, by keys)
+// in two kernels, so that every sum has one owner and a fixed order; S and dP are computed in both (7 products, not 5).
+//
+// Products are 32 x 32 x 16 matrix instructions with the scores transposed: a lane owns one query row (in k_attn_dkv one
+// key) and 16 of 32 scores, so a row's maximum and sum take one exchange between the wave's halves, and the 16 values,
+// rounded to bfloat16, are the next product's operand as they lie: the contraction runs over the rows in the order in
+// which the lanes hold them, and the other operand is read from LDS in that order by transposing reads.  Query rows are
+// numbered token by token, the heads of a key/value head's group side by side, so that a tile of keys serves the whole
+// group, and the keys' gradients sum over the group inside one block.
+//
+// What bounds them: the matrix units, and the power that they draw.  A loop of these instructions from registers, with
+// random bits, sustains 1.75 PFLOP/s on this card, the forward of 1 x 8192 tokens of 32 heads (8 of keys) of 128 1.03 (532
+// us causal), its backward 0.82 of five products, 1.15 of the seven (1684 us); with zeros as inputs, and all else the same,
+// 394 and 1232 us: the clock falls from 2.4 to 1.6 .. 1.95 GHz under load.  No single part of a step bounds it: with the loads
+// and barriers left out the forward took 9 % less, without the exponentials 8 %, without the reads of LDS 9 %.
 #include <climits>
 
 #include "../../include/fp8ds.h"
@@ -144,8 +165,9 @@ template <int DB> __device__ __forceinline__ bf16x8 read_tr(const uint8_t *p, co
     const i16x4 a = read_tr4(p + rd.tr[d][0]), b = read_tr4(p + rd.tr[d][1]);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-// The same addresses from three registers: the pieces' numbers enter by exclusive or.  16 of those a step cost less than
-// 13 registers where these are short.
+// The same addresses from three registers: the pieces' numbers enter by exclusive or.  In the kernels with 200 and more
+// registers in use these instructions cost less than the 13 registers (k_attn_dkv spills with a Reader; the forward and
+// k_attn_dq take the same time with either).
 template <int DB> struct Walker {
     uint32_t row0, tr0, tr1;
     __device__ __forceinline__ explicit Walker(int lane) {
@@ -375,7 +397,13 @@ __device__ __forceinline__ float *part_stats(const Attention &a, int split) {
 
 }  // namespace
 
-// A block: 128 query rows of one key/value head, 32 to each wave; all waves read the same keys.
+// A block: 128 query rows of one key/value head, 32 to each wave; all waves read the same 64 keys a step, from two turns of
+// LDS (64 KB, two blocks to a CU, so that one block's barrier and exponentials lie beside the other's products).  The
+// probabilities are rounded to bfloat16 (off by up to 2^-8 of each term, as the output itself): the matrix instruction's
+// type; with float32 ones in three parts the second product takes three times as long.  4 x 2048 tokens, 32 heads, 8 of
+// keys, of 128, causal: 168 .. 180 us, 0.8 PFLOP/s (half of a tile at the diagonal counts for nothing, and a block's
+// start and end take 4 us of 45); without a mask 280 us, 0.98; 1 x 16384 causal 1.07.  What a head size that fills no
+// block of 32 costs: 72 is computed as 96 (1 x 2048 41 us; as 128 46, and 2 x 4096 of 96 237 and 263 us).
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     using S = Shape<DB>;
@@ -591,7 +619,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     emit.finish(a);
 }
 
-// A block: up to 32 query rows of one key/value head; its waves share the keys.
+// A block: up to 32 query rows of one key/value head; its waves share the keys, 32 to a wave, each with two turns of LDS of
+// its own and no barrier until the end.  Bound by the bytes of K and V: 16 sequences of up to 4096 keys, 8 key heads of 128,
+// 170 MB in 33.5 us, 5.0 TB/s, what a copy reaches; k_attn_join behind it 5.0 us.
 template <int DB>
 __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a) {
     using S = Shape<DB>;
@@ -704,7 +734,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     if (a.splits == 1) emit.finish(a);
 }
 
-// The splits' sums of each row, joined in order.  16 threads a row; rows of no sequence stay as they are.
+// The splits' sums of each row, joined in order.  16 threads a row; rows of no sequence stay as they are.  Bound by the
+// latency of two dependent rounds of loads (5 us), then by the parts' bytes: 8192 rows of 8 parts, 34 MB, 8.7 us.
 __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
     const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int d = (threadIdx.x & 15) * 8;
@@ -769,7 +800,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
 // probability is off by 2^-8 at most), kTops of them at most, one to a wave of k_attn_fwd.  These rows are computed again
 // with probabilities of 32 bits, kTopParts blocks to a row, and the last block of a row to come joins their sums in order.  The
 // sums pass between the blocks by accesses of their own to memory that all XCDs see: a fence would write a whole L2 back
-// (17 us at 4 x 2048 with fences, 13 in two launches).
+// (17 us at 4 x 2048 with fences, 13 in two launches).  10.6 us: three dependent rounds of reads, of the waves' maxima by
+// every block, of keys, of values.
 __device__ __forceinline__ void shared_store(float *p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ float shared_load(const float *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
@@ -948,7 +980,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
 // ---------------------------------------------------------------------------------- backward
 // Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  A lane's loads of a
 // tile lie `turn` = 16 or 32 rows apart, its tiles 128 (two sets of waves).  EVEN: G divides `turn`, so that a lane keeps
-// its head and its offset, and only the bases move; otherwise the rows are walked, not divided.
+// its head and its offset, and only the bases move; otherwise the rows are walked, not divided.  (1 x 4096 tokens, 32 heads, 8
+// of keys, of 128: backward 559 us, walked 650; heads of 64: 336 and 343.)
 template <int DB, bool EVEN> struct GroupLoads {
     using S = Shape<DB>;
     static constexpr int turn = S::rows_a_load * kWaves, n = kStepRows / turn;       // loads of a wave for one tile
@@ -1004,7 +1037,12 @@ template <int DB, bool EVEN> struct GroupLoads {
 };
 
 // A block: 128 keys of one key/value head over all query rows of its group that see them.  Two sets of four waves take
-// turns at the steps of 64 rows, 32 keys to each wave of a set; the second set's sums are added to the first's at the end.
+// turns at the steps of 64 rows, 32 keys to each wave of a set; the second set's sums are added to the first's at the end.  A
+// wave's K and V stay in registers, its dK and dV in accumulators: with heads of 128 that is 192 of the 256 registers that
+// two waves a SIMD leave to each, so that what else a step keeps is counted (addresses by exclusive or, operands one or two
+// products ahead; a spilled register's reload waits for the loads in flight as well: 400 us with spills, 331 without).
+// 4 x 2048 tokens, 32 heads, 8 of keys, of 128, causal: 272 .. 323 us, 0.85 .. 1.0 PFLOP/s of its four products; 1 x 8192
+// 1103 us, 1.0.  The matrix units are in use for 59 % of the cycles at the clock that the power leaves.
 template <int DB, bool EVEN>
 __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a) {
     using S = Shape<DB>;
@@ -1195,8 +1233,10 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
         }
 }
 
-// A block: 128 query rows, 32 to each wave, over the keys that they see.  It also leaves what the keys' gradients need of
-// each row in the workspace, in the order [key/value head, token, head of the group].
+// A block: 128 query rows, 32 to each wave, over the keys that they see, as the forward.  It also leaves what the keys'
+// gradients need of each row in the workspace, in the order [key/value head, token, head of the group].  4 x 2048 tokens, 32
+// heads, 8 of keys, of 128, causal: 215 .. 249 us, 0.8 .. 0.95 PFLOP/s of its three products; 1 x 8192 750 .. 791 us, 1.0; matrix
+// units in use for 64 % of the cycles.
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;
@@ -1365,10 +1405,14 @@ struct Plan {
     bool few;
     int64_t blocks, splits;
 };
-// Few query rows to a sequence (32 at the mean: one block of 32): the waves share the keys.  Fewer blocks than the GPU
+// Few query rows to a sequence (32 at the mean: one block of 32): the waves share the keys.  8 key heads, 4 rows to each of 16
+// sequences of 4096 keys: 46.5 us and 48 with blocks of 128 rows, 32 rows to each of 4 of 8192 keys 29.7 and 32.2; past that
+// it depends on what fills the GPU (64 rows to each of 16 of 4096 keys 50 and 54, to each of 64 of 1024 88 and 49).
+// Fewer blocks than the GPU
 // holds at a time (one block of few rows to a CU, two of the others): the keys are split, into as many parts as bring the
 // blocks nearest to that.  16 sequences of up to 4096 keys, 8 key heads, 144 blocks: 44.4 us whole, 37.7 in two parts, 40.5
-// in three, 39.9 in four, 49 in eight.
+// in three, 39.9 in four, 49 in eight.  Parts no shorter than 512 keys of blocks of 128 rows (one sequence of 2048 keys, 256
+// tokens: 28 us, with 256 keys 31.6, with 1024 30.6), of 256 of the others.
 Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ragged) {
     Plan p;
     p.few = Tq * G <= kFewRows * B;

@@ -1,4 +1,11 @@
 // router.hip -- the choice of experts from the router's logits, with the balance loss, and its gradient, on gfx950.
+//
+// One read of the logits: the first choice is the row's maximum, which the softmax is taken about; every further choice is a
+// maximum over what is left.  A block adds its rows' probabilities and choices up, and a second launch joins the blocks
+// in order.  Bound by latency up to some thousand rows (8192 of 64 experts, 4 choices: 9.4 us, a launch of 5.9 and one of
+// 4.0), then by the instructions of the choices: 32768 rows of 256 experts, 8 choices, 21.8 us for 19 MB.
+// Backward: with g_j = dweights_j, c_e = dloss E counts_e / (choices * rows), w the weights
+//   dp = c + g at the choices (normalised: (g - <w, g>) / sum of p),  dlogits = p (dp - <p, dp>)
 #include <climits>
 
 #include "../../include/fp8ds.h"
@@ -217,8 +224,9 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const Route a) {
 }
 
 // Up to 256 experts: a wave takes four rows, 16 lanes to a row, lane l of them the experts l, l + 16, ...  No step leaves
-// the 16 lanes, so that a choice costs a row a quarter of the wave's instructions (32768 rows of 256 experts, 8 choices:
-// 31 us with a wave to a row).
+// the 16 lanes, so that a choice costs a row a quarter of the wave's instructions.  32768 rows of 256 experts, 8 choices:
+// 25.5 us, with a wave to a row 35.3; of 8192 rows, whose waves take four rows and no more, 17.8 and 15.7.  More experts do
+// not fit a lane's registers: V logits, keys, sums and the next row's logits.
 template <int CTRL> __device__ __forceinline__ uint32_t max16(uint32_t v) { return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true)); }
 __device__ __forceinline__ uint32_t row_max(uint32_t v) { return max16<0x121>(max16<0x122>(max16<0x124>(max16<0x128>(v)))); }      // row_ror 8, 4, 2, 1
 template <int CTRL> __device__ __forceinline__ float add16(float v) {
@@ -392,7 +400,8 @@ __global__ __launch_bounds__(64) void k_moe_route_loss(const Route a, int blocks
     *a.loss = loss_of(a.E, both, all, a.counts[a.E]);
 }
 
-// dlogits[e] = p_e (c_e - s) + the chosen experts' own part; a wave to a row.
+// dlogits[e] = p_e (c_e - s) + the chosen experts' own part; a wave to a row.  Bound by latency: 8192 rows of 64 experts 4.7 us,
+// 5 MB.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_moe_route_bwd(const Route a) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
