@@ -7,6 +7,8 @@
 //   P = exp2((S - lse / scale) scale log2(e)),  dS = P (dO V^T - <dO, O>)
 //   dQ = scale dS K (k_attn_dq, by query rows);  dV = P^T dO,  dK = scale dS^T Q (k_attn_dkv, by keys)
 // in two kernels, so that every sum has one owner and a fixed order; S and dP are computed in both (7 products, not 5).
+// P and dS are rounded to bfloat16 as operands: the gradients are off by 0.0024 .. 0.0026 of their norm, 0.0017 of which is their
+// own rounding to bfloat16 and as much that of the operands.  In two parts each they would take ten products for seven.
 //
 // Products are 32 x 32 x 16 matrix instructions with the scores transposed: a lane owns one query row (in k_attn_dkv one
 // key) and 16 of 32 scores, so a row's maximum and sum take one exchange between the wave's halves, and the 16 values,
@@ -1406,8 +1408,9 @@ struct Plan {
     int64_t blocks, splits;
 };
 // Few query rows to a sequence (32 at the mean: one block of 32): the waves share the keys.  8 key heads, 4 rows to each of 16
-// sequences of 4096 keys: 46.5 us and 48 with blocks of 128 rows, 32 rows to each of 4 of 8192 keys 29.7 and 32.2; past that
-// it depends on what fills the GPU (64 rows to each of 16 of 4096 keys 50 and 54, to each of 64 of 1024 88 and 49).
+// sequences of 4096 keys: 46.5 us and 48 with blocks of 128 rows, 32 rows to each of 4 of 8192 keys 29.7 and 32.2.  Up to 64
+// rows, two blocks that read the same keys, as long as these blocks are one round (64 rows to each of 16 of 4096 keys 50
+// and 54, to one of 8192 19 and 21.5, to one of 2882 15.6 and 19.5; to each of 64 of 1024, four rounds, 88 and 49; 128 rows to each of 16 53 and 39).
 // Fewer blocks than the GPU
 // holds at a time (one block of few rows to a CU, two of the others): the keys are split, into as many parts as bring the
 // blocks nearest to that.  16 sequences of up to 4096 keys, 8 key heads, 144 blocks: 44.4 us whole, 37.7 in two parts, 40.5
@@ -1415,7 +1418,7 @@ struct Plan {
 // tokens: 28 us, with 256 keys 31.6, with 1024 30.6), of 256 of the others.
 Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ragged) {
     Plan p;
-    p.few = Tq * G <= kFewRows * B;
+    p.few = Tq * G <= kFewRows * B || (Tq * G <= 2 * kFewRows * B && most_tiles(Tq, B, G, kFewRows, ragged) * Hkv <= kCUs);
     const int64_t tiles = most_tiles(Tq, B, G, p.few ? kFewRows : kRows, ragged) * Hkv;
     const int64_t slots = p.few ? kCUs : 2 * kCUs, shortest = p.few ? 256 : 512;
     int64_t s = tiles > 0 ? (slots + tiles / 2) / tiles : 1;

@@ -474,12 +474,12 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * D % 8 == 0, 8 <= D <= 128; strides % 8 == 0; token strides >= D (one token: any) and below 2^23; data 16-byte
  * aligned; T * heads <= 2^28; the heads that share a key/value head lie within 2^30 elements.
  * 1e-30 <= softmax_scale <= 1e30; window only with causal.  Scores, softmax and sums are float32; the probabilities
- * are rounded to bfloat16 as operands of the matrix cores (with up to 32 rows Tq * Hq / Hkv to a sequence they are not),
- * which puts o off by up to 2^-8 of sum_j p |v|.  The amax is that of unrounded probabilities: the rows that may hold it
- * are computed again, the 16 largest of those within 1/64 of the largest.  A NaN or an infinity in q, k or v may reach every row
- * of its sequence, those that do not see it too.  workspace: fp8_attention_workspace_bytes is enough for any call of
- * these sizes (one that splits nothing and wants no amax takes none: NULL), 16-byte aligned, no initialisation; calls
- * that overlap in time must not share it.
+ * are rounded to bfloat16 as operands of the matrix cores, which puts o off by up to 2^-8 of sum_j p |v| (with few rows
+ * to a sequence, up to 32 of Tq * Hq / Hkv at the mean and up to 64 of few sequences, they are not rounded).  The amax is
+ * that of unrounded probabilities: the rows that may hold it are computed again, the 16 largest of those within 1/64 of the
+ * largest.  A NaN or an infinity in q, k or v may reach every row of its sequence, those that do not see it too.
+ * workspace: fp8_attention_workspace_bytes is enough for any call of these sizes (one that splits nothing and wants no amax
+ * takes none: NULL), 16-byte aligned, no initialisation; calls that overlap in time must not share it.
  */
 typedef struct {
     uint16_t *data;
