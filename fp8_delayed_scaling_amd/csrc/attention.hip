@@ -304,12 +304,35 @@ __device__ __forceinline__ Seen seen(const Attention &a, int pos, int lq, int lk
     return Seen{a.window > 0 ? max(0, at - a.window + 1) : 0, min(lk, at + 1)};
 }
 
+// The running reference of a row's sums, in units of log2 (m; ref: 0 for none).  An exponential is exp2(fma(score, s2, -ref)), and
+// ref a rounding of score * s2 for the largest: where that passes 2^30, half a step of it is 32 and more, and the largest
+// exponential would be 0 or an infinity.  Such a row takes the power of two below s2, with which the product is exact: scores a
+// step apart are then 2^-32 and less of each other with either.  Nothing changes for all other rows, nor in time (1 x 8192 524
+// us with and without; (score - m) * s2 for every score instead, one instruction more, 549).
+constexpr float kFar = 0x1p30f;
+constexpr float kFarLse = 0x1p24f;               // beyond it no digit of exp(score - lse) is left of a float32 lse
+struct Reference {
+    float m = -kInf, ref = 0.f, s2;
+    __device__ __forceinline__ explicit Reference(float all) : s2(all) {}
+    // from the largest score so far: what the sums are to be multiplied by
+    __device__ __forceinline__ float move(float top, float all) {
+        const float mx = top * all, mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        if (mx > m) {
+            s2 = fabsf(mx) > kFar ? __uint_as_float(__float_as_uint(all) & 0xFF800000u) : all;
+            ref = top * s2;
+        }
+        m = mn;
+        return al;
+    }
+};
+
 // The running softmax of k_attn_fwd_few, 32 keys a step.  Its probabilities enter the second product as three bfloat16, which
 // hold all 24 bits: bytes and not products are the bound there, so exact ones cost nothing (k_attn_fwd rounds them to one).
 template <int DB> struct Softmax {
     f32x16 o[DB];
-    float m = -kInf, l = 0.f;                    // in units of log2; l: of this lane's keys only
-    __device__ __forceinline__ Softmax() {
+    Reference r;
+    float l = 0.f;                               // of this lane's keys only
+    __device__ __forceinline__ explicit Softmax(float s2) : r(s2) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -334,20 +357,18 @@ template <int DB> struct Softmax {
         float mx = s[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
-        mx = both_halves_max(mx) * s2;
-        if (__any(mx > m + 8.f)) {               // no lane past 2^8 of its reference: the sums are kept as they are
-            const float mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-            m = mn;
+        mx = both_halves_max(mx);
+        if (__any(mx * s2 > r.m + 8.f)) {        // no lane past 2^8 of its reference: the sums are kept as they are
+            const float al = r.move(mx, s2);
             l *= al;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= al;
         }
-        const float ref = m == -kInf ? 0.f : m;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, -ref));
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], r.s2, -r.ref));
             l += s[i];
         }
 #pragma unroll
@@ -449,7 +470,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-    float m = -kInf, ref = 0.f, l = 0.f;         // the sums' reference in units of log2 (ref: 0 for none), this lane's keys' sum
+    Reference row(s2);
+    float l = 0.f;                               // of this lane's keys only
     if (lo < hi) {
         loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
         loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
@@ -489,18 +511,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
 #pragma unroll
             for (int i = n * 16 / kRun; i < (n + 1) * 16 / kRun; ++i) {
                 mx = fmaxf(mx, s[kb][i]);
-                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], s2, -ref));
+                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], row.s2, -row.ref));
                 asm volatile("" : "+v"(e));          // here, not behind the branch that they might not reach
                 part[kb] += e;
                 p[kb][i / 8][i % 8] = (__bf16)e;
             }
         };
         auto settle = [&](int kb) __attribute__((always_inline)) {
-            mx = both_halves_max(mx) * s2;
-            if (__any(mx > m + 8.f)) {
-                const float mn = fmaxf(m, mx), al = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                ref = mn == -kInf ? 0.f : mn;
+            mx = both_halves_max(mx);
+            if (__any(mx * s2 > row.m + 8.f)) {
+                const float al = row.move(mx, s2);
                 l *= al;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
@@ -569,13 +589,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     l = both_halves_sum(l);
     if (a.splits > 1) {
         if (!there) return;
-        const int64_t row = token * a.Hq + head;
+        const int64_t at_row = token * a.Hq + head;
         if (lane < 32) {
-            float *st = part_stats(a, split) + row * 2;
-            st[0] = m;
+            float *st = part_stats(a, split) + at_row * 2;
+            st[0] = row.m;
             st[1] = l;
         }
-        float *to = part_sums(a, split) + row * a.D;
+        float *to = part_sums(a, split) + at_row * a.D;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -586,7 +606,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
         return;
     }
     const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;       // a NaN stays one
-    if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (there && lane < 32 && a.lse != nullptr) a.lse[(int64_t)head * a.Tq + token] = l == 0.f ? -kInf : (row.m + __builtin_amdgcn_logf(l)) * kLn2;
     // The rows go out through LDS, kLanes lanes to a row and 8 elements to a lane, so that the casts are one short loop: as
     // straight code from the registers they took more of the instruction cache than all else.
     constexpr int kLanes = DB == 2 ? 8 : 16, kPieces = 2 * kLanes;   // 16-byte pieces of a row; lane l's row keeps them at p ^ l
@@ -657,7 +677,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
     const Reader<DB> rd(lane);
     const float s2 = a.softmax_scale * kLog2e;
-    Softmax<DB> sm;
+    Softmax<DB> sm(s2);
     const int mine = wave * kTile;
     int j = lo + wave * 32;
     if (j < hi) {
@@ -687,7 +707,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_fwd_few(const Attention a)
     // the four waves' sums, joined in order
     const float l = both_halves_sum(sm.l);
     if (lane < 32) {
-        stats[wave][lane][0] = sm.m;
+        stats[wave][lane][0] = sm.r.m;
         stats[wave][lane][1] = l;
     }
     __syncthreads();
@@ -908,7 +928,6 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     s = __builtin_fmaf(q[d * 8 + 2 * i + 1], bf16_hi(x[d][i]), __builtin_fmaf(q[d * 8 + 2 * i], bf16_lo(x[d][i]), s));
-            s *= s2;
         }
         float mx = s;
 #pragma unroll
@@ -916,7 +935,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         if (lane == 0) fred[wave] = mx;
         __syncthreads();
         const float mn = fmaxf(fmaxf(m, fmaxf(fred[0], fred[1])), fmaxf(fred[2], fred[3])), ref = mn == -kInf ? 0.f : mn;
-        const float al = __builtin_amdgcn_exp2f(m - ref), p = __builtin_amdgcn_exp2f(s - ref);
+        const float al = __builtin_amdgcn_exp2f((m - ref) * s2), p = __builtin_amdgcn_exp2f((s - ref) * s2);
         m = mn;
         l = l * al + p;
 #pragma unroll
@@ -971,7 +990,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     for (int i = 0; i < kTopParts; ++i) m = fmaxf(m, pm[i]);
 #pragma unroll
     for (int i = 0; i < kTopParts; ++i) {
-        const float w = pm[i] == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm[i] - m);
+        const float w = pm[i] == -kInf ? 0.f : __builtin_amdgcn_exp2f((pm[i] - m) * s2);
         sum += w * pl[i];
         v += w * pv[i];
     }
@@ -1258,7 +1277,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
     load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, a.dout.p, there, a.D, lane >> 5);
     const float s2 = uniform_value(a.softmax_scale * kLog2e);
-    // -lse / scale and -<dout, out> of the row.  The output was rounded to bfloat16, which is off by up to 2^-8 of its terms
+    // -lse / scale, -inf where the row has no probabilities to compute again, and -<dout, out> of the row.  The output was rounded to bfloat16, which is off by up to 2^-8 of its terms
     // there; the sum of the slopes P (dP - <dout, out>) is what is missing, so that the keys' gradients get the exact one.
     float low = -kInf, delta = 0.f, slope_sum = 0.f;
     {
@@ -1272,7 +1291,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     }
     if (there) {
         const float lse = a.lse[(int64_t)head * a.Tq + token];
-        low = lse == -kInf ? -kInf : -lse / a.softmax_scale;
+        low = fabsf(lse) >= kFarLse ? -kInf : -lse / a.softmax_scale;
         if (lane < 32) a.part[((int64_t)kvh * a.Tq + sq.begin) * a.G + r] = low;
         low *= s2;
     }

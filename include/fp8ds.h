@@ -477,7 +477,8 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * are rounded to bfloat16 as operands of the matrix cores, which puts o off by up to 2^-8 of sum_j p |v| (with few rows
  * to a sequence, up to 32 of Tq * Hq / Hkv at the mean and up to 64 of few sequences, they are not rounded).  The amax is
  * that of unrounded probabilities: the rows that may hold it are computed again, the 16 largest of those within 1/64 of the
- * largest.  A NaN or an infinity in q, k or v may reach every row of its sequence, those that do not see it too.
+ * largest.  Scores may have any magnitude up to 2^127: a row whose keys are all at one lowest value weighs them alike.
+ * A NaN or an infinity in q, k or v may reach every row of its sequence, those that do not see it too.
  * workspace: fp8_attention_workspace_bytes is enough for any call of these sizes (one that splits nothing and wants no amax
  * takes none: NULL), 16-byte aligned, no initialisation; calls that overlap in time must not share it.
  */
@@ -502,7 +503,8 @@ int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads o
  *
  * out, lse: what the forward wrote.  dq, dk, dv: bfloat16, strided as q, k, v may be (no two elements in one
  * place, none in an input's), so that they can be slices of the QKV layer's output gradient; rows of no sequence are
- * not written.
+ * not written.  A row whose |lse| is 2^24 or more (-inf: it sees no key) gives no gradient: exp(s - lse) cannot be had from a
+ * float32 lse of that size.
  * The rest as fp8_attention_fwd.  p and ds are rounded to bfloat16 as operands; every sum is float32 in a
  * fixed order: the same run to run.
  */
