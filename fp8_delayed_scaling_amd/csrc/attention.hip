@@ -818,18 +818,22 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
     emit.finish(a);
 }
 
-// The amax.  Outputs made of rounded probabilities tell which rows may hold it: those within 1/64 of the largest (a rounded
-// probability is off by 2^-8 at most), kTops of them at most, one to a wave of k_attn_fwd.  These rows are computed again
-// with probabilities of 32 bits, kTopParts blocks to a row, and the last block of a row to come joins their sums in order.  The
-// sums pass between the blocks by accesses of their own to memory that all XCDs see: a fence would write a whole L2 back
-// (17 us at 4 x 2048 with fences, 13 in two launches).  10.6 us: three dependent rounds of reads, of the waves' maxima by
-// every block, of keys, of values.
+// The amax.  An output made of rounded probabilities is off by up to 2^-8 sum p |v|, so the largest of them only tells which
+// rows are likely to hold it: of each wave's rows (32 of k_attn_fwd, 4 of k_attn_join) the largest, of those within 1/64 of
+// the largest of all the kTops largest.  These are computed again with probabilities of 32 bits.  What is left is a row
+// that its own rounding put below another, of the same wave or by more than 1/64 where values cancel: the amax is off by
+// 2^-7 max(sum p |v|) at most, two roundings, and by float32 roundings alone where no two rows are that near.  (Unrounded
+// probabilities for every row, in two operands, would take 204 us for 152 at 4 x 2048, and 117 for 80 at 2 x 256 on 8192 keys.)
+// kTopParts blocks take a row, and the last of a row to come joins their sums in order.  The sums pass between the blocks by
+// accesses of their own to memory that all XCDs see: a fence would write a whole L2 back (17 us at 4 x 2048 with fences, 13
+// in two launches).  10.6 us: three dependent rounds of reads, of the waves' maxima by every block, of keys, of values.
 __device__ __forceinline__ void shared_store(float *p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ float shared_load(const float *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
     constexpr int kChunk = kThreads;                                 // keys at a time
     __shared__ uint32_t red[kWaves], value[kThreads];
+    __shared__ uint64_t red2[kWaves];
     __shared__ float fred[kWaves], prob[kChunk], q[128], acc[16][128];
     __shared__ int found[kThreads], rows[kTops], all, last;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -855,8 +859,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         if (blockIdx.x == 0 && t == 0) fold_amax_bits(a.amax, top);
         return;
     }
-    // the candidates as they are found, then the kTops largest of them, of equal ones the first in the order of the waves
-    uint32_t least = max(__float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64)), 1u);
+    // the kTops largest candidates, of equal ones the first in the order of the waves: listed as they are found and ranked, or, of
+    // more than a list holds, one by one, each the largest behind the one before
+    const uint32_t least = max(__float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64)), 1u);
     auto find = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
         if (max(max(x.x, x.y), max(x.z, x.w)) < least) return;
 #pragma unroll
@@ -866,27 +871,43 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
                 if (at < kThreads) found[at] = 4 * i + u, value[at] = x[u];
             }
     };
-    for (;;) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) find(held[i], t + i * kThreads);
+    for (int i = 0; i < kHeld; ++i) find(held[i], t + i * kThreads);
 #pragma unroll 8
-        for (int i = t + kHeld * kThreads; i < n; i += kThreads) find(tops[i], i);
-        __syncthreads();
-        if (all <= kThreads || least == top) break;                  // (the same in all threads)
-        __syncthreads();
-        if (t == 0) all = 0;
-        least += (top - least + 1) / 2;                              // too many: only the upper half
-        __syncthreads();
-    }
+    for (int i = t + kHeld * kThreads; i < n; i += kThreads) find(tops[i], i);
+    __syncthreads();
     if (all <= kThreads) {
         if (t < all) {
             int before = 0;
             for (int i = 0; i < all; ++i) before += value[i] > value[t] || (value[i] == value[t] && found[i] < found[t]);
             if (before < kTops) rows[before] = a.top_row[found[t]];
         }
-    } else if (t == 0) {                                             // all of them as large as the largest
-        for (int i = 0, n = 0; n < kTops; ++i)
-            if (a.top[i] == top) rows[n++] = a.top_row[i];
+    } else {
+        uint64_t last_one = ~UINT64_C(0);                            // its value, then the complement of its number
+        for (int r = 0; r < kTops; ++r) {
+            uint64_t best = 0;
+            auto most = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint64_t mine = (uint64_t)x[u] << 32 | (uint32_t)~(4 * i + u);
+                    best = mine < last_one && mine > best ? mine : best;
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) most(held[i], t + i * kThreads);
+#pragma unroll 8
+            for (int i = t + kHeld * kThreads; i < n; i += kThreads) most(tops[i], i);
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) {
+                const uint64_t other = __shfl_xor((unsigned long long)best, o, 64);
+                best = best > other ? best : other;
+            }
+            if (lane == 0) red2[wave] = best;
+            __syncthreads();
+            last_one = max(max(red2[0], red2[1]), max(red2[2], red2[3]));
+            if (t == 0) rows[r] = a.top_row[~(uint32_t)last_one];
+            __syncthreads();
+        }
     }
     __syncthreads();
     const int c = blockIdx.x / kTopParts, part = blockIdx.x % kTopParts;

@@ -476,8 +476,10 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * 1e-30 <= softmax_scale <= 1e30; window only with causal.  Scores, softmax and sums are float32; the probabilities
  * are rounded to bfloat16 as operands of the matrix cores, which puts o off by up to 2^-8 of sum_j p |v| (with few rows
  * to a sequence, up to 32 of Tq * Hq / Hkv at the mean and up to 64 of few sequences, they are not rounded).  The amax is
- * that of unrounded probabilities: the rows that may hold it are computed again, the 16 largest of those within 1/64 of the
- * largest.  Scores may have any magnitude up to 2^127: a row whose keys are all at one lowest value weighs them alike.
+ * that of o as computed, of which the largest rows are computed again with unrounded probabilities: of the rows that share a wave
+ * the largest, of those within 1/64 of the largest of all the 16 largest.  It is off by at most 2^-7 max(sum_j p |v|), two
+ * roundings, and by float32 roundings alone where no two rows are nearer to each other than their roundings.
+ * Scores may have any magnitude up to 2^127: a row whose keys are all at one lowest value weighs them alike.
  * A NaN or an infinity in q, k or v may reach every row of its sequence, those that do not see it too.
  * workspace: fp8_attention_workspace_bytes is enough for any call of these sizes (one that splits nothing and wants no amax
  * takes none: NULL), 16-byte aligned, no initialisation; calls that overlap in time must not share it.
