@@ -59,6 +59,9 @@ class AttentionBlock:
     def forward(self, x, offsets=None):
         T, width, H, kv, D = self.shape
         self.offsets, batch = offsets, self.batch if offsets is None else offsets.numel() - 1
+        if offsets is not None:                              # rows of no sequence are not written: an earlier batch may have been longer
+            self.a8.zero_()
+            self.dqkv.zero_()
         size = [F.fp8_attention_workspace_bytes(T, T, batch, H, kv, D), F.fp8_attention_bwd_workspace_bytes(T, T, batch, H, kv, D)]
         if self.ws is None or self.ws.numel() < max(size):
             self.ws = torch.empty(max(size), device="cuda", dtype=torch.uint8)
