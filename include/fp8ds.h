@@ -470,6 +470,9 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * [offsets[b], offsets[b + 1]) (held to [0, T) as they are read); both NULL: B sequences of equal lengths.
  * They must not fall: a falling pair is an empty sequence, and rows that several sequences then cover hold any
  * of their results or none.  Rows of no sequence are neither read nor written.
+ * A cache that grows without moving has a slot of n tokens for each sequence; its unused part is a sequence without queries:
+ * offsets_k = 0, used[0], n, n + used[1], 2 n, ..., offsets_q = 0, q[0], q[0], q[0] + q[1], ..., twice as many sequences.  The
+ * forward does not read the unused parts, the backward writes zeros as their keys' gradients.
  *
  * D % 8 == 0, 8 <= D <= 128; strides % 8 == 0; token strides >= D (one token: any) and below 2^23; data 16-byte
  * aligned; T * heads <= 2^28; the heads that share a key/value head lie within 2^30 elements.
