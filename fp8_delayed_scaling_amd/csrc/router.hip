@@ -225,7 +225,8 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const Route a) {
 
 // Up to 256 experts: a wave takes four rows, 16 lanes to a row, lane l of them the experts l, l + 16, ...  No step leaves
 // the 16 lanes, so that a choice costs a row a quarter of the wave's instructions.  32768 rows of 256 experts, 8 choices:
-// 25.5 us, with a wave to a row 35.3; of 8192 rows, whose waves take four rows and no more, 17.8 and 15.7.  More experts do
+// 25.4 us, with a wave to a row 35.2; of 8192 rows, for half of the waves, 15.6 and 15.8; of 1024 14.3 and 11.4.  The rows go
+// round the blocks: in runs of 64 to a block three blocks of four had none (8192 rows 18.7, 128 17.2 for 13.2).  More experts do
 // not fit a lane's registers: V logits, keys, sums and the next row's logits.
 template <int CTRL> __device__ __forceinline__ uint32_t max16(uint32_t v) { return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true)); }
 __device__ __forceinline__ uint32_t row_max(uint32_t v) { return max16<0x121>(max16<0x122>(max16<0x124>(max16<0x128>(v)))); }      // row_ror 8, 4, 2, 1
@@ -251,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_route_rows(const Route a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) next[v] = v * 16 + l < a.E && t < a.T ? logit<BF16>(a.logits, t * a.ld + v * 16 + l) : -kInf;
     };
-    const int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * 4;
+    const int64_t first = ((int64_t)wave * gridDim.x + blockIdx.x) * 4;      // every block has rows before one has more
     load(first + group);
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + group;
@@ -465,9 +466,9 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const Route a) {
 namespace {
 // Rows that one block takes in one turn (64 of up to 256 experts, 16 of more) it finishes by itself, in one launch; more rows
 // are spread, and joined in a second.  us with one block and with several, bfloat16: 64 rows of 64 experts, 4 choices 5.3
-// and 7.2, 128 rows 7.1 and 7.4; 64 rows of 256, 8 choices 11.9 and 15.7, 128 rows 18.7 and 16.0; 64 rows of 1024 (four
-// turns) 32.5 and 16.6.  256 blocks, one to a CU, at most: 32768 rows of 256 experts 25.5, with 128 blocks 39, with 512
-// 30.9 (the second block of a CU waits for the first's LDS); 8192 rows of 64 9.4, 9.8 and 11.7.
+// and 8.1, 128 rows 7.4 and 6.6 .. 8.0; 64 rows of 256, 8 choices 11.8 and 15.1, 128 rows 18.8 and 13.2; 64 rows of 1024 (four
+// turns) 25.1 and 14.4.  256 blocks, one to a CU, at most: 32768 rows of 256 experts 25.4, with 128 blocks 39.2, with 512
+// 31.0 (the second block of a CU waits for the first's LDS); 8192 rows of 64 8.9, 10.4 and 13.4.
 int64_t route_blocks(int64_t T, int64_t E) {
     if (T <= (E <= 256 ? 4 : 1) * kWaves) return 1;
     const int64_t n = (T + kWaves - 1) / kWaves;
