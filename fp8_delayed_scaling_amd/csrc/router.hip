@@ -449,7 +449,7 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const Route a) {
         }
         const float all_of = s1 + (a.normalise ? 0.f : s2), each = a.normalise ? s2 : 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) d[v] = p[v] * inv * (c[v] - all_of);
+        for (int v = 0; v < V; ++v) d[v] = dead ? 0.f : p[v] * inv * (c[v] - all_of);
         if (a.dweights != nullptr && !dead)
             for (int j = 0; j < a.top; ++j) {
                 const int e = uniform(a.experts[t * a.top + j]);

@@ -539,7 +539,7 @@ int fp8_attention_bwd(fp8ds_heads dout, fp8ds_heads q, fp8ds_heads k, fp8ds_head
  *
  * fp8_moe_route_bwd -- dlogits (type of logits, row stride ld_d) from dweights [T, top] and *dloss, either may be NULL:
  * counts are constants, weights and prob_sum are functions of the logits.  experts, weights, lse, counts: what the
- * forward wrote; a choice outside [0, E) has no gradient; padding rows get zeros.  Rows masked by a
+ * forward wrote; a choice outside [0, E) has no gradient; padding rows get zeros, whatever the gradients are.  Rows masked by a
  * lowest value instead of -inf are rows like any other: every expert has the same share of them, in both directions.
  */
 size_t fp8_moe_route_workspace_bytes(int64_t T, int64_t E);

@@ -1,5 +1,5 @@
 """The router's gradient where logits are far from zero: rows and experts masked by a lowest value instead of -inf, logits that
-float32's lse holds without their digits behind the point."""
+float32's lse holds without their digits behind the point; and padding under a gradient that is not finite."""
 import math
 
 import pytest
@@ -48,3 +48,15 @@ def test_logits_of_every_magnitude(power, sign):
     x = sign * 2.0 ** power * (1 + step)
     for normalise in (False, True):
         check(x, 4, normalise)
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_padding_under_a_gradient_that_is_not_finite(bad, bf16):
+    """Padding rows get zeros whatever the gradients are."""
+    x = make(100, 40, 1, bf16, padded=0.0)
+    x[[0, 7, 99]] = -math.inf
+    f = run(x, 4)
+    dw = torch.full((100, 4), bad, device=DEV)
+    got = backward(x, f, dw, torch.full((1,), bad, device=DEV), True)
+    assert bool((got[[0, 7, 99]] == 0).all()) and bool(got[1].isnan().any())
