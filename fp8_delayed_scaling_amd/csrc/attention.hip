@@ -7,8 +7,9 @@
 //   P = exp2((S - lse / scale) scale log2(e)),  dS = P (dO V^T - <dO, O>)
 //   dQ = scale dS K (k_attn_dq, by query rows);  dV = P^T dO,  dK = scale dS^T Q (k_attn_dkv, by keys)
 // in two kernels, so that every sum has one owner and a fixed order; S and dP are computed in both (7 products, not 5).
-// P and dS are rounded to bfloat16 as operands: the gradients are off by 0.0024 .. 0.0026 of their norm, 0.0017 of which is their
-// own rounding to bfloat16 and as much that of the operands.  In two parts each they would take ten products for seven.
+// P and dS are rounded to bfloat16 as operands: the gradients are off by 0.0023 .. 0.0025 of their norm, 0.0017 of which is their
+// own rounding to bfloat16 and as much that of the operands.  In two parts each they take ten products for seven: 4 x 2048
+// tokens 725 us for 467, 1 x 8192 2630 for 1660.
 //
 // Products are 32 x 32 x 16 matrix instructions with the scores transposed: a lane owns one query row (in k_attn_dkv one
 // key) and 16 of 32 scores, so a row's maximum and sum take one exchange between the wave's halves, and the 16 values,
@@ -423,7 +424,8 @@ __device__ __forceinline__ float *part_stats(const Attention &a, int split) {
 // A block: 128 query rows of one key/value head, 32 to each wave; all waves read the same 64 keys a step, from two turns of
 // LDS (64 KB, two blocks to a CU, so that one block's barrier and exponentials lie beside the other's products).  The
 // probabilities are rounded to bfloat16 (off by up to 2^-8 of each term, as the output itself): the matrix instruction's
-// type; with float32 ones in three parts the second product takes three times as long.  4 x 2048 tokens, 32 heads, 8 of
+// type.  The output is off by 0.0023 of its norm, in two parts, with twice the products for the sums, by 0.0017, its own rounding:
+// 204 us for 152 at 4 x 2048 without an amax, 729 for 525 at 1 x 8192.  4 x 2048 tokens, 32 heads, 8 of
 // keys, of 128, causal: 168 .. 180 us, 0.8 PFLOP/s (half of a tile at the diagonal counts for nothing, and a block's
 // start and end take 4 us of 45); without a mask 280 us, 0.98; 1 x 16384 causal 1.07.  What a head size that fills no
 // block of 32 costs: 72 is computed as 96 (1 x 2048 41 us; as 128 46, and 2 x 4096 of 96 237 and 263 us).
@@ -1276,13 +1278,23 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
 }
 
 // A block: 128 query rows, 32 to each wave, over the keys that they see, as the forward.  It also leaves what the keys'
-// gradients need of each row in the workspace, in the order [key/value head, token, head of the group].  4 x 2048 tokens, 32
+// gradients need of each row in the workspace, in the order [key/value head, token, head of the group].
+// <dout, out> of the rounded output is off by e, up to 2^-8 of its terms.  The slopes P (dP - <dout, out>) of a row then have the
+// sum -e instead of 0: that goes into what the keys' gradients take, and dQ lacks -e sum P k.  Heads of up to 96 keep sum P k
+// beside dQ, a seventh product that shares dS's operands: 4 x 2048 of 64 292 us for 272 with both kernels, 1 x 8192 of 96 (16
+// heads, 4 of keys; three registers spill) 972 for 907.  Above 96 there are no registers for it: blocks of up to 256 keys, where e
+// counts most, go over their keys twice, for the sum first (8 x 256 of 128 65 us for 56; window 128 at 4 x 2048 184 for 168), and
+// others leave e in dQ.  Error of all gradients against 64 bits, their own rounding being 0.0017: with e 0.0025 (2048
+// keys) .. 0.0028 (window 5), without it 0.0023 .. 0.0024.
+//  4 x 2048 tokens, 32
 // heads, 8 of keys, of 128, causal: 215 .. 249 us, 0.8 .. 0.95 PFLOP/s of its three products; 1 x 8192 750 .. 791 us, 1.0; matrix
 // units in use for 64 % of the cycles.
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;
-    constexpr int kTile = kKeys * S::pitch, kRun = 2 * DB, kAhead = 3;
+    constexpr int kTile = kKeys * S::pitch, kRun = 2 * DB, kAhead = DB == 3 ? 2 : 3;
+    constexpr bool kWithKeys = DB <= 3;          // sum P k is kept
+    constexpr int kTwice = 256;                  // keys of a block that goes over them twice instead
     __shared__ __align__(1024) uint8_t k0[kTile], k1[kTile], v0[kTile], v1[kTile];      // as in the forward
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.Hkv;
@@ -1298,8 +1310,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     load_query<DB>(qf, a.q.p + token * a.q.ts + head * a.q.hs, a.q.p, there, a.D, lane >> 5);
     load_query<DB>(df, a.dout.p + token * a.dout.ts + head * a.dout.hs, a.dout.p, there, a.D, lane >> 5);
     const float s2 = uniform_value(a.softmax_scale * kLog2e);
-    // -lse / scale, -inf where the row has no probabilities to compute again, and -<dout, out> of the row.  The output was rounded to bfloat16, which is off by up to 2^-8 of its terms
-    // there; the sum of the slopes P (dP - <dout, out>) is what is missing, so that the keys' gradients get the exact one.
+    // -lse / scale, -inf where the row has no probabilities to compute again, and -<dout, out> of the row
     float low = -kInf, delta = 0.f, slope_sum = 0.f;
     {
         bf16x8 of[S::ks];
@@ -1322,29 +1333,70 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     const RowLoads<DB, kKeys, kWaves> loads_k(lane, wave, a.D, a.k.ts), loads_v(lane, wave, a.D, a.v.ts);
     const uint16_t *kp = a.k.p + sk.begin * a.k.ts + kvh * a.k.hs, *vp = a.v.p + sk.begin * a.v.ts + kvh * a.v.hs;
     Walker<DB> rd(lane);
-    f32x16 dq[DB];
+    auto load = [&](int j, uint8_t *tk, uint8_t *tv) __attribute__((always_inline)) {
+        if (j >= hi) return;
+        loads_k(kp + (int64_t)j * a.k.ts, a.k.ts, sk.len - j, tk);
+        loads_v(vp + (int64_t)j * a.v.ts, a.v.ts, sk.len - j, tv);
+    };
+    auto hide = [&](f32x16 &s, int key0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int key = key0 + 4 * (lane >> 5) + (i >> 2) * 8 + (i & 3);
+            s[i] = key >= see.lo && key < see.hi ? s[i] : -kInf;
+        }
+    };
+    load(lo, k0, v0);
+    if (!kWithKeys && hi - lo <= kTwice) {       // the sum of the slopes first
+        auto sums = [&](int j, const uint8_t *tk, const uint8_t *tv, uint8_t *next_k, uint8_t *next_v) __attribute__((always_inline)) {
+            FP8DS_WAIT_ALL();
+            FP8DS_BARRIER();
+            load(j + kKeys, next_k, next_v);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                f32x16 s, p;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = 0.f, p[i] = delta;
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) {
+                    s = mfma(read_row(tk + kb * 32 * S::pitch + rd.row(k)), qf[k], s);
+                    p = mfma(read_row(tv + kb * 32 * S::pitch + rd.row(k)), df[k], p);
+                }
+                hide(s, j + kb * 32);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) slope_sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], s2, low)) * p[i];
+            }
+        };
+        for (int j = lo; j < hi; j += 2 * kKeys) {
+            sums(j, k0, v0, k1, v1);
+            if (j + kKeys >= hi) break;
+            sums(j + kKeys, k1, v1, k0, v0);
+        }
+        delta -= both_halves_sum(slope_sum);
+        slope_sum = 0.f;
+        FP8DS_WAIT_ALL();
+        FP8DS_BARRIER();                                             // every wave has read the tiles
+        load(lo, k0, v0);
+    }
+    f32x16 dq[DB], pk[kWithKeys ? DB : 1];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[d][i] = 0.f;
-    if (lo < hi) {
-        loads_k(kp + (int64_t)lo * a.k.ts, a.k.ts, sk.len - lo, k0);
-        loads_v(vp + (int64_t)lo * a.v.ts, a.v.ts, sk.len - lo, v0);
-    }
+#pragma unroll
+    for (int d = 0; d < (kWithKeys ? DB : 1); ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[d][i] = 0.f;
     auto turn = [&](int j, const uint8_t *tk, const uint8_t *tv, uint8_t *next_k, uint8_t *next_v) __attribute__((always_inline)) {
         FP8DS_WAIT_ALL();
         FP8DS_BARRIER();
         const int next = j + kKeys;
-        if (next < hi) {
-            loads_k(kp + (int64_t)next * a.k.ts, a.k.ts, sk.len - next, next_k);
-            loads_v(vp + (int64_t)next * a.v.ts, a.v.ts, sk.len - next, next_v);
-        }
+        load(next, next_k, next_v);
         if (j >= end.hi || next <= first.lo) return;
         const bool masked = next > first.hi || j < end.lo;
         // Six runs of products, kRun each: scores and dP of 32 keys, of the next 32, and the sums over either.  As in the keys'
         // gradients: operands kAhead products ahead, the exponentials beside dP, the slopes beside the run after it.
         f32x16 s[2], p[2];
-        bf16x8 f[kAhead], sf[2][2];
+        bf16x8 f[kAhead], sf[2][2], pf[2][2];
         auto read = [&](int n) __attribute__((always_inline)) {
             const int run = n / kRun, i = n % kRun;
             if (run < 4) return read_row((run & 1 ? tv : tk) + (run >> 1) * 32 * S::pitch + rd.row(i));
@@ -1364,6 +1416,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
                 }
             }
             if (n == kRun - 1) sf[kb][0] = pack8(p[kb], 0), sf[kb][1] = pack8(p[kb], 1);
+            if (kWithKeys && n == kRun - 1) pf[kb][0] = pack8(s[kb], 0), pf[kb][1] = pack8(s[kb], 1);
         };
         rd.fresh();
         __builtin_amdgcn_sched_barrier(0);
@@ -1385,14 +1438,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
                 if (kb == 1) slopes(0, n);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (masked) {
-                const int h4 = j + kb * 32 + 4 * (lane >> 5);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = h4 + (i >> 2) * 8 + (i & 3);
-                    s[kb][i] = key >= see.lo && key < see.hi ? s[kb][i] : -kInf;
-                }
-            }
+            if (masked) hide(s[kb], j + kb * 32);
             rd.fresh();
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1408,7 +1454,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
         for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int n = 0; n < kRun; ++n) {
-                dq[n % DB] = mfma(step((4 + kb) * kRun + n), sf[kb][n / DB], dq[n % DB]);
+                const bf16x8 now = step((4 + kb) * kRun + n);
+                dq[n % DB] = mfma(now, sf[kb][n / DB], dq[n % DB]);
+                if constexpr (kWithKeys) pk[n % DB] = mfma(now, pf[kb][n / DB], pk[n % DB]);
                 if (kb == 0) slopes(1, n);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -1422,6 +1470,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     }
     slope_sum = both_halves_sum(slope_sum);
     if (there && lane < 32) a.part[(int64_t)a.Tq * a.Hq + ((int64_t)kvh * a.Tq + sq.begin) * a.G + r] = delta - slope_sum;
+    if constexpr (kWithKeys) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dq[d][i] = __builtin_fmaf(-slope_sum, pk[d][i], dq[d][i]);
+    }
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll

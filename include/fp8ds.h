@@ -510,6 +510,8 @@ int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads o
  * place, none in an input's), so that they can be slices of the QKV layer's output gradient; rows of no sequence are
  * not written.  A row whose |lse| is 2^24 or more (-inf: it sees no key) gives no gradient: exp(s - lse) cannot be had from a
  * float32 lse of that size.
+ * <dout, out> counts as sum_j p <dout, v>, which it is before out's rounding; in dq of heads above 96 over more than 256 keys
+ * that rounding counts.  So out and lse have to be those of this call's keys: sum_j p = 1.
  * The rest as fp8_attention_fwd.  p and ds are rounded to bfloat16 as operands; every sum is float32 in a
  * fixed order: the same run to run.
  */
