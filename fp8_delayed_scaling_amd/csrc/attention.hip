@@ -18,8 +18,9 @@
 // numbered token by token, the heads of a key/value head's group side by side, so that a tile of keys serves the whole
 // group, and the keys' gradients sum over the group inside one block.
 //
-// What bounds them: the matrix units, and the power that they draw.  A loop of these instructions from registers, with
-// random bits, sustains 1.75 PFLOP/s on this card, the forward of 1 x 8192 tokens of 32 heads (8 of keys) of 128 1.03 (532
+// What bounds long ones: the matrix units, in use for 59 % (k_attn_dkv) and 64 % (k_attn_dq) of the cycles at 1 x 8192, and the power
+// that they draw; shorter ones, 4 x 2048 with 52, 51 and 40 % (k_attn_fwd), the blocks' starts and ends, tiles that are half masked, and
+// the waits inside a step.  A loop of these instructions from registers, with random bits, sustains 1.75 PFLOP/s on this card, the forward of 1 x 8192 tokens of 32 heads (8 of keys) of 128 1.03 (532
 // us causal), its backward 0.82 of five products, 1.15 of the seven (1684 us); with zeros as inputs, and all else the same,
 // 394 and 1232 us: the clock falls from 2.4 to 1.6 .. 1.95 GHz under load.  No single part of a step bounds it: with the loads
 // and barriers left out the forward took 9 % less, without the exponentials 8 %, without the reads of LDS 9 %.
@@ -422,13 +423,15 @@ __device__ __forceinline__ float *part_stats(const Attention &a, int split) {
 }  // namespace
 
 // A block: 128 query rows of one key/value head, 32 to each wave; all waves read the same 64 keys a step, from two turns of
-// LDS (64 KB, two blocks to a CU, so that one block's barrier and exponentials lie beside the other's products).  The
-// probabilities are rounded to bfloat16 (off by up to 2^-8 of each term, as the output itself): the matrix instruction's
-// type.  The output is off by 0.0023 of its norm, in two parts, with twice the products for the sums, by 0.0017, its own rounding:
-// 204 us for 152 at 4 x 2048 without an amax, 729 for 525 at 1 x 8192.  4 x 2048 tokens, 32 heads, 8 of
-// keys, of 128, causal: 168 .. 180 us, 0.8 PFLOP/s (half of a tile at the diagonal counts for nothing, and a block's
-// start and end take 4 us of 45); without a mask 280 us, 0.98; 1 x 16384 causal 1.07.  What a head size that fills no
-// block of 32 costs: 72 is computed as 96 (1 x 2048 41 us; as 128 46, and 2 x 4096 of 96 237 and 263 us).
+// LDS (64 KB, two blocks to a CU, so that one block's barrier and exponentials lie beside the other's products).  A wave none
+// of whose rows sees a step computes it all the same: a branch around it would have the sums copied.  The probabilities are
+// rounded to bfloat16 (off by up to 2^-8 of each term, as the output itself): the matrix instruction's type.  The output is
+// off by 0.0023 of its norm, in two parts, with twice the products for the sums, by 0.0017, its own rounding: 204 us for 152
+// at 4 x 2048 without an amax, 729 for 525 at 1 x 8192.
+// 4 x 2048 tokens, 32 heads, 8 of keys, of 128, causal: 168 .. 180 us, 0.8 PFLOP/s (half of a tile at the diagonal counts for
+// nothing, and a block's start and end take 4 us of 45); without a mask 280 us, 0.98; 1 x 16384 causal 1.07; 1 x 8192 with a
+// window of 1024 and the amax 175.  What a head size that fills no block of 32 costs: 72 is computed as 96 (1 x 2048 41 us; as
+// 128 46, and 2 x 4096 of 96 237 and 263 us), sizes up to 56 as 64.
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(const Attention a) {
     using S = Shape<DB>;
@@ -828,7 +831,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const Attention a) {
 // probabilities for every row, in two operands, would take 204 us for 152 at 4 x 2048, and 117 for 80 at 2 x 256 on 8192 keys.)
 // kTopParts blocks take a row, and the last of a row to come joins their sums in order.  The sums pass between the blocks by
 // accesses of their own to memory that all XCDs see: a fence would write a whole L2 back (17 us at 4 x 2048 with fences, 13
-// in two launches).  10.6 us: three dependent rounds of reads, of the waves' maxima by every block, of keys, of values.
+// in two launches).  10.6 .. 11.7 us: three dependent rounds of reads, of the waves' maxima by every block, of keys, of values.
 __device__ __forceinline__ void shared_store(float *p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ float shared_load(const float *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
@@ -862,7 +865,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         return;
     }
     // the kTops largest candidates, of equal ones the first in the order of the waves: listed as they are found and ranked, or, of
-    // more than a list holds, one by one, each the largest behind the one before
+    // more than a list holds, one by one, each the largest behind the one before (in little code: unrolled it made every call
+    // 1.2 us longer, which fetches it past)
     const uint32_t least = max(__float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64)), 1u);
     auto find = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
         if (max(max(x.x, x.y), max(x.z, x.w)) < least) return;
@@ -895,11 +899,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
                     best = mine < last_one && mine > best ? mine : best;
                 }
             };
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) most(held[i], t + i * kThreads);
-#pragma unroll 8
-            for (int i = t + kHeld * kThreads; i < n; i += kThreads) most(tops[i], i);
-#pragma unroll
+#pragma unroll 1
+            for (int i = t; i < n; i += kThreads) most(tops[i], i);
+#pragma unroll 1
             for (int o = 32; o >= 1; o >>= 1) {
                 const uint64_t other = __shfl_xor((unsigned long long)best, o, 64);
                 best = best > other ? best : other;
@@ -1025,7 +1027,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
 // Rows of the group's heads, 64 at a time, for 4 waves: row r is token r / G, head r % G of the group.  A lane's loads of a
 // tile lie `turn` = 16 or 32 rows apart, its tiles 128 (two sets of waves).  EVEN: G divides `turn`, so that a lane keeps
 // its head and its offset, and only the bases move; otherwise the rows are walked, not divided.  (1 x 4096 tokens, 32 heads, 8
-// of keys, of 128: backward 559 us, walked 650; heads of 64: 336 and 343.)
+// of keys, of 128: backward 559 us, walked 650: the walk's instructions at each load, and k_attn_dkv spills; heads of 64, where
+// it does not: 336 and 343.)
 template <int DB, bool EVEN> struct GroupLoads {
     using S = Shape<DB>;
     static constexpr int turn = S::rows_a_load * kWaves, n = kStepRows / turn;       // loads of a wave for one tile
@@ -1084,7 +1087,8 @@ template <int DB, bool EVEN> struct GroupLoads {
 // turns at the steps of 64 rows, 32 keys to each wave of a set; the second set's sums are added to the first's at the end.  A
 // wave's K and V stay in registers, its dK and dV in accumulators: with heads of 128 that is 192 of the 256 registers that
 // two waves a SIMD leave to each, so that what else a step keeps is counted (addresses by exclusive or, operands one or two
-// products ahead; a spilled register's reload waits for the loads in flight as well: 400 us with spills, 331 without).
+// products ahead; a spilled register's reload waits for the loads in flight as well: 400 us with spills, 331 without).  Above
+// heads of 96 the walked rows of GroupLoads still spill four (20 bytes): they take two registers more.
 // 4 x 2048 tokens, 32 heads, 8 of keys, of 128, causal: 272 .. 323 us, 0.85 .. 1.0 PFLOP/s of its four products; 1 x 8192
 // 1103 us, 1.0.  The matrix units are in use for 59 % of the cycles at the clock that the power leaves.
 template <int DB, bool EVEN>
@@ -1504,12 +1508,16 @@ struct Plan {
 // Few query rows to a sequence (32 at the mean: one block of 32): the waves share the keys.  8 key heads, 4 rows to each of 16
 // sequences of 4096 keys: 46.5 us and 48 with blocks of 128 rows, 32 rows to each of 4 of 8192 keys 29.7 and 32.2.  Up to 64
 // rows, two blocks that read the same keys, as long as these blocks are one round (64 rows to each of 16 of 4096 keys 50
-// and 54, to one of 8192 19 and 21.5, to one of 2882 15.6 and 19.5; to each of 64 of 1024, four rounds, 88 and 49; 128 rows to each of 16 53 and 39).
-// Fewer blocks than the GPU
-// holds at a time (one block of few rows to a CU, two of the others): the keys are split, into as many parts as bring the
-// blocks nearest to that.  16 sequences of up to 4096 keys, 8 key heads, 144 blocks: 44.4 us whole, 37.7 in two parts, 40.5
-// in three, 39.9 in four, 49 in eight.  Parts no shorter than 512 keys of blocks of 128 rows (one sequence of 2048 keys, 256
-// tokens: 28 us, with 256 keys 31.6, with 1024 30.6), of 256 of the others.
+// and 54, to one of 8192 19 and 21.5, to one of 2882 15.6 and 19.5; to each of 64 of 1024, four rounds, 88 and 49; 128 rows to
+// each of 16 53 and 39).
+// Fewer blocks than the GPU holds at a time (one block of few rows to a CU, two of the others): the keys are split, into as
+// many parts as bring the blocks nearest to that.  16 sequences of up to 4096 keys, 8 key heads, 144 blocks: 44.4 us whole,
+// 37.7 in two parts, 40.5 in three, 39.9 in four, 49 in eight, each over the same cache time after time, of which part stays
+// on the chip (over others in between 46 in two parts).  Parts no shorter than 512 keys of blocks of 128 rows (one sequence of
+// 2048 keys, 256 tokens: 28 us, with 256 keys 31.6, with 1024 30.6), of 256 of the others: of the keys that there are at the
+// mean.  What a window leaves of them is not counted, so its parts are shorter and some empty (one token on 8192 keys, window
+// 1024: 32 parts of which 8 have keys, 18.5 us), nor that one sequence may be longer than the others.  The places are those
+// of heads of 128, as are nearly all figures; of 64 a CU holds three blocks of 128 rows by registers, two of few rows by LDS.
 Plan fwd_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hkv, int64_t G, bool ragged) {
     Plan p;
     p.few = Tq * G <= kFewRows * B || (Tq * G <= 2 * kFewRows * B && most_tiles(Tq, B, G, kFewRows, ragged) * Hkv <= kCUs);
