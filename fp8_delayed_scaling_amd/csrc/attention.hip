@@ -18,12 +18,13 @@
 // numbered token by token, the heads of a key/value head's group side by side, so that a tile of keys serves the whole
 // group, and the keys' gradients sum over the group inside one block.
 //
-// What bounds long ones: the matrix units, in use for 59 % (k_attn_dkv) and 64 % (k_attn_dq) of the cycles at 1 x 8192, and the power
-// that they draw; shorter ones, 4 x 2048 with 52, 51 and 40 % (k_attn_fwd), the blocks' starts and ends, tiles that are half masked, and
-// the waits inside a step.  A loop of these instructions from registers, with random bits, sustains 1.75 PFLOP/s on this card, the forward of 1 x 8192 tokens of 32 heads (8 of keys) of 128 1.03 (532
-// us causal), its backward 0.82 of five products, 1.15 of the seven (1684 us); with zeros as inputs, and all else the same,
-// 394 and 1232 us: the clock falls from 2.4 to 1.6 .. 1.95 GHz under load.  No single part of a step bounds it: with the loads
-// and barriers left out the forward took 9 % less, without the exponentials 8 %, without the reads of LDS 9 %.
+// What bounds long ones: the matrix units, in use for 59 % (k_attn_dkv) and 64 % (k_attn_dq) of the cycles at 1 x 8192, and
+// the power that they draw; shorter ones, 4 x 2048 with 52, 51 and 40 % (k_attn_fwd), the blocks' starts and ends, tiles that
+// are half masked, and the waits inside a step.  A loop of these instructions from registers, with random bits, sustains
+// 1.75 PFLOP/s on this card, the forward of 1 x 8192 tokens of 32 heads (8 of keys) of 128 1.03 (532 us causal), its backward
+// 0.82 of five products, 1.15 of the seven (1684 us); with zeros as inputs, and all else the same, 394 and 1232 us: the
+// clock falls from 2.4 to 1.6 .. 1.95 GHz under load.  No single part of a step bounds it: with the loads and barriers left
+// out the forward took 9 % less, without the exponentials 8 %, without the reads of LDS 9 %.
 #include <climits>
 
 #include "../../include/fp8ds.h"
@@ -865,8 +866,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_amax(const Attention a) {
         return;
     }
     // the kTops largest candidates, of equal ones the first in the order of the waves: listed as they are found and ranked, or, of
-    // more than a list holds, one by one, each the largest behind the one before (in little code: unrolled it made every call
-    // 1.2 us longer, which fetches it past)
+    // more than a list holds, one by one, each the largest behind the one before (not unrolled: the longer code between what
+    // runs before and after it made calls that never take it 1.2 us slower)
     const uint32_t least = max(__float_as_uint(__uint_as_float(top) * (1.f - 1.f / 64)), 1u);
     auto find = [&](const u32x4 &x, int i) __attribute__((always_inline)) {
         if (max(max(x.x, x.y), max(x.z, x.w)) < least) return;
@@ -1283,16 +1284,15 @@ __global__ __launch_bounds__(2 * kThreads, 2) void k_attn_dkv(const Attention a)
 
 // A block: 128 query rows, 32 to each wave, over the keys that they see, as the forward.  It also leaves what the keys'
 // gradients need of each row in the workspace, in the order [key/value head, token, head of the group].
-// <dout, out> of the rounded output is off by e, up to 2^-8 of its terms.  The slopes P (dP - <dout, out>) of a row then have the
-// sum -e instead of 0: that goes into what the keys' gradients take, and dQ lacks -e sum P k.  Heads of up to 96 keep sum P k
-// beside dQ, a seventh product that shares dS's operands: 4 x 2048 of 64 292 us for 272 with both kernels, 1 x 8192 of 96 (16
-// heads, 4 of keys; three registers spill) 972 for 907.  Above 96 there are no registers for it: blocks of up to 256 keys, where e
-// counts most, go over their keys twice, for the sum first (8 x 256 of 128 65 us for 56; window 128 at 4 x 2048 184 for 168), and
-// others leave e in dQ.  Error of all gradients against 64 bits, their own rounding being 0.0017: with e 0.0025 (2048
-// keys) .. 0.0028 (window 5), without it 0.0023 .. 0.0024.
-//  4 x 2048 tokens, 32
-// heads, 8 of keys, of 128, causal: 215 .. 249 us, 0.8 .. 0.95 PFLOP/s of its three products; 1 x 8192 750 .. 791 us, 1.0; matrix
-// units in use for 64 % of the cycles.
+// <dout, out> of the rounded output is off by e, up to 2^-8 of its terms.  The slopes P (dP - <dout, out>) of a row then have
+// the sum -e instead of 0: that goes into what the keys' gradients take, and dQ lacks -e sum P k.  Heads of up to 96 keep
+// sum P k beside dQ, one more product of dQ's operands: 4 x 2048 of 64 292 us for 272 with both kernels, 1 x 8192 of 96 (16 heads,
+// 4 of keys; two registers spill, nine where operands are read three products ahead, in the same time) 960 for 904.
+// Above 96 there are no registers for it: blocks of up to 256 keys, where e counts most, go over their keys twice, for the
+// sum first (8 x 256 of 128 65 us for 56; window 128 at 4 x 2048 186 for 168), others leave e in dQ.  Error of all gradients
+// against 64 bits, their own rounding being 0.0017: with e 0.0025 (2048 keys) .. 0.0028 (window 5), without it 0.0023 .. 0.0024.
+// 4 x 2048 tokens, 32 heads, 8 of keys, of 128, causal: 215 .. 251 us, 0.8 .. 0.95 PFLOP/s of its three products; 1 x 8192
+// 750 .. 791 us, 1.0.
 template <int DB>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(const Attention a) {
     using S = Shape<DB>;

@@ -466,7 +466,7 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * q, out: Tq tokens of Hq heads of D bfloat16 elements, k, v: Tk tokens of Hkv heads (Hq % Hkv == 0), each
  * with strides of its own: slices of the QKV layer's output, head-major caches, heads that share one
  * (head stride 0 for inputs).  lse: [Hq, Tq] float32 or NULL.  out8: [Tq, Hq * D] or NULL, out.data may be
- * NULL with it.  offsets_q, offsets_k: [B + 1] int32 each on the device, sequence b's tokens are
+ * NULL with it; none of them may lie in an input's memory.  offsets_q, offsets_k: [B + 1] int32 each on the device, sequence b's tokens are
  * [offsets[b], offsets[b + 1]) (held to [0, T) as they are read); both NULL: B sequences of equal lengths.
  * They must not fall: a falling pair is an empty sequence, and rows that several sequences then cover hold any
  * of their results or none.  Rows of no sequence are neither read nor written.
@@ -508,8 +508,8 @@ int fp8_attention_fwd(fp8ds_heads q, fp8ds_heads k, fp8ds_heads v, fp8ds_heads o
  *
  * out, lse: what the forward wrote.  dq, dk, dv: bfloat16, strided as q, k, v may be (no two elements in one
  * place, none in an input's), so that they can be slices of the QKV layer's output gradient; rows of no sequence are
- * not written.  A row whose |lse| is 2^24 or more (-inf: it sees no key) gives no gradient: exp(s - lse) cannot be had from a
- * float32 lse of that size.
+ * not written.  p is off by up to 2^-22 |lse| of itself for lse's float32; a row whose |lse| is 2^24 or more (-inf: it sees no
+ * key) gives no gradient, as no digit of p is left.
  * <dout, out> counts as sum_j p <dout, v>, which it is before out's rounding; in dq of heads above 96 over more than 256 keys
  * that rounding counts.  So out and lse have to be those of this call's keys: sum_j p = 1.
  * The rest as fp8_attention_fwd.  p and ds are rounded to bfloat16 as operands; every sum is float32 in a
