@@ -466,8 +466,9 @@ int fp8_grouped_wgrad(const uint8_t *At, int fa, const float *a_scale_inv, int64
  * q, out: Tq tokens of Hq heads of D bfloat16 elements, k, v: Tk tokens of Hkv heads (Hq % Hkv == 0), each
  * with strides of its own: slices of the QKV layer's output, head-major caches, heads that share one
  * (head stride 0 for inputs).  lse: [Hq, Tq] float32 or NULL.  out8: [Tq, Hq * D] or NULL, out.data may be
- * NULL with it; none of them may lie in an input's memory.  offsets_q, offsets_k: [B + 1] int32 each on the device, sequence b's tokens are
- * [offsets[b], offsets[b + 1]) (held to [0, T) as they are read); both NULL: B sequences of equal lengths.
+ * NULL with it; no output may lie in an input's memory.  offsets_q, offsets_k: [B + 1] int32 each on the device,
+ * sequence b's tokens are [offsets[b], offsets[b + 1]) (held to [0, T) as they are read); both NULL: B sequences
+ * of equal lengths.
  * They must not fall: a falling pair is an empty sequence, and rows that several sequences then cover hold any
  * of their results or none.  Rows of no sequence are neither read nor written.
  * A cache that grows without moving has a slot of n tokens for each sequence; its unused part is a sequence without queries:
